@@ -30,6 +30,9 @@ __all__ = [
     "bnbx_gemm_nf4_workspace_bytes", "bnbx_gemm_nf4", "bnbx_gemm_nf4_dx", "bnbx_gemm_nf4_lora",
     "bnbx_lora_down", "bnbx_probe_stream_read", "BNBX_PROBE_SINK_WORDS", "EXPORTED_SYMBOLS", "BNBX_QUANT_NF4", "BNBX_QUANT_FP4",
     "BNBX_DTYPE_BF16", "BNBX_DTYPE_F16", "BNBX_DQ_NONE", "BNBX_DQ_LINEAR", "BNBX_DQ_DYNAMIC",
+    "rows_library_path", "rows_lib", "ROWS_EXPORTED_SYMBOLS", "BNBX_ROWS_MAX_GROUPS",
+    "RowGroupsDesc", "bnbx_group_rows_workspace_bytes", "bnbx_group_rows",
+    "bnbx_gemm_nf4_experts",
 ]
 
 BNBX_OK = 0
@@ -63,6 +66,12 @@ EXPORTED_SYMBOLS = (
     "bnbx_probe_stream_read",          # include/bnbx_probe.h (measurement aid)
 )
 BNBX_PROBE_SINK_WORDS = 1024
+
+# libbnbx_rows.so (include/bnbx_rows.h)
+BNBX_ROWS_MAX_GROUPS = 1024
+ROWS_EXPORTED_SYMBOLS = (
+    "bnbx_group_rows_workspace_bytes", "bnbx_group_rows", "bnbx_gemm_nf4_experts",
+)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -117,6 +126,17 @@ class GemvItem(ctypes.Structure):
         ("N", ctypes.c_int32),
         ("y", ctypes.c_void_p),
         ("ldy", ctypes.c_int64),
+    ]
+
+
+class RowGroupsDesc(ctypes.Structure):
+    """bnbx_row_groups: a plan of grouped rows (device pointers)."""
+
+    _fields_ = [
+        ("offsets", ctypes.c_void_p),
+        ("order", ctypes.c_void_p),
+        ("groups", ctypes.c_int32),
+        ("rows", ctypes.c_int32),
     ]
 
 
@@ -180,6 +200,41 @@ def lib() -> ctypes.CDLL:
     L.bnbx_probe_stream_read.argtypes = [vp, sz, vp, sz, vp, vp]
     L.bnbx_probe_stream_read.restype = i32
     _lib = L
+    return L
+
+
+_rows_lib = None
+
+
+def rows_library_path() -> str:
+    return os.path.join(_HERE, "libbnbx_rows.so")
+
+
+def rows_lib() -> ctypes.CDLL:
+    """Load libbnbx_rows.so, the row-grouped operators (built in-tree by
+    dequant_gemm_nf4_amd.build)."""
+    global _rows_lib
+    if _rows_lib is not None:
+        return _rows_lib
+    path = rows_library_path()
+    if not os.path.exists(path):
+        raise BnbxLibraryMissing(
+            f"{path} is not built; run `python -m dequant_gemm_nf4_amd.build` (no fallback exists)")
+    try:
+        import torch  # noqa: F401  (before the library, as in lib())
+    except ImportError:  # pragma: no cover
+        pass
+    L = ctypes.CDLL(path)
+    vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+    sp, gp = ctypes.POINTER(Nf4State), ctypes.POINTER(RowGroupsDesc)
+    L.bnbx_group_rows_workspace_bytes.argtypes = [i32, i32]
+    L.bnbx_group_rows_workspace_bytes.restype = sz
+    L.bnbx_group_rows.argtypes = [vp, i32, i32, vp, vp, vp, sz, vp]
+    L.bnbx_group_rows.restype = i32
+    L.bnbx_gemm_nf4_experts.argtypes = [vp, i64, i32, vp, sp, gp, i32, i32, i32, i32, vp, i64,
+                                        i32, vp]
+    L.bnbx_gemm_nf4_experts.restype = i32
+    _rows_lib = L
     return L
 
 
@@ -337,3 +392,24 @@ def bnbx_probe_stream_read(a, a_bytes: int, b, b_bytes: int, sink, stream=None) 
             raise BnbxError(BNBX_E_INVAL, "bnbx_probe_stream_read: byte count past the buffer")
     _check(lib().bnbx_probe_stream_read(_ptr(a), int(a_bytes), _ptr(b), int(b_bytes), _ptr(sink),
                                         _stream(stream)), "bnbx_probe_stream_read")
+
+
+def bnbx_group_rows_workspace_bytes(rows: int, groups: int) -> int:
+    return int(rows_lib().bnbx_group_rows_workspace_bytes(int(rows), int(groups)))
+
+
+def bnbx_group_rows(ids, rows: int, groups: int, offsets, order, workspace=None,
+                    workspace_bytes: int = 0, stream=None) -> None:
+    _check(rows_lib().bnbx_group_rows(_ptr(ids), int(rows), int(groups), _ptr(offsets),
+                                      _ptr(order), _ptr(workspace), int(workspace_bytes),
+                                      _stream(stream)), "bnbx_group_rows")
+
+
+def bnbx_gemm_nf4_experts(x, ldx: int, x_rows: int, packed, state: Nf4State, plan: RowGroupsDesc,
+                          N: int, K: int, gather: int, scatter: int, y, ldy: int, y_rows: int,
+                          stream=None) -> None:
+    _check(rows_lib().bnbx_gemm_nf4_experts(_ptr(x), int(ldx), int(x_rows), _ptr(packed),
+                                            ctypes.byref(state), ctypes.byref(plan), int(N),
+                                            int(K), int(gather), int(scatter), _ptr(y), int(ldy),
+                                            int(y_rows), _stream(stream)),
+           "bnbx_gemm_nf4_experts")

@@ -1,5 +1,6 @@
-"""Build libbnbx.so (the HIP kernels and the C ABI of include/bnbx.h) for
-gfx950, in-tree, with hipcc.  ``python -m dequant_gemm_nf4_amd.build``."""
+"""Build libbnbx.so (the HIP kernels and the C ABI of include/bnbx.h) and
+libbnbx_rows.so (the row-grouped operators, include/bnbx_rows.h) for gfx950,
+in-tree, with hipcc.  ``python -m dequant_gemm_nf4_amd.build``."""
 
 from __future__ import annotations
 
@@ -12,10 +13,13 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbnbx.so")
-SOURCES = ["bnbx_api.hip", "bnbx_quant.hip", "bnbx_dequant.hip", "bnbx_gemv.hip", "bnbx_gemv16.hip",
+ROWS_LIB = os.path.join(PKG, "libbnbx_rows.so")
+SOURCES = ["bnbx_api.hip", "bnbx_tables.hip", "bnbx_quant.hip", "bnbx_dequant.hip", "bnbx_gemv.hip", "bnbx_gemv16.hip",
            "bnbx_gemv_grouped.hip", "bnbx_gemv_lora.hip",
            "bnbx_gemm.hip",
            "bnbx_gemm_dx.hip", "bnbx_lora.hip", "bnbx_probe.hip"]
+ROWS_SOURCES = ["bnbx_rows_api.hip", "bnbx_tables.hip", "bnbx_rows_group.hip",
+                "bnbx_rows_stream.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -42,27 +46,30 @@ def _run(cmd):
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libbnbx.so; returns the library path."""
+    """Compile every source and link both libraries; returns libbnbx.so's
+    path."""
     os.makedirs(BUILD, exist_ok=True)
-    objs = []
     procs = []
-    for src in SOURCES:
-        obj = os.path.join(BUILD, src.replace(".hip", ".o"))
-        cmd = [HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+    for src in dict.fromkeys(SOURCES + ROWS_SOURCES):
+        cmd = [HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", _obj(src)]
         if verbose:
             print(" ".join(cmd))
         procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE,
                                             text=True)))
-        objs.append(obj)
     for cmd, p in procs:
         out, err = p.communicate()
         if p.returncode != 0:
             sys.stderr.write(out + err)
             raise RuntimeError("hipcc failed: " + " ".join(cmd))
-    tmp = LIB + ".tmp"
-    _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp])
-    os.replace(tmp, LIB)
+    for lib, sources in ((LIB, SOURCES), (ROWS_LIB, ROWS_SOURCES)):
+        tmp = lib + ".tmp"
+        _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *map(_obj, sources), "-o", tmp])
+        os.replace(tmp, lib)
     return LIB
+
+
+def _obj(src: str) -> str:
+    return os.path.join(BUILD, src.replace(".hip", ".o"))
 
 
 if __name__ == "__main__":

@@ -85,7 +85,9 @@ constexpr int kDynZeroCode = 127;
 // The device copy (constant memory, one per translation unit).
 static __constant__ DynMap kDynMapDev = make_dyn_map();
 
-// The one-time host tables (built on first use, immutable afterwards).
+// The one-time host tables (built on first use, immutable afterwards;
+// bnbx_tables.hip).  tables_ok: their self-check passed.
+bool tables_ok();
 const float* levels_f32(int quant_type);   // float[16], by code
 const EncodeTable& encode_table(int quant_type);
 const LevelTable& level_table(int quant_type);

@@ -1,0 +1,131 @@
+// Device helpers of the kernels over grouped rows.
+#pragma once
+
+#include "bnbx_device.hpp"
+#include "bnbx_rows.hpp"
+
+namespace bnbx {
+
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+constexpr uint32_t kFar = 0x80000000u;   // an offset past every buffer resource
+constexpr int kXcds = 8;
+
+__device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes,
+                                           0x00020000);
+}
+
+// Inclusive prefix sum over the wave.
+__device__ __forceinline__ int wave_scan(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// A row tile: places [r0, r1) of group g.
+struct RowTile {
+  int g, r0, r1;
+};
+
+// Row tiles of TM places, group by group (a tile never spans groups).  Every
+// wave finds its workgroup's tile by itself from the bounds on the device:
+// lane l takes group 64 c + l, a prefix over the lanes numbers the tiles.
+// Bounds are clamped to the plan's rows.
+template <int TM>
+struct RowTiles {
+  const int32_t* offsets;
+  int groups, rows;
+
+  __device__ __forceinline__ void bounds(int g, int& a, int& b) const {
+    a = b = 0;
+    if (g < groups) {
+      a = offsets[g];
+      b = offsets[g + 1];
+      a = a < 0 ? 0 : a > rows ? rows : a;
+      b = b < a ? a : b > rows ? rows : b;
+    }
+  }
+  __device__ __forceinline__ int count() const {
+    if (offsets == nullptr) return (rows + TM - 1) / TM;
+    int n = 0;
+    for (int c = 0; c < groups; c += 64) {
+      int a, b;
+      bounds(c + (int)(threadIdx.x & 63), a, b);
+      n += __builtin_amdgcn_readlane(wave_scan((b - a + TM - 1) / TM), 63);
+    }
+    return __builtin_amdgcn_readfirstlane(n);
+  }
+  // Tile t < count().
+  __device__ __forceinline__ RowTile find(int t) const {
+    RowTile r{0, 0, 0};
+    if (offsets == nullptr) {
+      r.r0 = t * TM;
+      r.r1 = r.r0 + TM < rows ? r.r0 + TM : rows;
+      return r;
+    }
+    int base = 0;
+    for (int c = 0; c < groups; c += 64) {
+      int a, b;
+      bounds(c + (int)(threadIdx.x & 63), a, b);
+      const int n = (b - a + TM - 1) / TM;
+      const int incl = base + wave_scan(n);
+      const uint64_t past = __ballot(incl > t);
+      if (past != 0) {
+        const int l = __builtin_ctzll(past);
+        const int first = __builtin_amdgcn_readlane(incl - n, l);
+        const int ga = __builtin_amdgcn_readlane(a, l), gb = __builtin_amdgcn_readlane(b, l);
+        r.g = c + l;
+        r.r0 = ga + (t - first) * TM;
+        r.r1 = r.r0 + TM < gb ? r.r0 + TM : gb;
+        return r;
+      }
+      base = __builtin_amdgcn_readlane(incl, 63);
+    }
+    return r;
+  }
+};
+
+// This workgroup's number among `total` items, XCD-aware: workgroup b runs on
+// XCD b % 8, and consecutive items go to one XCD (they share weights or rows
+// in its L2).  -1: nothing to do.
+__device__ __forceinline__ int64_t xcd_item(int64_t total) {
+  const int64_t per = (total + kXcds - 1) / kXcds;
+  const int64_t slot = blockIdx.x / kXcds, xcd = blockIdx.x % kXcds;
+  const int64_t id = xcd * per + slot;
+  return slot < per && id < total ? id : -1;
+}
+
+// Rows of X and Y of a place (-1: outside, the place is left out).
+__device__ __forceinline__ int x_row_of(const RowsGemm& a, int place) {
+  int row = place;
+  if (a.gather > 0) {
+    row = a.order[place];
+    if (a.gather > 1 && row >= 0) row = (int)((uint32_t)row / (uint32_t)a.gather);
+  }
+  return row >= 0 && row < a.x_rows ? row : -1;
+}
+__device__ __forceinline__ int y_row_of(const RowsGemm& a, int place) {
+  const int row = a.scatter ? a.order[place] : place;
+  return row >= 0 && row < a.y_rows ? row : -1;
+}
+
+// Eight binary16 values as two bf16 operands, hi + lo, exactly: binary16 has
+// 11 significant bits, bf16 8, and the rest fits lo (bf16 reaches far below
+// binary16's subnormals).
+__device__ __forceinline__ void split_f16(u32x4_t v, u32x4_t& hi, u32x4_t& lo) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const f16x2_t p = __builtin_bit_cast(f16x2_t, (uint32_t)v[k]);
+    const float a = (float)p[0], b = (float)p[1];
+    const uint32_t h = pack_bf16x2(a, b);
+    hi[k] = h;
+    const float ra = a - bf16lo_to_f32(h), rb = b - bf16hi_to_f32(h);
+    lo[k] = pack_bf16x2(ra, rb);
+  }
+}
+
+}  // namespace bnbx

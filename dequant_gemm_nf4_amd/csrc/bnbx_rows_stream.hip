@@ -1,0 +1,414 @@
+// 4-bit products over grouped rows, few rows a group, for gfx950:
+//   Y_i = X_i . W_hat_g^T (+ XA_i . B_a^T),  i a place of group g,
+// W_hat_g[n][k] = rnd16(L[code] * scale), the dequantized weight exactly as
+// stored (the products run on the same 16-bit values bnbx_dequantize_nf4
+// gives), fp32 accumulation, one rounding of Y.
+//
+// Bound: streaming the packed weights of every group that has rows, once per
+// row tile (RB x 16 places), and the vector work of the dequant.
+//
+// A wave takes units of 16 weight rows x 256 k (2 KB packed).  Loads are
+// quad-coalesced (lane x: 16 bytes of row x / 4, twice); a 2 KB LDS stage per
+// wave turns them so that lane (q, r) (q = lane / 16, r = lane % 16) holds the
+// 32 bytes of block q of row r: one block scale and one 16-entry table per
+// lane and unit.  Dword m of them is the A operand of MFMA m (16x16x32: A row
+// r, eight k); which eight k feed which MFMA is free as long as X agrees: lane
+// q of X takes k = 64 q + 8 m.  So D has the weight rows down the values
+// (n = 4 q + v) and the places across the lanes (i = lane % 16).
+//
+// X goes through LDS, double-buffered, in slices of 256 k: 32 chunks of 16
+// bytes a row, chunk c of row r in slot c ^ (r % 16), so that 16 lanes reading
+// one chunk of 16 rows hit 64 banks.
+//
+// WN waves of a workgroup take different weight rows (and share X), WK waves
+// split K slice by slice; their sums meet in LDS in wave order.  WK > 1 is for
+// launches whose weight rows alone give the GPU too few waves.
+#include "bnbx_rows_device.hpp"
+#include "bnbx_tab16.hpp"
+
+namespace bnbx {
+namespace {
+
+constexpr int kSlice = 256;          // k per unit
+constexpr int kAhead = 2;            // units loaded ahead
+
+template <int RB, int NB, int WN, int WK, bool DQ, bool F16>
+__global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, int tiles_n,
+                                                                  LevelTable lv) {
+  constexpr int TM = 16 * RB, TN = 16 * NB * WN;
+  constexpr int kXBuf = WK * TM * kSlice;            // 16-bit elements
+  constexpr int kXLoads = RB * 8 / WN > 0 ? RB * 8 / WN : 1;   // 1 KB loads of X a wave
+  constexpr int kStages = WN * WK * 2048;
+  constexpr int kRedBytes = (WK - 1) * WN * RB * NB * 1024;
+  constexpr int kLds = 2 * kXBuf * 2 + kStages;
+  static_assert(kRedBytes <= kLds, "the partial sums reuse X and the stages");
+  static_assert(RB * 8 % WN == 0 || WN > RB * 8, "X loads split evenly over the waves");
+  __shared__ __attribute__((aligned(16))) unsigned char smem[kLds];
+  __shared__ float dmap[256];
+
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wn = wave % WN, wk = wave / WN;
+  const int r = lane & 15, q = lane >> 4;      // MFMA layout
+  const int lr = lane >> 2, lp = lane & 3;     // load layout: row, piece
+
+  const RowTiles<TM> tiles{a.offsets, a.groups, a.rows};
+  const int nt = tiles.count();
+  const int64_t id = xcd_item((int64_t)nt * tiles_n);
+  if (id < 0) return;
+  // row tiles of one group and the same weight rows are neighbours: they
+  // meet in one L2
+  const int tn = __builtin_amdgcn_readfirstlane((int)(id / nt));
+  const RowTile tile = tiles.find(__builtin_amdgcn_readfirstlane((int)(id % nt)));
+  const int n0 = tn * TN + wn * 16 * NB;
+
+  const bool dyn = a.double_quant == kDqDynamic;
+  if (DQ && dyn)
+    for (int e = t; e < 256; e += WN * WK * 64) dmap[e] = kDynMapDev.v[e];
+  const float mu = DQ ? *a.mean : 0.0f;
+  const uint32_t rowK2 = (uint32_t)a.K >> 1, nkb = (uint32_t)a.K >> 6;
+  const int nslices = (a.K + kSlice - 1) / kSlice;
+  const int nsteps = (nslices + WK - 1) / WK;
+
+  // Resources of this group's weight: 64-bit bases, 32-bit offsets inside.
+  const uint32_t nblocks = (uint32_t)a.N * nkb;
+  const int64_t blk0 = (int64_t)tile.g * nblocks;
+  const rsrc_t rw = make_rsrc(a.packed + (int64_t)tile.g * a.N * rowK2, (uint32_t)a.N * rowK2);
+  const rsrc_t rq = make_rsrc((const char*)a.absmax + blk0 * (DQ ? 1 : 4),
+                              DQ ? nblocks : nblocks * 4u);
+  const uint32_t grem = (uint32_t)(blk0 & 255);   // the group's first block in its scale group
+  const rsrc_t rg = make_rsrc(DQ ? a.absmax2 + (blk0 >> 8) : nullptr,
+                              DQ ? (grem + nblocks + 255u) / 256u * 4u : 0u);
+
+  struct Unit {
+    u32x4_t w[2];
+    uint32_t q;    // code byte, or the fp32 block maximum
+    float s;       // group scale
+  };
+  uint32_t wrow[NB], brow[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int nl = n0 + 16 * j + lr, nm = n0 + 16 * j + r;
+    wrow[j] = nl < a.N ? (uint32_t)nl * rowK2 + 16u * (uint32_t)lp : kFar;
+    brow[j] = nm < a.N ? (uint32_t)nm * nkb + (uint32_t)q : kFar;
+  }
+  auto load_unit = [&](Unit& u, int j, int slice) {
+    const bool in = slice < nslices;
+    const uint32_t wo = in ? wrow[j] + (uint32_t)slice * (kSlice / 2) : kFar;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      u.w[h] = __builtin_amdgcn_raw_buffer_load_b128(rw, wo + 64u * h, 0, 2);
+    // the lane's block; past the end of the row it has no scale and no value
+    const bool bin = in && brow[j] != kFar && 4u * (uint32_t)slice + (uint32_t)q < nkb;
+    const uint32_t blk = brow[j] + 4u * (uint32_t)slice;
+    if (DQ) {
+      u.q = __builtin_amdgcn_raw_buffer_load_b8(rq, bin ? blk : kFar, 0, 0);
+      u.s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                          rg, bin ? ((grem + blk) >> 8) * 4u : kFar, 0, 0));
+    } else {
+      u.q = __builtin_amdgcn_raw_buffer_load_b32(rq, bin ? blk * 4u : kFar, 0, 0);
+      u.s = 0.0f;
+    }
+  };
+  auto scale_of = [&](const Unit& u, int j, int slice) {
+    const bool bin = brow[j] != kFar && 4u * (uint32_t)slice + (uint32_t)q < nkb;
+    float sc;
+    if (DQ) {
+      if (dyn) {
+        const float prod = dmap[u.q & 0xffu] * u.s;
+        sc = prod + mu;
+      } else {
+        sc = dq_scale((float)(int8_t)(uint8_t)u.q, u.s, mu);
+      }
+    } else {
+      sc = __builtin_bit_cast(float, u.q);
+    }
+    return bin ? sc : 0.0f;
+  };
+
+  // Units of the first steps go out before the rows of X are looked up.
+  Unit un[kAhead][NB];
+#pragma unroll
+  for (int p = 0; p < kAhead; ++p)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) load_unit(un[p][j], j, p * WK + wk);
+
+  // X: the WN waves of one K part copy its slice, 2 rows an instruction
+  // (lane l: row l / 32, slot l % 32).  Rows past the tile repeat its first
+  // row (their results are never stored); chunks past K repeat chunk 0 (their
+  // operands are zeroed below).
+  uint16_t* const xs = (uint16_t*)smem;
+  unsigned char* const stage = smem + 2 * kXBuf * 2 + wave * 2048;
+  const bool xwave = WN <= RB * 8 || wn < RB * 8;
+  const uint16_t* xp[kXLoads];
+  int xk[kXLoads];
+  uint32_t xslot[kXLoads];
+#pragma unroll
+  for (int i = 0; i < kXLoads; ++i) {
+    const int row = 2 * (wn * kXLoads + i) + (lane >> 5);
+    const int place = tile.r0 + row < tile.r1 ? tile.r0 + row : tile.r0;
+    int xr = xwave ? x_row_of(a, place) : 0;
+    xr = xr < 0 ? 0 : xr;
+    xp[i] = a.x + (int64_t)xr * a.ldx;
+    xk[i] = 8 * ((lane & 31) ^ (row & 15));
+    xslot[i] = (uint32_t)((wk * TM + row) * kSlice + 8 * (lane & 31));
+  }
+  u32x4_t xv[kXLoads];
+  auto load_x = [&](int slice) {
+    if (!xwave) return;
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i) {
+      const int k = slice * kSlice + xk[i];
+      xv[i] = *(const u32x4_t*)(xp[i] + (k < a.K ? k : 0));
+    }
+  };
+  auto put_x = [&](int buf) {
+    if (!xwave) return;
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i) *(u32x4_t*)(xs + buf * kXBuf + xslot[i]) = xv[i];
+  };
+  auto barrier = [] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+
+  // Stage slots: piece p (16 bytes) of row w at slot 8 w + (p ^ f(w)), free of
+  // bank conflicts both ways.
+  auto fold = [](int w) { return ((w >> 1) & 1) * 4 + ((w >> 2) & 3); };
+  const uint32_t ws0 = 16u * (uint32_t)(8 * lr + (lp ^ fold(lr)));
+  const uint32_t rs0 = 16u * (uint32_t)(8 * r + ((2 * q) ^ fold(r)));
+
+  f32x4_t acc[NB][RB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+#pragma unroll
+    for (int i = 0; i < RB; ++i) acc[j][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  auto step = [&](Unit (&u)[NB], int s) {
+    const int slice = s * WK + wk;
+    Tab16 tab[NB];
+    u32x4_t w[NB][2];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      tab[j] = make_tab16_any<F16>(lv, scale_of(u[j], j, slice));
+      *(u32x4_t*)(stage + ws0) = u[j].w[0];
+      *(u32x4_t*)(stage + (ws0 ^ 64u)) = u[j].w[1];
+      w[j][0] = *(const u32x4_t*)(stage + rs0);
+      w[j][1] = *(const u32x4_t*)(stage + (rs0 ^ 16u));
+      load_unit(u[j], j, (s + kAhead) * WK + wk);
+    }
+    const uint16_t* xb = xs + (s & 1) * kXBuf + wk * TM * kSlice;
+    const bool tail = (slice + 1) * kSlice > a.K;   // uniform
+    const bool kin = 4u * (uint32_t)slice + (uint32_t)q < nkb;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      u32x4_t xo[RB];
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        xo[i] = *(const u32x4_t*)(xb + (16 * i + r) * kSlice + 8 * ((8 * q + m) ^ r));
+        if (tail && !kin) xo[i] = u32x4_t{0u, 0u, 0u, 0u};
+      }
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        uint32_t o[4];
+        decode8(w[j][m >> 2][m & 3], tab[j], o);
+        const u32x4_t wo = {o[0], o[1], o[2], o[3]};
+#pragma unroll
+        for (int i = 0; i < RB; ++i) acc[j][i] = mfma_16x16x32<F16>(wo, xo[i], acc[j][i]);
+      }
+    }
+  };
+
+  load_x(wk);
+  put_x(0);
+  barrier();
+  for (int s = 0; s < nsteps; s += kAhead) {
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p) {
+      if (s + p < nsteps) {
+        if (s + p + 1 < nsteps) load_x((s + p + 1) * WK + wk);
+        step(un[p], s + p);
+        if (s + p + 1 < nsteps) put_x((s + p + 1) & 1);
+        barrier();
+      }
+    }
+  }
+
+  // Low-rank term: the adapters whose places meet the tile, each in steps of
+  // 32 ranks, shared out over the WK waves.  XA's two planes and, for fp16, B
+  // split into two bf16 parts (11 bits: exact) keep the term's error at 2^-16
+  // of it; products run in bf16 for the range.  Each adapter's term is summed
+  // apart and added to its own places only, so one adapter's infinities never
+  // reach another request's row.
+  if (a.lora.offsets != nullptr) {
+    const LoraRows& lo = a.lora;
+    int seg = 0;
+    for (int c = 0; c < lo.adapters; c += 64) {
+      int b0 = 0, b1 = 0;
+      const int gl = c + lane;
+      if (gl < lo.adapters) {
+        b0 = lo.offsets[gl];
+        b1 = lo.offsets[gl + 1];
+      }
+      uint64_t hit = __ballot(b0 < b1 && b0 < tile.r1 && b1 > tile.r0);
+      while (hit != 0) {
+        const int l = __builtin_ctzll(hit);
+        hit &= hit - 1;
+        const int s0 = __builtin_amdgcn_readlane(b0, l), s1 = __builtin_amdgcn_readlane(b1, l);
+        const uint16_t* bb = lo.b + (int64_t)(c + l) * lo.stride_b;
+        f32x4_t term[NB][RB];
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int i = 0; i < RB; ++i) term[j][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = 0; k < lo.r; k += 32, ++seg) {
+          if (seg % WK != wk) continue;   // uniform in the wave
+          const int k8 = k + 8 * q;
+          u32x4_t bh[NB], bl[NB];
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            const int n = n0 + 16 * j + r;
+            u32x4_t v = {0u, 0u, 0u, 0u};
+            if (k8 < lo.r && n < a.N) v = *(const u32x4_t*)(bb + (int64_t)n * lo.ldb + k8);
+            bh[j] = v;
+            if (F16) split_f16(v, bh[j], bl[j]);
+          }
+#pragma unroll
+          for (int i = 0; i < RB; ++i) {
+            const int place = tile.r0 + 16 * i + r;
+            u32x4_t xh = {0u, 0u, 0u, 0u}, xl = {0u, 0u, 0u, 0u};
+            if (k8 < lo.r && place < tile.r1 && place >= s0 && place < s1) {
+              const uint16_t* xa = lo.xa + (int64_t)place * 2 * lo.r + k8;
+              xh = *(const u32x4_t*)xa;
+              xl = *(const u32x4_t*)(xa + lo.r);
+            }
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+              term[j][i] = mfma_16x16x32<false>(bh[j], xh, term[j][i]);
+              term[j][i] = mfma_16x16x32<false>(bh[j], xl, term[j][i]);
+              if (F16) term[j][i] = mfma_16x16x32<false>(bl[j], xh, term[j][i]);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+          const int place = tile.r0 + 16 * i + r;
+          const bool own = place >= s0 && place < s1;
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[j][i][v] = own ? acc[j][i][v] + term[j][i][v] : acc[j][i][v];
+        }
+      }
+    }
+  }
+
+  // The K parts' sums, in wave order (X and the stages are free: every wave
+  // has passed the last barrier).
+  if (WK > 1) {
+    f32x4_t* const red = (f32x4_t*)smem;
+    if (wk > 0) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+          red[(((wk - 1) * WN + wn) * NB * RB + j * RB + i) * 64 + lane] = acc[j][i];
+    }
+    __syncthreads();
+    if (wk > 0) return;
+#pragma unroll
+    for (int p = 0; p < WK - 1; ++p)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+          const f32x4_t v = red[((p * WN + wn) * NB * RB + j * RB + i) * 64 + lane];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][i][e] += v[e];
+        }
+  }
+
+  // Lane (q, r): place r of each 16, weight rows 4 q .. 4 q + 3 of each 16.
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    const int place = tile.r0 + 16 * i + r;
+    if (place >= tile.r1 || x_row_of(a, place) < 0) continue;
+    const int row = y_row_of(a, place);
+    if (row < 0) continue;
+    uint16_t* const yr = a.y + (int64_t)row * a.ldy;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int n = n0 + 16 * j + 4 * q;
+      const uint32_t p0 = pack16x2<F16>(acc[j][i][0], acc[j][i][1]);
+      const uint32_t p1 = pack16x2<F16>(acc[j][i][2], acc[j][i][3]);
+      if (n + 3 < a.N && ((uintptr_t)(yr + n) & 7) == 0) {
+        *(uint2*)(yr + n) = make_uint2(p0, p1);
+      } else {
+        if (n < a.N) yr[n] = (uint16_t)p0;
+        if (n + 1 < a.N) yr[n + 1] = (uint16_t)(p0 >> 16);
+        if (n + 2 < a.N) yr[n + 2] = (uint16_t)p1;
+        if (n + 3 < a.N) yr[n + 3] = (uint16_t)(p1 >> 16);
+      }
+    }
+  }
+}
+
+template <int RB, int NB, int WN, int WK>
+hipError_t launch_one(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream) {
+  constexpr int TM = 16 * RB, TN = 16 * NB * WN;
+  const int tiles_n = (a.N + TN - 1) / TN;
+  const int64_t most = a.rows / TM + (a.groups < a.rows ? a.groups : a.rows);   // row tiles
+  const int64_t grid = (most * tiles_n + kXcds - 1) / kXcds * kXcds;
+  if (grid > 0x7fffffff) return hipErrorNotSupported;
+  const LevelTable& lv = level_table(quant_type);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(WN * WK * 64), 0, stream, a, tiles_n,
+                       lv);
+  };
+  if (a.double_quant != kDqNone) {
+    if (f16) go(rows_stream_kernel<RB, NB, WN, WK, true, true>);
+    else go(rows_stream_kernel<RB, NB, WN, WK, true, false>);
+  } else {
+    if (f16) go(rows_stream_kernel<RB, NB, WN, WK, false, true>);
+    else go(rows_stream_kernel<RB, NB, WN, WK, false, false>);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rows_stream(const RowsGemm& a, int quant_type, bool f16, int cus,
+                              hipStream_t stream) {
+  const int groups = a.offsets == nullptr ? 1 : (a.groups < a.rows ? a.groups : a.rows);
+  const int mean_rows = (a.rows + groups - 1) / groups;
+  const int rb = mean_rows <= 16 ? 1 : mean_rows <= 32 ? 2 : 4;
+  // Row tiles the launch is likely to have, times 16-row weight slabs.
+  const int64_t tm = 16 * rb;
+  const int64_t slabs = (int64_t)groups * ((mean_rows + tm - 1) / tm) * ((a.N + 15) / 16);
+  const int64_t waves = slabs / (rb == 4 ? 2 : 1);
+  const int64_t full = (int64_t)cus * 16;
+  if (rb == 1) {
+    if (waves >= full) return launch_one<1, 1, 8, 1>(a, quant_type, f16, stream);
+    if (waves * 4 >= full) return launch_one<1, 1, 2, 4>(a, quant_type, f16, stream);
+    return launch_one<1, 1, 1, 8>(a, quant_type, f16, stream);
+  }
+  if (rb == 2) {
+    if (waves >= full) return launch_one<2, 1, 8, 1>(a, quant_type, f16, stream);
+    return launch_one<2, 1, 2, 4>(a, quant_type, f16, stream);
+  }
+  if (waves * 2 >= full) return launch_one<4, 2, 4, 1>(a, quant_type, f16, stream);
+  return launch_one<4, 2, 2, 2>(a, quant_type, f16, stream);
+}
+
+int device_cus() {
+  static int n = 0;
+  if (n == 0) {
+    int dev = 0, v = 0;
+    if (hipGetDevice(&dev) == hipSuccess &&
+        hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess &&
+        v > 0)
+      n = v;
+    else
+      n = 256;
+  }
+  return n;
+}
+
+}  // namespace bnbx

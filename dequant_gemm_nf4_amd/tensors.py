@@ -8,7 +8,9 @@ import dataclasses
 
 import torch
 
-from . import (Nf4State, bnbx_dequantize_nf4, bnbx_gemm_nf4, bnbx_gemm_nf4_dx, bnbx_gemm_nf4_lora,
+from . import (Nf4State, RowGroupsDesc, bnbx_dequantize_nf4, bnbx_gemm_nf4_experts,
+               bnbx_group_rows, bnbx_group_rows_workspace_bytes,
+               bnbx_gemm_nf4, bnbx_gemm_nf4_dx, bnbx_gemm_nf4_lora,
                bnbx_gemm_nf4_workspace_bytes, bnbx_gemv_nf4, bnbx_gemv_nf4_grouped, bnbx_lora_down,
                bnbx_quantize_nf4, bnbx_quantize_nf4_grouped,
                bnbx_quantize_nf4_grouped_workspace_bytes, bnbx_quantize_nf4_workspace_bytes)
@@ -206,3 +208,113 @@ def linear_lora(x: torch.Tensor, q: QuantizedWeight, lora_a: torch.Tensor, lora_
     xa = lora_down(x, lora_a, scale, stream=stream)
     return gemm_lora(x, q, xa, lora_b, out=out, stream=stream)
 
+
+
+# --------------------------------------------------------------------------
+# rows that belong to groups (include/bnbx_rows.h)
+# --------------------------------------------------------------------------
+@dataclasses.dataclass
+class RowGroups:
+    """A plan of bnbx_group_rows: the rows 0 .. rows-1 in group order.  Group
+    g holds the places offsets[g] .. offsets[g+1]-1 of ``order``; places
+    behind offsets[groups] are rows of no group."""
+
+    groups: int
+    offsets: torch.Tensor   # int32 [groups + 1]
+    order: torch.Tensor     # int32 [rows]
+
+    @property
+    def rows(self) -> int:
+        return self.order.shape[0]
+
+    @property
+    def desc(self) -> RowGroupsDesc:
+        return RowGroupsDesc(self.offsets.data_ptr(), self.order.data_ptr(), self.groups,
+                             self.order.shape[0])
+
+
+def _check_plan(rows: RowGroups, device) -> None:
+    for name, t, n in (("offsets", rows.offsets, rows.groups + 1),
+                       ("order", rows.order, rows.order.numel())):
+        if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"plan: {name} must be a contiguous int32 vector of {n}")
+        if t.device != device:
+            raise ValueError(f"plan: {name} is on {t.device}, the data on {device}")
+
+
+def _check_matrix(name: str, t: torch.Tensor, cols: int, dtype, device) -> None:
+    if t.dim() != 2 or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [rows, {cols}], not {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.stride(1) != 1 and t.numel() > 0:
+        raise ValueError(f"{name} must have contiguous rows")
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride; of a matrix of at most one row (whose stride torch leaves
+    open) its width, rounded up to the ABI's 8."""
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+def _on(device):
+    """The device of the data as the current one, for the launch."""
+    if device.type != "cuda":
+        raise ValueError(f"the data must be on a GPU, not on {device}")
+    return torch.cuda.device(device)
+
+
+def empty_row_groups(rows: int, groups: int, device="cuda") -> RowGroups:
+    return RowGroups(groups, torch.empty(groups + 1, dtype=torch.int32, device=device),
+                     torch.empty(rows, dtype=torch.int32, device=device))
+
+
+def group_rows(ids: torch.Tensor, groups: int, out: RowGroups | None = None,
+               workspace: torch.Tensor | None = None, stream=None) -> RowGroups:
+    """bnbx_group_rows: the plan of an int32 vector of group ids (any id
+    outside 0 .. groups-1: no group), on the device, stable."""
+    if ids.dtype != torch.int32 or ids.dim() != 1 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 vector")
+    plan = out if out is not None else empty_row_groups(ids.numel(), groups, ids.device)
+    if plan.groups != groups or plan.rows != ids.numel():
+        raise ValueError("out: a plan of other sizes")
+    _check_plan(plan, ids.device)
+    with _on(ids.device):
+        nbytes = bnbx_group_rows_workspace_bytes(ids.numel(), groups)
+        if nbytes and workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=ids.device)
+        bnbx_group_rows(ids, ids.numel(), groups, plan.offsets, plan.order,
+                        workspace if nbytes else None,
+                        workspace.numel() * workspace.element_size() if nbytes else 0, stream)
+    return plan
+
+
+def _check_stack(q: QuantizedWeight, rows: RowGroups) -> None:
+    if len(q.shape) != 3 or q.shape[0] != rows.groups:
+        raise ValueError(f"the weight must be a stack [{rows.groups}, N, K], not {q.shape}")
+
+
+def gemm_experts(x: torch.Tensor, q: QuantizedWeight, rows: RowGroups, gather: int = 0,
+                 scatter: bool = False, out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """Y_i = X_i . W_hat_g^T for the places i of every group g of the plan
+    (bnbx_gemm_nf4_experts), W_hat [groups, N, K].  ``gather`` >= 1 reads row
+    order[i] // gather of x (top_k for tokens with top_k slots), 0 row i;
+    ``scatter`` writes row order[i] of the result, else row i.  Rows without a
+    group keep what ``out`` holds (zero if it is allocated here)."""
+    _check_stack(q, rows)
+    _, N, K = q.shape
+    _check_matrix("x", x, K, q.dtype, q.packed.device)
+    _check_plan(rows, x.device)
+    y = out if out is not None else torch.zeros(rows.rows, N, dtype=q.dtype, device=x.device)
+    _check_matrix("out", y, N, q.dtype, x.device)
+    if (gather == 0 and x.shape[0] < rows.rows) or y.shape[0] < rows.rows:
+        raise ValueError("fewer rows than the plan has places")
+    if gather > 0 and x.shape[0] * gather < rows.rows:
+        raise ValueError("fewer rows of x than the plan's slots belong to")
+    with _on(x.device):
+        bnbx_gemm_nf4_experts(x, _ld(x), x.shape[0], q.packed, q.state, rows.desc, N, K, gather,
+                              int(scatter), y, _ld(y), y.shape[0], stream)
+    return y
