@@ -32,7 +32,8 @@ __all__ = [
     "BNBX_DTYPE_BF16", "BNBX_DTYPE_F16", "BNBX_DQ_NONE", "BNBX_DQ_LINEAR", "BNBX_DQ_DYNAMIC",
     "rows_library_path", "rows_lib", "ROWS_EXPORTED_SYMBOLS", "BNBX_ROWS_MAX_GROUPS",
     "RowGroupsDesc", "bnbx_group_rows_workspace_bytes", "bnbx_group_rows",
-    "bnbx_gemm_nf4_experts",
+    "bnbx_gemm_nf4_experts", "bnbx_gemm_nf4_experts_dx", "AdaptersDesc",
+    "bnbx_gemm_nf4_adapters_workspace_bytes", "bnbx_gemm_nf4_adapters",
 ]
 
 BNBX_OK = 0
@@ -71,6 +72,8 @@ BNBX_PROBE_SINK_WORDS = 1024
 BNBX_ROWS_MAX_GROUPS = 1024
 ROWS_EXPORTED_SYMBOLS = (
     "bnbx_group_rows_workspace_bytes", "bnbx_group_rows", "bnbx_gemm_nf4_experts",
+    "bnbx_gemm_nf4_experts_dx", "bnbx_gemm_nf4_adapters_workspace_bytes",
+    "bnbx_gemm_nf4_adapters",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -137,6 +140,21 @@ class RowGroupsDesc(ctypes.Structure):
         ("order", ctypes.c_void_p),
         ("groups", ctypes.c_int32),
         ("rows", ctypes.c_int32),
+    ]
+
+
+class AdaptersDesc(ctypes.Structure):
+    """bnbx_adapters: the low-rank adapters of a call (device pointers)."""
+
+    _fields_ = [
+        ("lora_a", ctypes.c_void_p),
+        ("lora_b", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("lda", ctypes.c_int64),
+        ("stride_a", ctypes.c_int64),
+        ("ldb", ctypes.c_int64),
+        ("stride_b", ctypes.c_int64),
+        ("r", ctypes.c_int32),
     ]
 
 
@@ -234,6 +252,13 @@ def rows_lib() -> ctypes.CDLL:
     L.bnbx_gemm_nf4_experts.argtypes = [vp, i64, i32, vp, sp, gp, i32, i32, i32, i32, vp, i64,
                                         i32, vp]
     L.bnbx_gemm_nf4_experts.restype = i32
+    L.bnbx_gemm_nf4_experts_dx.argtypes = L.bnbx_gemm_nf4_experts.argtypes
+    L.bnbx_gemm_nf4_experts_dx.restype = i32
+    L.bnbx_gemm_nf4_adapters_workspace_bytes.argtypes = [i32, i32]
+    L.bnbx_gemm_nf4_adapters_workspace_bytes.restype = sz
+    L.bnbx_gemm_nf4_adapters.argtypes = [vp, i64, vp, sp, gp, i32, i32,
+                                         ctypes.POINTER(AdaptersDesc), vp, i64, vp, sz, vp]
+    L.bnbx_gemm_nf4_adapters.restype = i32
     _rows_lib = L
     return L
 
@@ -413,3 +438,27 @@ def bnbx_gemm_nf4_experts(x, ldx: int, x_rows: int, packed, state: Nf4State, pla
                                             int(K), int(gather), int(scatter), _ptr(y), int(ldy),
                                             int(y_rows), _stream(stream)),
            "bnbx_gemm_nf4_experts")
+
+
+def bnbx_gemm_nf4_experts_dx(dy, lddy: int, dy_rows: int, packed, state: Nf4State,
+                             plan: RowGroupsDesc, N: int, K: int, gather: int, scatter: int, dx,
+                             lddx: int, dx_rows: int, stream=None) -> None:
+    _check(rows_lib().bnbx_gemm_nf4_experts_dx(_ptr(dy), int(lddy), int(dy_rows), _ptr(packed),
+                                               ctypes.byref(state), ctypes.byref(plan), int(N),
+                                               int(K), int(gather), int(scatter), _ptr(dx),
+                                               int(lddx), int(dx_rows), _stream(stream)),
+           "bnbx_gemm_nf4_experts_dx")
+
+
+def bnbx_gemm_nf4_adapters_workspace_bytes(rows: int, r: int) -> int:
+    return int(rows_lib().bnbx_gemm_nf4_adapters_workspace_bytes(int(rows), int(r)))
+
+
+def bnbx_gemm_nf4_adapters(x, ldx: int, packed, state: Nf4State, plan: RowGroupsDesc, N: int,
+                           K: int, adapters: AdaptersDesc, y, ldy: int, workspace=None,
+                           workspace_bytes: int = 0, stream=None) -> None:
+    _check(rows_lib().bnbx_gemm_nf4_adapters(_ptr(x), int(ldx), _ptr(packed), ctypes.byref(state),
+                                             ctypes.byref(plan), int(N), int(K),
+                                             ctypes.byref(adapters), _ptr(y), int(ldy),
+                                             _ptr(workspace), int(workspace_bytes),
+                                             _stream(stream)), "bnbx_gemm_nf4_adapters")

@@ -49,9 +49,25 @@ struct RowsGemm {
   LoraRows lora;
 };
 
+// The adapters' down-projections into xa's planes (bnbx_rows_lora.hip).
+struct LoraDown {
+  const int32_t* offsets;
+  int adapters;
+  int r;
+  const uint16_t* a;        // adapter g's A [r, K], row j at a + g stride + j ld
+  int64_t lda, stride_a;
+  const float* scale;       // [adapters]
+};
+hipError_t launch_rows_lora_down(const RowsGemm& a, const LoraDown& d, bool f16, int cus,
+                                 uint16_t* xa, hipStream_t stream);
+
 // Streaming form: row tiles of 16, 32 or 64 places (bnbx_rows_stream.hip).
 hipError_t launch_rows_stream(const RowsGemm& a, int quant_type, bool f16, int cus,
                               hipStream_t stream);
+
+// dX_i = dY_i . W_hat_g: x is dY [x_rows, N], y is dX [y_rows, K]; N a
+// multiple of 64 (bnbx_rows_dx.hip).
+hipError_t launch_rows_dx(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream);
 
 // Compute units of the current device.
 int device_cus();

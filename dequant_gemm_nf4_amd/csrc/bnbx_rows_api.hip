@@ -108,4 +108,61 @@ int bnbx_gemm_nf4_experts(const uint16_t* x, int64_t ldx, int x_rows, const uint
                                         device_cus(), (hipStream_t)stream));
 }
 
+int bnbx_gemm_nf4_experts_dx(const uint16_t* dy, int64_t lddy, int dy_rows,
+                             const uint8_t* packed, const bnbx_nf4_state* st,
+                             const bnbx_row_groups* plan, int N, int K, int gather, int scatter,
+                             uint16_t* dx, int64_t lddx, int dx_rows, void* stream) {
+  int s = check_plan(plan);
+  if (s != BNBX_OK) return s;
+  s = check_rows(dy, lddy, dy_rows, N, packed, st, plan->groups, N, K, gather, scatter, dx, lddx,
+                 dx_rows, K);
+  if (s != BNBX_OK) return s;
+  if (N % 64 != 0) return BNBX_E_UNSUPPORTED;
+  if (plan->rows == 0 || dy_rows == 0 || dx_rows == 0) return BNBX_OK;
+  const RowsGemm a = rows_gemm(dy, lddy, dy_rows, packed, st, plan, N, K, gather, scatter, dx,
+                               lddx, dx_rows);
+  return rows_status(launch_rows_dx(a, st->quant_type, st->compute_dtype == BNBX_DTYPE_F16,
+                                    (hipStream_t)stream));
+}
+
+size_t bnbx_gemm_nf4_adapters_workspace_bytes(int rows, int r) {
+  if (rows < 0 || r < 16 || r > 256 || r % 16 != 0) return 0;
+  return (size_t)rows * 2 * (size_t)r * sizeof(uint16_t);
+}
+
+int bnbx_gemm_nf4_adapters(const uint16_t* x, int64_t ldx, const uint8_t* packed,
+                           const bnbx_nf4_state* st, const bnbx_row_groups* plan, int N, int K,
+                           const bnbx_adapters* ad, uint16_t* y, int64_t ldy, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  int s = check_plan(plan);
+  if (s != BNBX_OK) return s;
+  s = check_rows(x, ldx, plan->rows, K, packed, st, 1, N, K, 1, 1, y, ldy, plan->rows, N);
+  if (s != BNBX_OK) return s;
+  if (ad == nullptr || ad->lora_a == nullptr || ad->lora_b == nullptr || ad->scale == nullptr)
+    return BNBX_E_INVAL;
+  if (ad->r < 16 || ad->r > 256 || ad->r % 16 != 0) return BNBX_E_INVAL;
+  if (ad->lda < K || ad->ldb < ad->r || ad->stride_a < 0 || ad->stride_b < 0) return BNBX_E_INVAL;
+  if (ad->lda % 8 != 0 || ad->ldb % 8 != 0 || ad->stride_a % 8 != 0 || ad->stride_b % 8 != 0)
+    return BNBX_E_ALIGN;
+  if (!aligned(ad->lora_a, 16) || !aligned(ad->lora_b, 16) || !aligned(ad->scale, 4))
+    return BNBX_E_ALIGN;
+  if (plan->rows == 0) return BNBX_OK;
+  const size_t need = bnbx_gemm_nf4_adapters_workspace_bytes(plan->rows, ad->r);
+  if (workspace == nullptr || workspace_bytes < need) return BNBX_E_WORKSPACE;
+  if (!aligned(workspace, 16)) return BNBX_E_ALIGN;
+  const bool f16 = st->compute_dtype == BNBX_DTYPE_F16;
+  const int cus = device_cus();
+  hipStream_t hs = (hipStream_t)stream;
+  RowsGemm a = rows_gemm(x, ldx, plan->rows, packed, st, plan, N, K, 1, 1, y, ldy, plan->rows);
+  const LoraDown d{plan->offsets, plan->groups, ad->r, ad->lora_a, ad->lda, ad->stride_a,
+                   ad->scale};
+  const hipError_t e = launch_rows_lora_down(a, d, f16, cus, (uint16_t*)workspace, hs);
+  if (e != hipSuccess) return rows_status(e);
+  a.offsets = nullptr;   // the shared weight: one group of all rows
+  a.groups = 1;
+  a.lora = LoraRows{plan->offsets, plan->groups, ad->r, (const uint16_t*)workspace, ad->lora_b,
+                    ad->ldb, ad->stride_b};
+  return rows_status(launch_rows_stream(a, st->quant_type, f16, cus, hs));
+}
+
 }  // extern "C"

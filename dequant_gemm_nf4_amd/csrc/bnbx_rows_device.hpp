@@ -15,6 +15,12 @@ __device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
                                            0x00020000);
 }
 
+// Range of a resource over `bytes` bytes (at most what 32-bit offsets that
+// stay below kFar can reach).
+__device__ __forceinline__ uint32_t rsrc_bytes(int64_t bytes) {
+  return bytes <= 0 ? 0u : bytes < (int64_t)kFar ? (uint32_t)bytes : kFar;
+}
+
 // Inclusive prefix sum over the wave.
 __device__ __forceinline__ int wave_scan(int v) {
   const int lane = threadIdx.x & 63;

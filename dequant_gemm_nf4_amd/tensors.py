@@ -8,7 +8,9 @@ import dataclasses
 
 import torch
 
-from . import (Nf4State, RowGroupsDesc, bnbx_dequantize_nf4, bnbx_gemm_nf4_experts,
+from . import (AdaptersDesc, Nf4State, RowGroupsDesc, bnbx_dequantize_nf4, bnbx_gemm_nf4_experts,
+               bnbx_gemm_nf4_adapters, bnbx_gemm_nf4_adapters_workspace_bytes,
+               bnbx_gemm_nf4_experts_dx,
                bnbx_group_rows, bnbx_group_rows_workspace_bytes,
                bnbx_gemm_nf4, bnbx_gemm_nf4_dx, bnbx_gemm_nf4_lora,
                bnbx_gemm_nf4_workspace_bytes, bnbx_gemv_nf4, bnbx_gemv_nf4_grouped, bnbx_lora_down,
@@ -296,6 +298,22 @@ def _check_stack(q: QuantizedWeight, rows: RowGroups) -> None:
         raise ValueError(f"the weight must be a stack [{rows.groups}, N, K], not {q.shape}")
 
 
+def _rows_product(call, name: str, t: torch.Tensor, q: QuantizedWeight, rows: RowGroups,
+                  cin: int, cout: int, gather: int, scatter: bool, out, stream) -> torch.Tensor:
+    _check_matrix(name, t, cin, q.dtype, q.packed.device)
+    _check_plan(rows, t.device)
+    y = out if out is not None else torch.zeros(rows.rows, cout, dtype=q.dtype, device=t.device)
+    _check_matrix("out", y, cout, q.dtype, t.device)
+    if gather < 0:
+        raise ValueError("gather must be 0 or the slots per row")
+    if t.shape[0] * max(gather, 1) < rows.rows or y.shape[0] < rows.rows:
+        raise ValueError("fewer rows than the plan has places")
+    with _on(t.device):
+        call(t, _ld(t), t.shape[0], q.packed, q.state, rows.desc, q.shape[1], q.shape[2], gather,
+             int(scatter), y, _ld(y), y.shape[0], stream)
+    return y
+
+
 def gemm_experts(x: torch.Tensor, q: QuantizedWeight, rows: RowGroups, gather: int = 0,
                  scatter: bool = False, out: torch.Tensor | None = None,
                  stream=None) -> torch.Tensor:
@@ -305,16 +323,64 @@ def gemm_experts(x: torch.Tensor, q: QuantizedWeight, rows: RowGroups, gather: i
     ``scatter`` writes row order[i] of the result, else row i.  Rows without a
     group keep what ``out`` holds (zero if it is allocated here)."""
     _check_stack(q, rows)
-    _, N, K = q.shape
+    return _rows_product(bnbx_gemm_nf4_experts, "x", x, q, rows, q.shape[2], q.shape[1], gather,
+                         scatter, out, stream)
+
+
+def gemm_experts_dx(dy: torch.Tensor, q: QuantizedWeight, rows: RowGroups, gather: int = 0,
+                    scatter: bool = False, out: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """dX_i = dY_i . W_hat_g (bnbx_gemm_nf4_experts_dx, the input gradient of
+    gemm_experts; N a multiple of 64): dY [.., N], the result [.., K]; rows are
+    read and written as in gemm_experts."""
+    _check_stack(q, rows)
+    return _rows_product(bnbx_gemm_nf4_experts_dx, "dy", dy, q, rows, q.shape[1], q.shape[2],
+                         gather, scatter, out, stream)
+
+
+def linear_adapters(x: torch.Tensor, q: QuantizedWeight, rows: RowGroups, lora_a: torch.Tensor,
+                    lora_b: torch.Tensor, scale: torch.Tensor, out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y = X . W_hat^T + s_g . (X . A_g^T) . B_g^T with the adapter of each
+    row's group (bnbx_gemm_nf4_adapters): A [groups, r, K], B [groups, N, r] (any
+    strides of whole rows), scale float32 [groups]; rows of no group get the
+    4-bit product alone."""
+    if len(q.shape) != 2:
+        raise ValueError(f"the weight must be [N, K], not {q.shape}")
+    N, K = q.shape
     _check_matrix("x", x, K, q.dtype, q.packed.device)
     _check_plan(rows, x.device)
-    y = out if out is not None else torch.zeros(rows.rows, N, dtype=q.dtype, device=x.device)
+    if x.shape[0] != rows.rows:
+        raise ValueError(f"x has {x.shape[0]} rows, the plan {rows.rows}")
+    if lora_a.dim() != 3 or lora_b.dim() != 3 or lora_a.shape[0] != rows.groups:
+        raise ValueError(f"the adapters must be A [{rows.groups}, r, {K}] and "
+                         f"B [{rows.groups}, {N}, r]")
+    r = lora_a.shape[1]
+    for name, t, shape in (("lora_a", lora_a, (rows.groups, r, K)),
+                           ("lora_b", lora_b, (rows.groups, N, r)),
+                           ("scale", scale, (rows.groups,))):
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {shape}, not {tuple(t.shape)}")
+        if t.dtype != (torch.float32 if name == "scale" else q.dtype):
+            raise TypeError(f"{name}: {t.dtype}")
+        if t.device != x.device or t.stride(-1) != 1 and t.numel() > 1:
+            raise ValueError(f"{name} must be on {x.device} with contiguous rows")
+    y = out if out is not None else torch.empty(rows.rows, N, dtype=q.dtype, device=x.device)
     _check_matrix("out", y, N, q.dtype, x.device)
-    if (gather == 0 and x.shape[0] < rows.rows) or y.shape[0] < rows.rows:
-        raise ValueError("fewer rows than the plan has places")
-    if gather > 0 and x.shape[0] * gather < rows.rows:
-        raise ValueError("fewer rows of x than the plan's slots belong to")
+    if y.shape[0] != rows.rows:
+        raise ValueError(f"out has {y.shape[0]} rows, the plan {rows.rows}")
+    desc = AdaptersDesc(lora_a.data_ptr(), lora_b.data_ptr(), scale.data_ptr(), _row(lora_a),
+                        lora_a.stride(0) if rows.groups > 1 else 0, _row(lora_b),
+                        lora_b.stride(0) if rows.groups > 1 else 0, r)
     with _on(x.device):
-        bnbx_gemm_nf4_experts(x, _ld(x), x.shape[0], q.packed, q.state, rows.desc, N, K, gather,
-                              int(scatter), y, _ld(y), y.shape[0], stream)
+        nbytes = bnbx_gemm_nf4_adapters_workspace_bytes(rows.rows, r)
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        bnbx_gemm_nf4_adapters(x, _ld(x), q.packed, q.state, rows.desc, N, K, desc, y, _ld(y),
+                               workspace, workspace.numel() * workspace.element_size(), stream)
     return y
+
+
+def _row(t: torch.Tensor) -> int:
+    """Row stride of a stack of matrices."""
+    return t.stride(1) if t.shape[1] > 1 else t.shape[2]

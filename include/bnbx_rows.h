@@ -92,6 +92,57 @@ BNBX_ROWS_API int bnbx_gemm_nf4_experts(const uint16_t* x, int64_t ldx, int x_ro
                                         int scatter, uint16_t* y, int64_t ldy, int y_rows,
                                         void* stream);
 
+/* Input gradient of bnbx_gemm_nf4_experts (frozen weights): for place i of
+ * group g,   dX[row_x(i)] = dY[row_y(i)] . W_hat_g,   dY [dy_rows, N], dX
+ * [dx_rows, K], with row_y(i) = order[i] / gather or i and row_x(i) = order[i] or
+ * i as above.  Where the forward gathered with top_k, call with scatter 1: dX
+ * then has a row per slot, and a token's gradient is the sum of its slots' rows.
+ * The other arguments, what is left untouched and the errors as above (lddy for
+ * ldx, lddx for ldy), except: N a multiple of 64, and dY below 2 GiB where
+ * gather is not 0 (else BNBX_E_UNSUPPORTED). */
+BNBX_ROWS_API int bnbx_gemm_nf4_experts_dx(const uint16_t* dy, int64_t lddy, int dy_rows,
+                                           const uint8_t* packed, const bnbx_nf4_state* st,
+                                           const bnbx_row_groups* plan, int N, int K, int gather,
+                                           int scatter, uint16_t* dx, int64_t lddx, int dx_rows,
+                                           void* stream);
+
+/* The adapters of a call, one per group of its plan (host descriptor; device
+ * pointers).  A lower rank than r is held as r with zero rows of A or zero
+ * columns of B. */
+typedef struct {
+  const uint16_t* lora_a; /* adapter g's A [r, K], row j at lora_a + g*stride_a + j*lda;
+                             lda >= K, lda and stride_a % 8 == 0, 16-byte aligned     */
+  const uint16_t* lora_b; /* adapter g's B [N, r], row n at lora_b + g*stride_b + n*ldb;
+                             ldb >= r, ldb and stride_b % 8 == 0, 16-byte aligned     */
+  const float* scale;     /* s_g, float[groups]                                       */
+  int64_t lda, stride_a, ldb, stride_b;
+  int32_t r;              /* a multiple of 16, 16 <= r <= 256                         */
+} bnbx_adapters;
+
+/* Bytes of device workspace bnbx_gemm_nf4_adapters needs for `rows` rows and
+ * rank r; 0 for invalid arguments. */
+BNBX_ROWS_API size_t bnbx_gemm_nf4_adapters_workspace_bytes(int rows, int r);
+
+/* One shared 4-bit linear layer beside the adapters of many requests:
+ *   Y_m = X_m . W_hat^T + s_g . (X_m . A_g^T) . B_g^T   for row m of group g,
+ *   Y_m = X_m . W_hat^T                                 for a row of no group.
+ * X [rows, K] and Y [rows, N] in the requests' own order, rows = plan->rows; the
+ * plan (bnbx_group_rows of the rows' adapter ids) gives each adapter its rows,
+ * any number of them, and must list every row in `order`: a row it does not
+ * list is not written.  Values are of st->compute_dtype; both products
+ * accumulate in fp32, X . A_g^T keeps 16 significant bits, and Y is rounded
+ * once.  An adapter with infinities or NaN reaches its own rows only.
+ *   x, packed, st, N, K  as bnbx_gemm_nf4 (st->n = N * K)
+ *   y          device, row m at y + m*ldy; ldy >= N (written)
+ *   workspace  device, >= bnbx_gemm_nf4_adapters_workspace_bytes(...) bytes,
+ *              16-byte aligned; scratch
+ * Errors: as bnbx_gemm_nf4_experts, and BNBX_E_WORKSPACE. */
+BNBX_ROWS_API int bnbx_gemm_nf4_adapters(const uint16_t* x, int64_t ldx, const uint8_t* packed,
+                                         const bnbx_nf4_state* st, const bnbx_row_groups* plan,
+                                         int N, int K, const bnbx_adapters* adapters, uint16_t* y,
+                                         int64_t ldy, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
 #ifdef __cplusplus
 }
 #endif
