@@ -65,11 +65,18 @@ hipError_t launch_rows_lora_down(const RowsGemm& a, const LoraDown& d, bool f16,
 hipError_t launch_rows_stream(const RowsGemm& a, int quant_type, bool f16, int cus,
                               hipStream_t stream);
 
+// Tiled form: row tiles of 256 places (bnbx_rows_gemm.hip), and with a
+// low-rank term (bnbx_rows_gemm_lora.hip).  hipErrorNotSupported where X does
+// not fit 32-bit offsets.
+hipError_t launch_rows_gemm(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream);
+hipError_t launch_rows_gemm_lora(const RowsGemm& a, int quant_type, bool f16,
+                                 hipStream_t stream);
+
 // dX_i = dY_i . W_hat_g: x is dY [x_rows, N], y is dX [y_rows, K]; N a
 // multiple of 64 (bnbx_rows_dx.hip).
 hipError_t launch_rows_dx(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream);
 
 // Compute units of the current device.
-int device_cus();
+int rows_cus();
 
 }  // namespace bnbx

@@ -1,5 +1,6 @@
 // C entry points of libbnbx_rows (declared in include/bnbx_rows.h): argument
 // checks on the host and kernel launches.
+#include <stdlib.h>
 #include "../../include/bnbx_rows.h"
 #include "bnbx_checks.hpp"
 #include "bnbx_rows.hpp"
@@ -61,6 +62,24 @@ RowsGemm rows_gemm(const uint16_t* x, int64_t ldx, int x_rows, const uint8_t* pa
   return a;
 }
 
+// Rows a group on average (an upper bound on what the launch will find).
+int mean_rows(const RowsGemm& a) {
+  const int groups = a.offsets == nullptr ? 1 : (a.groups < a.rows ? a.groups : a.rows);
+  return (a.rows + groups - 1) / groups;
+}
+
+// The products of both operators: tiles of 256 places for many rows a
+// group, the streaming form for few (and for an X past 32-bit offsets).
+hipError_t launch_rows(const RowsGemm& a, int quant_type, bool f16, int cus, hipStream_t hs) {
+  static int thr = getenv("BNBX_T") ? atoi(getenv("BNBX_T")) : 128;
+  if (mean_rows(a) > thr) {
+    const hipError_t e = a.lora.offsets != nullptr ? launch_rows_gemm_lora(a, quant_type, f16, hs)
+                                                   : launch_rows_gemm(a, quant_type, f16, hs);
+    if (e != hipErrorNotSupported) return e;
+  }
+  return launch_rows_stream(a, quant_type, f16, cus, hs);
+}
+
 int rows_status(hipError_t e) {
   return e == hipErrorNotSupported ? BNBX_E_UNSUPPORTED : hip_status(e);
 }
@@ -104,8 +123,8 @@ int bnbx_gemm_nf4_experts(const uint16_t* x, int64_t ldx, int x_rows, const uint
   if (plan->rows == 0 || x_rows == 0 || y_rows == 0) return BNBX_OK;
   const RowsGemm a = rows_gemm(x, ldx, x_rows, packed, st, plan, N, K, gather, scatter, y, ldy,
                                y_rows);
-  return rows_status(launch_rows_stream(a, st->quant_type, st->compute_dtype == BNBX_DTYPE_F16,
-                                        device_cus(), (hipStream_t)stream));
+  return rows_status(launch_rows(a, st->quant_type, st->compute_dtype == BNBX_DTYPE_F16,
+                                 rows_cus(), (hipStream_t)stream));
 }
 
 int bnbx_gemm_nf4_experts_dx(const uint16_t* dy, int64_t lddy, int dy_rows,
@@ -151,7 +170,7 @@ int bnbx_gemm_nf4_adapters(const uint16_t* x, int64_t ldx, const uint8_t* packed
   if (workspace == nullptr || workspace_bytes < need) return BNBX_E_WORKSPACE;
   if (!aligned(workspace, 16)) return BNBX_E_ALIGN;
   const bool f16 = st->compute_dtype == BNBX_DTYPE_F16;
-  const int cus = device_cus();
+  const int cus = rows_cus();
   hipStream_t hs = (hipStream_t)stream;
   RowsGemm a = rows_gemm(x, ldx, plan->rows, packed, st, plan, N, K, 1, 1, y, ldy, plan->rows);
   const LoraDown d{plan->offsets, plan->groups, ad->r, ad->lora_a, ad->lda, ad->stride_a,
@@ -162,7 +181,7 @@ int bnbx_gemm_nf4_adapters(const uint16_t* x, int64_t ldx, const uint8_t* packed
   a.groups = 1;
   a.lora = LoraRows{plan->offsets, plan->groups, ad->r, (const uint16_t*)workspace, ad->lora_b,
                     ad->ldb, ad->stride_b};
-  return rows_status(launch_rows_stream(a, st->quant_type, f16, cus, hs));
+  return rows_status(launch_rows(a, st->quant_type, f16, cus, hs));
 }
 
 }  // extern "C"

@@ -397,7 +397,7 @@ hipError_t launch_rows_stream(const RowsGemm& a, int quant_type, bool f16, int c
   return launch_one<4, 2, 2, 2>(a, quant_type, f16, stream);
 }
 
-int device_cus() {
+int rows_cus() {
   static int n = 0;
   if (n == 0) {
     int dev = 0, v = 0;
