@@ -20,7 +20,8 @@ SOURCES = ["bnbx_api.hip", "bnbx_tables.hip", "bnbx_quant.hip", "bnbx_dequant.hi
            "bnbx_gemm_dx.hip", "bnbx_lora.hip", "bnbx_probe.hip"]
 ROWS_SOURCES = ["bnbx_rows_api.hip", "bnbx_tables.hip", "bnbx_rows_group.hip",
                 "bnbx_rows_stream.hip", "bnbx_rows_dx.hip",
-                "bnbx_rows_lora.hip", "bnbx_rows_gemm.hip", "bnbx_rows_gemm_lora.hip"]
+                "bnbx_rows_lora.hip", "bnbx_rows_gemm.hip", "bnbx_rows_gemm_lora.hip",
+                "bnbx_rows_dx_stream.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

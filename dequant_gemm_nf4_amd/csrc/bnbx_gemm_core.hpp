@@ -306,10 +306,10 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(
   __shared__ int yrow[ROWS ? BM : 1];   // the tile's rows of Y (ROWS)
   if constexpr (ROWS) {
     const RowTiles<BM> tiles{rows.offsets, rows.groups, rows.rows};
-    const int64_t id = xcd_item((int64_t)tiles.count() * tiles_n);
+    const int id = xcd_item(tiles.count() * tiles_n);
     if (id < 0) return;
-    const RowTile rt = tiles.find(__builtin_amdgcn_readfirstlane((int)(id / tiles_n)));
-    n0 = __builtin_amdgcn_readfirstlane((int)(id % tiles_n)) * BN;
+    const RowTile rt = tiles.find(__builtin_amdgcn_readfirstlane(id / tiles_n));
+    n0 = __builtin_amdgcn_readfirstlane(id % tiles_n) * BN;
     m0 = rt.r0;
     M = rt.r1;
     const int64_t blk0 = (int64_t)rt.g * N * (K >> 6);

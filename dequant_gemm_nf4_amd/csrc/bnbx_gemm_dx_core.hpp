@@ -103,10 +103,10 @@ __global__ __launch_bounds__(kThreads) void gemm_dx_kernel(
   __shared__ int yrow[ROWS ? TM : 1];   // the tile's rows of dX (ROWS)
   if constexpr (ROWS) {
     const RowTiles<TM> tiles{rows.offsets, rows.groups, rows.rows};
-    const int64_t id = xcd_item((int64_t)tiles.count() * tiles_k);
+    const int id = xcd_item(tiles.count() * tiles_k);
     if (id < 0) return;
-    const RowTile rt = tiles.find(__builtin_amdgcn_readfirstlane((int)(id / tiles_k)));
-    k0 = __builtin_amdgcn_readfirstlane((int)(id % tiles_k)) * TK;
+    const RowTile rt = tiles.find(__builtin_amdgcn_readfirstlane(id / tiles_k));
+    k0 = __builtin_amdgcn_readfirstlane(id % tiles_k) * TK;
     m0 = rt.r0;
     M = rt.r1;
     const int64_t blk0 = (int64_t)rt.g * N * (K >> 6);

@@ -76,6 +76,9 @@ hipError_t launch_rows_gemm_lora(const RowsGemm& a, int quant_type, bool f16,
 // multiple of 64 (bnbx_rows_dx.hip).
 hipError_t launch_rows_dx(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream);
 
+// The same over few rows a group (bnbx_rows_dx_stream.hip).
+hipError_t launch_rows_dx_stream(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream);
+
 // Compute units of the current device.
 int rows_cus();
 

@@ -95,13 +95,14 @@ struct RowTiles {
   }
 };
 
-// This workgroup's number among `total` items, XCD-aware: workgroup b runs on
+// This workgroup's number among `total` items (no more than the grid has
+// workgroups), XCD-aware: workgroup b runs on
 // XCD b % 8, and consecutive items go to one XCD (they share weights or rows
 // in its L2).  -1: nothing to do.
-__device__ __forceinline__ int64_t xcd_item(int64_t total) {
-  const int64_t per = (total + kXcds - 1) / kXcds;
-  const int64_t slot = blockIdx.x / kXcds, xcd = blockIdx.x % kXcds;
-  const int64_t id = xcd * per + slot;
+__device__ __forceinline__ int xcd_item(int total) {
+  const int per = (total + kXcds - 1) / kXcds;
+  const int slot = (int)(blockIdx.x / kXcds), xcd = (int)(blockIdx.x % kXcds);
+  const int id = xcd * per + slot;
   return slot < per && id < total ? id : -1;
 }
 
@@ -117,6 +118,25 @@ __device__ __forceinline__ int x_row_of(const RowsGemm& a, int place) {
 __device__ __forceinline__ int y_row_of(const RowsGemm& a, int place) {
   const int row = a.scatter ? a.order[place] : place;
   return row >= 0 && row < a.y_rows ? row : -1;
+}
+
+// The byte -> fp32 level pair table in LDS (64 KB at LDS offset 0): entry e,
+// (level of the high nibble, level of the low one), in 32 copies side by side,
+// 256 bytes an entry, so that one v_perm forms a read's address and b64 reads
+// never conflict.
+constexpr int kLutBytes = 256 * 256;
+__device__ __forceinline__ void lut_build(unsigned char* lds, const LevelTable& lv, int threads) {
+  const int lvl = level_lanes(lv);
+  for (int e = threadIdx.x; e < kLutBytes / 16; e += threads) {
+    const uint32_t b = (uint32_t)e / 16u;
+    const float hi = level_lookup(lvl, b >> 4), lo = level_lookup(lvl, b & 15u);
+    *(float4*)(lds + 16 * e) = make_float4(hi, lo, hi, lo);
+  }
+}
+// The pair of byte `e` of d; lcol = 8 (lane % 32).
+__device__ __forceinline__ float2 lut_pair(const unsigned char* lds, uint32_t d, uint32_t lcol,
+                                           int e) {
+  return *(const float2*)(lds + perm(d, lcol, 0x0c0c0000u | ((4u + e) << 8)));
 }
 
 // Eight binary16 values as two bf16 operands, hi + lo, exactly: binary16 has

@@ -32,11 +32,11 @@ __global__ __launch_bounds__(kThreads) void rows_lora_down_kernel(RowsGemm a, Lo
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const RowTiles<kTile> tiles{d.offsets, d.adapters, a.rows};
   const int nt = tiles.count();
-  const int64_t id = xcd_item((int64_t)nt * rank_tiles);
+  const int id = xcd_item(nt * rank_tiles);
   if (id < 0) return;
   // the rank tiles of one row tile are neighbours: they share X
-  const RowTile tile = tiles.find(__builtin_amdgcn_readfirstlane((int)(id / rank_tiles)));
-  const int c0 = __builtin_amdgcn_readfirstlane((int)(id % rank_tiles)) * 16 * RT;
+  const RowTile tile = tiles.find(__builtin_amdgcn_readfirstlane(id / rank_tiles));
+  const int c0 = __builtin_amdgcn_readfirstlane(id % rank_tiles) * 16 * RT;
 
   unsigned char* const stage = stages[wave];
   const int lr = lane >> 2, lp = lane & 3;   // load layout: row, piece

@@ -16,13 +16,23 @@
 // q of X takes k = 64 q + 8 m.  So D has the weight rows down the values
 // (n = 4 q + v) and the places across the lanes (i = lane % 16).
 //
+// Dequant.  Up to 32 places a tile (LUT): a byte -> fp32 level pair table in
+// LDS, 32 copies side by side so that its b64 reads never conflict (with 16
+// copies half of all LDS cycles were conflicts), 256 bytes an entry so that
+// one v_perm forms an address; two products and one conversion a byte, 2.3
+// vector instructions a weight in all.  64 places: the 16 products of a block
+// as register byte tables (decode8, 3.7 a weight), because LDS then serves the
+// operands of X and its table would leave one workgroup a CU.
+//
 // X goes through LDS, double-buffered, in slices of 256 k: 32 chunks of 16
 // bytes a row, chunk c of row r in slot c ^ (r % 16), so that 16 lanes reading
 // one chunk of 16 rows hit 64 banks.
 //
 // WN waves of a workgroup take different weight rows (and share X), WK waves
 // split K slice by slice; their sums meet in LDS in wave order.  WK > 1 is for
-// launches whose weight rows alone give the GPU too few waves.
+// launches whose weight rows alone give the GPU too few waves.  With WN = 1 no
+// wave shares X and each loads its operands straight from memory, only the
+// lanes whose place exists (one token: 4 of 64).
 #include "bnbx_rows_device.hpp"
 #include "bnbx_tab16.hpp"
 
@@ -30,22 +40,27 @@ namespace bnbx {
 namespace {
 
 constexpr int kSlice = 256;          // k per unit
-constexpr int kAhead = 2;            // units loaded ahead
 
-template <int RB, int NB, int WN, int WK, bool DQ, bool F16>
+
+template <int RB, int NB, int WN, int WK, bool LUT, int DQ, bool F16>
 __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, int tiles_n,
                                                                   LevelTable lv) {
-  constexpr int TM = 16 * RB, TN = 16 * NB * WN;
-  constexpr int kXBuf = WK * TM * kSlice;            // 16-bit elements
-  constexpr int kXLoads = RB * 8 / WN > 0 ? RB * 8 / WN : 1;   // 1 KB loads of X a wave
+  constexpr int TM = 16 * RB, TN = 16 * NB * WN, kThreads = WN * WK * 64;
+  constexpr int kAhead = 2;   // units loaded ahead, per 16 weight rows
+  constexpr bool DIRECT = WN == 1, DYN = DQ == kDqDynamic;
+  constexpr int kXBuf = DIRECT ? 0 : WK * TM * kSlice;   // 16-bit elements
+  constexpr int kXLoads = DIRECT ? 1 : RB * 8 / WN > 0 ? RB * 8 / WN : 1;   // 1 KB loads a wave
   constexpr int kStages = WN * WK * 2048;
   constexpr int kRedBytes = (WK - 1) * WN * RB * NB * 1024;
-  constexpr int kLds = 2 * kXBuf * 2 + kStages;
-  static_assert(kRedBytes <= kLds, "the partial sums reuse X and the stages");
-  static_assert(RB * 8 % WN == 0 || WN > RB * 8, "X loads split evenly over the waves");
-  __shared__ __attribute__((aligned(16))) unsigned char smem[kLds];
-  __shared__ float dmap[256];
+  // LDS: the byte table (at offset 0: its addresses are v_perm results), X,
+  // the waves' stages, the dynamic map; the partial sums reuse all of it.
+  constexpr int kLut = LUT ? kLutBytes : 0;
+  constexpr int kUsed = kLut + 2 * kXBuf * 2 + kStages + (DYN ? 1024 : 0);
+  constexpr int kLds = kUsed > kRedBytes ? kUsed : kRedBytes;
+  static_assert(DIRECT || RB * 8 % WN == 0 || WN > RB * 8, "X loads split evenly");
+  __shared__ __attribute__((aligned(256))) unsigned char smem[kLds];
 
+  float* const dmap = (float*)(smem + kLut + 2 * kXBuf * 2 + kStages);
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wn = wave % WN, wk = wave / WN;
@@ -54,17 +69,14 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
 
   const RowTiles<TM> tiles{a.offsets, a.groups, a.rows};
   const int nt = tiles.count();
-  const int64_t id = xcd_item((int64_t)nt * tiles_n);
+  const int id = xcd_item(nt * tiles_n);   // fits: the grid covers it
   if (id < 0) return;
   // row tiles of one group and the same weight rows are neighbours: they
   // meet in one L2
-  const int tn = __builtin_amdgcn_readfirstlane((int)(id / nt));
-  const RowTile tile = tiles.find(__builtin_amdgcn_readfirstlane((int)(id % nt)));
+  const int tn = __builtin_amdgcn_readfirstlane((int)((uint32_t)id / (uint32_t)nt));
+  const RowTile tile = tiles.find(id - tn * nt);
   const int n0 = tn * TN + wn * 16 * NB;
 
-  const bool dyn = a.double_quant == kDqDynamic;
-  if (DQ && dyn)
-    for (int e = t; e < 256; e += WN * WK * 64) dmap[e] = kDynMapDev.v[e];
   const float mu = DQ ? *a.mean : 0.0f;
   const uint32_t rowK2 = (uint32_t)a.K >> 1, nkb = (uint32_t)a.K >> 6;
   const int nslices = (a.K + kSlice - 1) / kSlice;
@@ -79,6 +91,9 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   const uint32_t grem = (uint32_t)(blk0 & 255);   // the group's first block in its scale group
   const rsrc_t rg = make_rsrc(DQ ? a.absmax2 + (blk0 >> 8) : nullptr,
                               DQ ? (grem + nblocks + 255u) / 256u * 4u : 0u);
+
+  // Slice of step s (none past the last step).
+  auto slice_of = [&](int s) { return s < nsteps ? s * WK + wk : nslices; };
 
   struct Unit {
     u32x4_t w[2];
@@ -114,7 +129,7 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
     const bool bin = brow[j] != kFar && 4u * (uint32_t)slice + (uint32_t)q < nkb;
     float sc;
     if (DQ) {
-      if (dyn) {
+      if (DYN) {
         const float prod = dmap[u.q & 0xffu] * u.s;
         sc = prod + mu;
       } else {
@@ -131,43 +146,76 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
 #pragma unroll
   for (int p = 0; p < kAhead; ++p)
 #pragma unroll
-    for (int j = 0; j < NB; ++j) load_unit(un[p][j], j, p * WK + wk);
+    for (int j = 0; j < NB; ++j) load_unit(un[p][j], j, slice_of(p));
 
-  // X: the WN waves of one K part copy its slice, 2 rows an instruction
-  // (lane l: row l / 32, slot l % 32).  Rows past the tile repeat its first
-  // row (their results are never stored); chunks past K repeat chunk 0 (their
-  // operands are zeroed below).
-  uint16_t* const xs = (uint16_t*)smem;
-  unsigned char* const stage = smem + 2 * kXBuf * 2 + wave * 2048;
-  const bool xwave = WN <= RB * 8 || wn < RB * 8;
+  if (LUT) lut_build(smem, lv, kThreads);
+  if (DYN)
+    for (int e = t; e < 256; e += kThreads) dmap[e] = kDynMapDev.v[e];
+
+  unsigned char* const stage = smem + kLut + 2 * kXBuf * 2 + wave * 2048;
+  auto barrier = [] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+
+  // X through LDS: the WN waves of one K part copy its slice, 2 rows an
+  // instruction (lane l: row l / 32, slot l % 32).  Rows past the tile repeat
+  // its first row (their results are never stored); chunks past K are zeros.
+  uint16_t* const xs = (uint16_t*)(smem + kLut);
   const uint16_t* xp[kXLoads];
   int xk[kXLoads];
   uint32_t xslot[kXLoads];
-#pragma unroll
-  for (int i = 0; i < kXLoads; ++i) {
-    const int row = 2 * (wn * kXLoads + i) + (lane >> 5);
-    const int place = tile.r0 + row < tile.r1 ? tile.r0 + row : tile.r0;
-    int xr = xwave ? x_row_of(a, place) : 0;
-    xr = xr < 0 ? 0 : xr;
-    xp[i] = a.x + (int64_t)xr * a.ldx;
-    xk[i] = 8 * ((lane & 31) ^ (row & 15));
-    xslot[i] = (uint32_t)((wk * TM + row) * kSlice + 8 * (lane & 31));
-  }
   u32x4_t xv[kXLoads];
+  if (!DIRECT) {
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i) {
+      // more waves than pairs of rows: two waves copy the same rows
+      const int row = (2 * (wn * kXLoads + i) + (lane >> 5)) % TM;
+      const int place = tile.r0 + row < tile.r1 ? tile.r0 + row : tile.r0;
+      int xr = x_row_of(a, place);
+      xr = xr < 0 ? 0 : xr;
+      xp[i] = a.x + (int64_t)xr * a.ldx;
+      xk[i] = 8 * ((lane & 31) ^ (row & 15));
+      xslot[i] = (uint32_t)((wk * TM + row) * kSlice + 8 * (lane & 31));
+    }
+  }
   auto load_x = [&](int slice) {
-    if (!xwave) return;
+    if (DIRECT) return;
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i) {
       const int k = slice * kSlice + xk[i];
       xv[i] = *(const u32x4_t*)(xp[i] + (k < a.K ? k : 0));
     }
   };
-  auto put_x = [&](int buf) {
-    if (!xwave) return;
+  auto put_x = [&](int buf, int slice) {
+    if (DIRECT) return;
+    const bool tail = (slice + 1) * kSlice > a.K;   // uniform
 #pragma unroll
-    for (int i = 0; i < kXLoads; ++i) *(u32x4_t*)(xs + buf * kXBuf + xslot[i]) = xv[i];
+    for (int i = 0; i < kXLoads; ++i) {
+      if (tail && slice * kSlice + xk[i] >= a.K) xv[i] = u32x4_t{0u, 0u, 0u, 0u};
+      *(u32x4_t*)(xs + buf * kXBuf + xslot[i]) = xv[i];
+    }
   };
-  auto barrier = [] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+  // X straight into operands (DIRECT): lane (q, r) reads its chunks of place
+  // r's row, if there is one; zeros past K and for places past the tile.
+  const uint16_t* dp[DIRECT ? RB : 1];
+  u32x4_t dx[DIRECT ? RB : 1][8];
+  if (DIRECT) {
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const int place = tile.r0 + 16 * i + r;
+      const int xr = place < tile.r1 ? x_row_of(a, place) : -1;
+      dp[i] = xr >= 0 ? a.x + (int64_t)xr * a.ldx + 64 * q : nullptr;
+    }
+  }
+  auto load_direct = [&](int slice) {
+    if (!DIRECT) return;
+    const bool kin = 4u * (uint32_t)slice + (uint32_t)q < nkb;
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        dx[i][m] = u32x4_t{0u, 0u, 0u, 0u};
+        if (dp[i] != nullptr && kin) dx[i][m] = *(const u32x4_t*)(dp[i] + slice * kSlice + 8 * m);
+      }
+  };
 
   // Stage slots: piece p (16 bytes) of row w at slot 8 w + (p ^ f(w)), free of
   // bank conflicts both ways.
@@ -181,55 +229,121 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
 #pragma unroll
     for (int i = 0; i < RB; ++i) acc[j][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
+  const uint32_t lcol = 8u * (uint32_t)(lane & 31);
+  // A unit in the MFMA layout: block q of row r, with its scale (or, for 64
+  // places, its table).
+  struct Op {
+    u32x4_t w[2];
+    float sc;
+  };
+  auto turn = [&](Op& o, Unit& u, int j, int s) {
+    o.sc = scale_of(u, j, slice_of(s));
+    *(u32x4_t*)(stage + ws0) = u.w[0];
+    *(u32x4_t*)(stage + (ws0 ^ 64u)) = u.w[1];
+    o.w[0] = *(const u32x4_t*)(stage + rs0);
+    o.w[1] = *(const u32x4_t*)(stage + (rs0 ^ 16u));
+    load_unit(u, j, slice_of(s + kAhead));
+  };
+  Op op[NB];
+  // Step s: `u` holds step s + 1's units, turned while step s multiplies.
+  // (With register tables, step s's own: the turned ones would cost registers
+  // that the accumulators need.)
   auto step = [&](Unit (&u)[NB], int s) {
-    const int slice = s * WK + wk;
-    Tab16 tab[NB];
+    if constexpr (!LUT)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) turn(op[j], u[j], j, s);
+    Tab16 tab[LUT ? 1 : NB];
     u32x4_t w[NB][2];
+    float sc[NB];
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      tab[j] = make_tab16_any<F16>(lv, scale_of(u[j], j, slice));
-      *(u32x4_t*)(stage + ws0) = u[j].w[0];
-      *(u32x4_t*)(stage + (ws0 ^ 64u)) = u[j].w[1];
-      w[j][0] = *(const u32x4_t*)(stage + rs0);
-      w[j][1] = *(const u32x4_t*)(stage + (rs0 ^ 16u));
-      load_unit(u[j], j, (s + kAhead) * WK + wk);
+      if constexpr (!LUT) tab[j] = make_tab16_any<F16>(lv, op[j].sc);
+      sc[j] = op[j].sc;
+      w[j][0] = op[j].w[0];
+      w[j][1] = op[j].w[1];
     }
     const uint16_t* xb = xs + (s & 1) * kXBuf + wk * TM * kSlice;
-    const bool tail = (slice + 1) * kSlice > a.K;   // uniform
-    const bool kin = 4u * (uint32_t)slice + (uint32_t)q < nkb;
+    if constexpr (LUT) {
+      // Table reads (and X) of MFMA m + 1 go out before the products of m.
+      float2 l2[2][NB][4];
+      u32x4_t xo[2][RB];
+      auto look = [&](int m) {
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      u32x4_t xo[RB];
+        for (int j = 0; j < NB; ++j) {
+          const uint32_t d = w[j][m >> 2][m & 3];
 #pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        xo[i] = *(const u32x4_t*)(xb + (16 * i + r) * kSlice + 8 * ((8 * q + m) ^ r));
-        if (tail && !kin) xo[i] = u32x4_t{0u, 0u, 0u, 0u};
+          for (int e = 0; e < 4; ++e) {
+            l2[m & 1][j][e] = lut_pair(smem, d, lcol, e);
+          }
+        }
+        if (!DIRECT)
+#pragma unroll
+          for (int i = 0; i < RB; ++i)
+            xo[m & 1][i] =
+                *(const u32x4_t*)(xb + (16 * i + r) * kSlice + 8 * ((8 * q + m) ^ r));
+      };
+      look(0);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) turn(op[j], u[j], j, s + 1);
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        if (m < 7) look(m + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          u32x4_t wo;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            wo[e] = pack16x2<F16>(l2[m & 1][j][e].x * sc[j], l2[m & 1][j][e].y * sc[j]);
+#pragma unroll
+          for (int i = 0; i < RB; ++i)
+            acc[j][i] = mfma_16x16x32<F16>(wo, DIRECT ? dx[DIRECT ? i : 0][m] : xo[m & 1][i],
+                                           acc[j][i]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
+    } else {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        uint32_t o[4];
-        decode8(w[j][m >> 2][m & 3], tab[j], o);
-        const u32x4_t wo = {o[0], o[1], o[2], o[3]};
+      for (int m = 0; m < 8; ++m) {
+        u32x4_t xo[RB];
 #pragma unroll
-        for (int i = 0; i < RB; ++i) acc[j][i] = mfma_16x16x32<F16>(wo, xo[i], acc[j][i]);
+        for (int i = 0; i < RB; ++i)
+          xo[i] = DIRECT ? dx[DIRECT ? i : 0][m]
+                         : *(const u32x4_t*)(xb + (16 * i + r) * kSlice + 8 * ((8 * q + m) ^ r));
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          uint32_t o[4];
+          decode8(w[j][m >> 2][m & 3], tab[j], o);
+          const u32x4_t wo = {o[0], o[1], o[2], o[3]};
+#pragma unroll
+          for (int i = 0; i < RB; ++i) acc[j][i] = mfma_16x16x32<F16>(wo, xo[i], acc[j][i]);
+        }
       }
     }
   };
 
-  load_x(wk);
-  put_x(0);
+  load_x(slice_of(0));
+  load_direct(slice_of(0));
+  put_x(0, slice_of(0));
   barrier();
-  for (int s = 0; s < nsteps; s += kAhead) {
+  if (LUT)
 #pragma unroll
-    for (int p = 0; p < kAhead; ++p) {
-      if (s + p < nsteps) {
-        if (s + p + 1 < nsteps) load_x((s + p + 1) * WK + wk);
-        step(un[p], s + p);
-        if (s + p + 1 < nsteps) put_x((s + p + 1) & 1);
-        barrier();
-      }
-    }
+    for (int j = 0; j < NB; ++j) turn(op[j], un[0][j], j, 0);
+  // No branch around a load: the compiler's waits count the loads issued
+  // since, and would wait for all of them where it cannot tell how many.
+  auto advance = [&](Unit (&u)[NB], int s) {
+    load_x(slice_of(s + 1));
+    step(u, s);
+    load_direct(slice_of(s + 1));
+    put_x((s + 1) & 1, slice_of(s + 1));
+    if (!DIRECT) barrier();
+  };
+  // (Pairs of steps; a step past the last one multiplies zeros.)
+  for (int s = 0; s < nsteps; s += 2) {
+    advance(un[LUT ? 1 : 0], s);
+    advance(un[LUT ? 0 : 1], s + 1);
   }
+  if (DIRECT) barrier();
 
   // Low-rank term: the adapters whose places meet the tile, each in steps of
   // 32 ranks, shared out over the WK waves.  XA's two planes and, for fp16, B
@@ -300,8 +414,8 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
     }
   }
 
-  // The K parts' sums, in wave order (X and the stages are free: every wave
-  // has passed the last barrier).
+  // The K parts' sums, in wave order (all of smem is free: every wave has
+  // passed the last barrier).
   if (WK > 1) {
     f32x4_t* const red = (f32x4_t*)smem;
     if (wk > 0) {
@@ -350,7 +464,7 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   }
 }
 
-template <int RB, int NB, int WN, int WK>
+template <int RB, int NB, int WN, int WK, bool LUT>
 hipError_t launch_one(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream) {
   constexpr int TM = 16 * RB, TN = 16 * NB * WN;
   const int tiles_n = (a.N + TN - 1) / TN;
@@ -362,12 +476,15 @@ hipError_t launch_one(const RowsGemm& a, int quant_type, bool f16, hipStream_t s
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(WN * WK * 64), 0, stream, a, tiles_n,
                        lv);
   };
-  if (a.double_quant != kDqNone) {
-    if (f16) go(rows_stream_kernel<RB, NB, WN, WK, true, true>);
-    else go(rows_stream_kernel<RB, NB, WN, WK, true, false>);
+  if (a.double_quant == kDqNone) {
+    if (f16) go(rows_stream_kernel<RB, NB, WN, WK, LUT, kDqNone, true>);
+    else go(rows_stream_kernel<RB, NB, WN, WK, LUT, kDqNone, false>);
+  } else if (a.double_quant == kDqLinear) {
+    if (f16) go(rows_stream_kernel<RB, NB, WN, WK, LUT, kDqLinear, true>);
+    else go(rows_stream_kernel<RB, NB, WN, WK, LUT, kDqLinear, false>);
   } else {
-    if (f16) go(rows_stream_kernel<RB, NB, WN, WK, false, true>);
-    else go(rows_stream_kernel<RB, NB, WN, WK, false, false>);
+    if (f16) go(rows_stream_kernel<RB, NB, WN, WK, LUT, kDqDynamic, true>);
+    else go(rows_stream_kernel<RB, NB, WN, WK, LUT, kDqDynamic, false>);
   }
   return hipGetLastError();
 }
@@ -382,19 +499,22 @@ hipError_t launch_rows_stream(const RowsGemm& a, int quant_type, bool f16, int c
   // Row tiles the launch is likely to have, times 16-row weight slabs.
   const int64_t tm = 16 * rb;
   const int64_t slabs = (int64_t)groups * ((mean_rows + tm - 1) / tm) * ((a.N + 15) / 16);
-  const int64_t waves = slabs / (rb == 4 ? 2 : 1);
-  const int64_t full = (int64_t)cus * 16;
+  // Few slabs (16 weight rows): one workgroup a slab, all its waves on K, up
+  // to two workgroups a CU; then 8 slabs a workgroup and K in two, while one
+  // round of them does; else 16 slabs a workgroup.  Measured on stacks of
+  // 4096 x 4096 and 14336 x 4096 in us: 512 slabs 17.7 / 22.4 / 35.5; 2048
+  // slabs 42.1 / 25.2 / 37.5; 7168 slabs 134 / 93 / 79.
   if (rb == 1) {
-    if (waves >= full) return launch_one<1, 1, 8, 1>(a, quant_type, f16, stream);
-    if (waves * 4 >= full) return launch_one<1, 1, 2, 4>(a, quant_type, f16, stream);
-    return launch_one<1, 1, 1, 8>(a, quant_type, f16, stream);
+    if (slabs <= 2 * (int64_t)cus) return launch_one<1, 1, 1, 8, true>(a, quant_type, f16, stream);
+    if (slabs <= 8 * (int64_t)cus) return launch_one<1, 1, 8, 2, true>(a, quant_type, f16, stream);
+    return launch_one<1, 1, 16, 1, true>(a, quant_type, f16, stream);
   }
   if (rb == 2) {
-    if (waves >= full) return launch_one<2, 1, 8, 1>(a, quant_type, f16, stream);
-    return launch_one<2, 1, 2, 4>(a, quant_type, f16, stream);
+    if (slabs <= 2 * (int64_t)cus) return launch_one<2, 1, 1, 8, true>(a, quant_type, f16, stream);
+    if (slabs <= 8 * (int64_t)cus) return launch_one<2, 1, 8, 1, true>(a, quant_type, f16, stream);
+    return launch_one<2, 1, 16, 1, true>(a, quant_type, f16, stream);
   }
-  if (waves * 2 >= full) return launch_one<4, 2, 4, 1>(a, quant_type, f16, stream);
-  return launch_one<4, 2, 2, 2>(a, quant_type, f16, stream);
+  return launch_one<4, 1, 8, 1, false>(a, quant_type, f16, stream);
 }
 
 int rows_cus() {

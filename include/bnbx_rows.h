@@ -98,8 +98,7 @@ BNBX_ROWS_API int bnbx_gemm_nf4_experts(const uint16_t* x, int64_t ldx, int x_ro
  * i as above.  Where the forward gathered with top_k, call with scatter 1: dX
  * then has a row per slot, and a token's gradient is the sum of its slots' rows.
  * The other arguments, what is left untouched and the errors as above (lddy for
- * ldx, lddx for ldy), except: N a multiple of 64, and dY below 2 GiB where
- * gather is not 0 (else BNBX_E_UNSUPPORTED). */
+ * ldx, lddx for ldy), except: N a multiple of 64 (else BNBX_E_UNSUPPORTED). */
 BNBX_ROWS_API int bnbx_gemm_nf4_experts_dx(const uint16_t* dy, int64_t lddy, int dy_rows,
                                            const uint8_t* packed, const bnbx_nf4_state* st,
                                            const bnbx_row_groups* plan, int N, int K, int gather,
