@@ -17,9 +17,12 @@
 // neighbouring columns of dX.
 //
 // Waves share nothing but the table: the WS waves of a workgroup own the same
-// 128 columns and take every WS-th unit of 32 rows; dY comes straight into
-// operands (lane (q, r): place r, 16 bytes).  The unit's 64 block scales are
-// formed one a lane and turned through 256 bytes of LDS.  At the end the
+// 128 columns and take every WS-th unit of 32 rows.  dY is loaded quad-coalesced
+// (lane x: 16 bytes of place x / 4: 22 cycles of the CU's address path a load,
+// against 67 with every lane on a line of its own, which bound the kernel) and
+// turned to lane (q, r): place r, 16 bytes, through a 1 KB stage per wave.  The
+// unit's 64 block scales are formed one a lane and turned through 256 bytes of
+// LDS.  At the end the
 // accumulators meet in LDS, pairwise in a fixed tree.
 #include "bnbx_rows_device.hpp"
 
@@ -27,6 +30,7 @@ namespace bnbx {
 namespace {
 
 constexpr int kCols = 128, kUnit = 32;
+constexpr int kAhead = 2;   // units loaded ahead
 
 template <int RB, int WS, int DQ, bool F16>
 __global__ __launch_bounds__(WS * 64) void rows_dx_stream_kernel(RowsGemm a, int tiles_k,
@@ -34,14 +38,15 @@ __global__ __launch_bounds__(WS * 64) void rows_dx_stream_kernel(RowsGemm a, int
   constexpr int TM = 16 * RB;
   constexpr bool DYN = DQ == kDqDynamic;
   constexpr int kAcc = 8 * RB;                      // f32x4 a lane
-  // LDS: the byte table (at offset 0), two scale sets a wave, the dynamic
-  // map; the tree of sums reuses all of it.
-  constexpr int kScl = kLutBytes, kMap = kScl + WS * 512;
+  // LDS: the byte table (at offset 0), two scale sets and a stage a wave, the
+  // dynamic map; the tree of sums reuses all of it.
+  constexpr int kScl = kLutBytes, kStage = kScl + WS * 512, kMap = kStage + WS * 1024;
   constexpr int kUsed = kMap + (DYN ? 1024 : 0), kRed = WS / 2 * kAcc * 1024;
   __shared__ __attribute__((aligned(256))) unsigned char smem[kUsed > kRed ? kUsed : kRed];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int r = lane & 15, q = lane >> 4;
+  const int r = lane & 15, q = lane >> 4;      // MFMA layout
+  const int lr = lane >> 2, lp = lane & 3;     // load layout: row, piece
 
   const RowTiles<TM> tiles{a.offsets, a.groups, a.rows};
   const int nt = tiles.count();
@@ -66,7 +71,8 @@ __global__ __launch_bounds__(WS * 64) void rows_dx_stream_kernel(RowsGemm a, int
   // Unit u: rows 32 u ..; columns past K read zeros and have scale zero.
   const int nunits = a.N / kUnit;
   const bool kin = k0 + 8 * r < a.K;
-  const uint32_t wlane = (uint32_t)(8 * q) * rowK2 + (uint32_t)(k0 + 8 * r) / 2u;
+  const uint32_t wlane =
+      kin ? (uint32_t)(8 * q) * rowK2 + (uint32_t)(k0 + 8 * r) / 2u : kFar;
   // the lane's own scale: row lane / 2, block lane % 2 of the unit
   const uint32_t sblk = (uint32_t)k0 / 64u + (uint32_t)(lane & 1);
   const bool sin = sblk < nkb;
@@ -75,24 +81,23 @@ __global__ __launch_bounds__(WS * 64) void rows_dx_stream_kernel(RowsGemm a, int
     uint32_t w[8];
     uint32_t q;
     float s;
+    u32x4_t y[RB];
   };
-  u32x4_t ynext[RB];   // dY of the next unit
   const uint16_t* yp[RB];
 #pragma unroll
   for (int i = 0; i < RB; ++i) {
     // places past the tile repeat its first row (never stored)
-    const int place = tile.r0 + 16 * i + r < tile.r1 ? tile.r0 + 16 * i + r : tile.r0;
+    const int place = tile.r0 + 16 * i + lr < tile.r1 ? tile.r0 + 16 * i + lr : tile.r0;
     int yr = x_row_of(a, place);
     yr = yr < 0 ? 0 : yr;
-    yp[i] = a.x + (int64_t)yr * a.ldx + 8 * q;
+    yp[i] = a.x + (int64_t)yr * a.ldx + 8 * lp;
   }
   auto load = [&](Unit& u, int at) {
     at = at < nunits ? at : nunits - 1;   // past the end: never used
     const uint32_t so = (uint32_t)at * kUnit * rowK2;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      u.w[i] = __builtin_amdgcn_raw_buffer_load_b32(
-          rw, kin ? wlane + (uint32_t)i * rowK2 : kFar, so, 0);
+      u.w[i] = __builtin_amdgcn_raw_buffer_load_b32(rw, wlane + (uint32_t)i * rowK2, so, 0);
     const uint32_t blk = slane + (uint32_t)at * kUnit * nkb;
     if (DQ) {
       u.q = __builtin_amdgcn_raw_buffer_load_b8(rq, sin ? blk : kFar, 0, 0);
@@ -102,11 +107,8 @@ __global__ __launch_bounds__(WS * 64) void rows_dx_stream_kernel(RowsGemm a, int
       u.q = __builtin_amdgcn_raw_buffer_load_b32(rq, sin ? blk * 4u : kFar, 0, 0);
       u.s = 0.0f;
     }
-  };
-  auto load_y = [&](int at) {
-    at = at < nunits ? at : nunits - 1;
 #pragma unroll
-    for (int i = 0; i < RB; ++i) ynext[i] = *(const u32x4_t*)(yp[i] + at * kUnit);
+    for (int i = 0; i < RB; ++i) u.y[i] = *(const u32x4_t*)(yp[i] + at * kUnit);
   };
   float* const dmap = (float*)(smem + kMap);
   auto scale_of = [&](const Unit& u) {
@@ -122,10 +124,9 @@ __global__ __launch_bounds__(WS * 64) void rows_dx_stream_kernel(RowsGemm a, int
     return sin ? sc : 0.0f;
   };
 
-  Unit un[2];
-  load(un[0], wave);
-  load_y(wave);
-  load(un[1], wave + WS);
+  Unit un[kAhead];
+#pragma unroll
+  for (int p = 0; p < kAhead; ++p) load(un[p], wave + p * WS);
   lut_build(smem, lv, WS * 64);
   if (DYN)
     for (int e = t; e < 256; e += WS * 64) dmap[e] = kDynMapDev.v[e];
@@ -139,6 +140,9 @@ __global__ __launch_bounds__(WS * 64) void rows_dx_stream_kernel(RowsGemm a, int
 
   const uint32_t lcol = 8u * (uint32_t)(lane & 31);
   float* const scl = (float*)(smem + kScl + wave * 512);   // two sets of [block][row]
+  unsigned char* const stage = smem + kStage + wave * 1024;
+  const uint32_t wslot = 16u * (uint32_t)(16 * lp + ((lr + 4 * lp) & 15));
+  const uint32_t rslot = 16u * (uint32_t)(16 * q + ((r + 4 * q) & 15));
   auto mul = [&](Unit& u, int at, int set) {
     scl[64 * set + 32 * (lane & 1) + (lane >> 1)] = scale_of(u);
     const float4 s0 = *(const float4*)&scl[64 * set + 32 * (r >> 3) + 8 * q];
@@ -149,9 +153,11 @@ __global__ __launch_bounds__(WS * 64) void rows_dx_stream_kernel(RowsGemm a, int
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = u.w[i];
 #pragma unroll
-    for (int i = 0; i < RB; ++i) y[i] = ynext[i];
-    load_y(at + WS);
-    load(u, at + 2 * WS);
+    for (int i = 0; i < RB; ++i) {
+      *(u32x4_t*)(stage + wslot) = u.y[i];
+      y[i] = *(const u32x4_t*)(stage + rslot);
+    }
+    load(u, at + kAhead * WS);
     float2 l2[2][8];
     auto look = [&](int e) {
 #pragma unroll
@@ -177,13 +183,16 @@ __global__ __launch_bounds__(WS * 64) void rows_dx_stream_kernel(RowsGemm a, int
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // Whole pairs of units (no branch around a load), then the odd one.
-  int at = wave;
-  for (; at + WS < nunits; at += 2 * WS) {
-    mul(un[0], at, 0);
-    mul(un[1], at + WS, 1);
+  // No branch around a load, only out of the loop: the compiler's waits count
+  // the loads issued since.
+  for (int at = wave; at < nunits;) {
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p) {
+      mul(un[p], at, p & 1);
+      at += WS;
+      if (at >= nunits) break;
+    }
   }
-  if (at < nunits) mul(un[0], at, 0);
 
   // The tree: the upper half of the waves hands over, the lower half adds.
   f32x4_t* const red = (f32x4_t*)smem;

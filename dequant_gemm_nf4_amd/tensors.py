@@ -4,6 +4,7 @@ computed here."""
 
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 
 import torch
@@ -215,7 +216,7 @@ def linear_lora(x: torch.Tensor, q: QuantizedWeight, lora_a: torch.Tensor, lora_
 # --------------------------------------------------------------------------
 # rows that belong to groups (include/bnbx_rows.h)
 # --------------------------------------------------------------------------
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True)
 class RowGroups:
     """A plan of bnbx_group_rows: the rows 0 .. rows-1 in group order.  Group
     g holds the places offsets[g] .. offsets[g+1]-1 of ``order``; places
@@ -225,6 +226,14 @@ class RowGroups:
     offsets: torch.Tensor   # int32 [groups + 1]
     order: torch.Tensor     # int32 [rows]
 
+    def __post_init__(self):
+        for name, t, n in (("offsets", self.offsets, self.groups + 1),
+                           ("order", self.order, self.order.numel())):
+            if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous():
+                raise ValueError(f"plan: {name} must be a contiguous int32 vector of {n}")
+        if self.offsets.device != self.order.device:
+            raise ValueError("plan: offsets and order are on different devices")
+
     @property
     def rows(self) -> int:
         return self.order.shape[0]
@@ -233,15 +242,6 @@ class RowGroups:
     def desc(self) -> RowGroupsDesc:
         return RowGroupsDesc(self.offsets.data_ptr(), self.order.data_ptr(), self.groups,
                              self.order.shape[0])
-
-
-def _check_plan(rows: RowGroups, device) -> None:
-    for name, t, n in (("offsets", rows.offsets, rows.groups + 1),
-                       ("order", rows.order, rows.order.numel())):
-        if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
-            raise ValueError(f"plan: {name} must be a contiguous int32 vector of {n}")
-        if t.device != device:
-            raise ValueError(f"plan: {name} is on {t.device}, the data on {device}")
 
 
 def _check_matrix(name: str, t: torch.Tensor, cols: int, dtype, device) -> None:
@@ -261,11 +261,14 @@ def _ld(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device):
     """The device of the data as the current one, for the launch."""
     if device.type != "cuda":
         raise ValueError(f"the data must be on a GPU, not on {device}")
-    return torch.cuda.device(device)
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def empty_row_groups(rows: int, groups: int, device="cuda") -> RowGroups:
@@ -277,20 +280,26 @@ def group_rows(ids: torch.Tensor, groups: int, out: RowGroups | None = None,
                workspace: torch.Tensor | None = None, stream=None) -> RowGroups:
     """bnbx_group_rows: the plan of an int32 vector of group ids (any id
     outside 0 .. groups-1: no group), on the device, stable."""
-    if ids.dtype != torch.int32 or ids.dim() != 1 or not ids.is_contiguous():
+    rows = ids.numel()
+    if ids.dtype != torch.int32 or ids.shape != (rows,) or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int32 vector")
-    plan = out if out is not None else empty_row_groups(ids.numel(), groups, ids.device)
-    if plan.groups != groups or plan.rows != ids.numel():
-        raise ValueError("out: a plan of other sizes")
-    _check_plan(plan, ids.device)
-    with _on(ids.device):
-        nbytes = bnbx_group_rows_workspace_bytes(ids.numel(), groups)
+    device = ids.device
+    plan = out if out is not None else empty_row_groups(rows, groups, device)
+    if plan.groups != groups or plan.rows != rows or plan.order.device != device:
+        raise ValueError("out: a plan of other sizes, or on another device")
+    with _on(device):
+        nbytes = bnbx_group_rows_workspace_bytes(rows, groups)
         if nbytes and workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=ids.device)
-        bnbx_group_rows(ids, ids.numel(), groups, plan.offsets, plan.order,
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        bnbx_group_rows(ids, rows, groups, plan.offsets, plan.order,
                         workspace if nbytes else None,
                         workspace.numel() * workspace.element_size() if nbytes else 0, stream)
     return plan
+
+
+def _check_plan(rows: RowGroups, device) -> None:
+    if rows.order.device != device:
+        raise ValueError(f"the plan is on {rows.order.device}, the data on {device}")
 
 
 def _check_stack(q: QuantizedWeight, rows: RowGroups) -> None:
@@ -300,15 +309,16 @@ def _check_stack(q: QuantizedWeight, rows: RowGroups) -> None:
 
 def _rows_product(call, name: str, t: torch.Tensor, q: QuantizedWeight, rows: RowGroups,
                   cin: int, cout: int, gather: int, scatter: bool, out, stream) -> torch.Tensor:
-    _check_matrix(name, t, cin, q.dtype, q.packed.device)
-    _check_plan(rows, t.device)
-    y = out if out is not None else torch.zeros(rows.rows, cout, dtype=q.dtype, device=t.device)
-    _check_matrix("out", y, cout, q.dtype, t.device)
+    device = q.packed.device
+    _check_matrix(name, t, cin, q.dtype, device)
+    _check_plan(rows, device)
+    y = out if out is not None else torch.zeros(rows.rows, cout, dtype=q.dtype, device=device)
+    _check_matrix("out", y, cout, q.dtype, device)
     if gather < 0:
         raise ValueError("gather must be 0 or the slots per row")
     if t.shape[0] * max(gather, 1) < rows.rows or y.shape[0] < rows.rows:
         raise ValueError("fewer rows than the plan has places")
-    with _on(t.device):
+    with _on(device):
         call(t, _ld(t), t.shape[0], q.packed, q.state, rows.desc, q.shape[1], q.shape[2], gather,
              int(scatter), y, _ld(y), y.shape[0], stream)
     return y
@@ -348,34 +358,33 @@ def linear_adapters(x: torch.Tensor, q: QuantizedWeight, rows: RowGroups, lora_a
     if len(q.shape) != 2:
         raise ValueError(f"the weight must be [N, K], not {q.shape}")
     N, K = q.shape
-    _check_matrix("x", x, K, q.dtype, q.packed.device)
-    _check_plan(rows, x.device)
+    device, groups = q.packed.device, rows.groups
+    _check_matrix("x", x, K, q.dtype, device)
+    _check_plan(rows, device)
     if x.shape[0] != rows.rows:
         raise ValueError(f"x has {x.shape[0]} rows, the plan {rows.rows}")
-    if lora_a.dim() != 3 or lora_b.dim() != 3 or lora_a.shape[0] != rows.groups:
-        raise ValueError(f"the adapters must be A [{rows.groups}, r, {K}] and "
-                         f"B [{rows.groups}, {N}, r]")
-    r = lora_a.shape[1]
-    for name, t, shape in (("lora_a", lora_a, (rows.groups, r, K)),
-                           ("lora_b", lora_b, (rows.groups, N, r)),
-                           ("scale", scale, (rows.groups,))):
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {shape}, not {tuple(t.shape)}")
-        if t.dtype != (torch.float32 if name == "scale" else q.dtype):
-            raise TypeError(f"{name}: {t.dtype}")
-        if t.device != x.device or t.stride(-1) != 1 and t.numel() > 1:
-            raise ValueError(f"{name} must be on {x.device} with contiguous rows")
-    y = out if out is not None else torch.empty(rows.rows, N, dtype=q.dtype, device=x.device)
-    _check_matrix("out", y, N, q.dtype, x.device)
+    r = lora_a.shape[1] if lora_a.dim() == 3 else 0
+    if lora_a.shape != (groups, r, K) or lora_b.shape != (groups, N, r) or scale.shape != (groups,):
+        raise ValueError(f"the adapters must be A [{groups}, r, {K}], B [{groups}, {N}, r] and "
+                         f"scale [{groups}], not {tuple(lora_a.shape)}, {tuple(lora_b.shape)} and "
+                         f"{tuple(scale.shape)}")
+    if lora_a.dtype != q.dtype or lora_b.dtype != q.dtype or scale.dtype != torch.float32:
+        raise TypeError(f"the adapters must be {q.dtype}, their scales float32")
+    if lora_a.device != device or lora_b.device != device or scale.device != device:
+        raise ValueError(f"the adapters must be on {device}")
+    if lora_a.stride(2) != 1 or lora_b.stride(2) != 1 or (groups > 1 and scale.stride(0) != 1):
+        raise ValueError("the adapters must have contiguous rows")
+    y = out if out is not None else torch.empty(rows.rows, N, dtype=q.dtype, device=device)
+    _check_matrix("out", y, N, q.dtype, device)
     if y.shape[0] != rows.rows:
         raise ValueError(f"out has {y.shape[0]} rows, the plan {rows.rows}")
     desc = AdaptersDesc(lora_a.data_ptr(), lora_b.data_ptr(), scale.data_ptr(), _row(lora_a),
-                        lora_a.stride(0) if rows.groups > 1 else 0, _row(lora_b),
-                        lora_b.stride(0) if rows.groups > 1 else 0, r)
-    with _on(x.device):
+                        lora_a.stride(0) if groups > 1 else 0, _row(lora_b),
+                        lora_b.stride(0) if groups > 1 else 0, r)
+    with _on(device):
         nbytes = bnbx_gemm_nf4_adapters_workspace_bytes(rows.rows, r)
         if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         bnbx_gemm_nf4_adapters(x, _ld(x), q.packed, q.state, rows.desc, N, K, desc, y, _ld(y),
                                workspace, workspace.numel() * workspace.element_size(), stream)
     return y
