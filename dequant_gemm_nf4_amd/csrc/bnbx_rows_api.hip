@@ -30,7 +30,9 @@ int check_rows(const uint16_t* x, int64_t ldx, int x_rows, int64_t kx, const uin
   if (ldx < kx || ldy < ny) return BNBX_E_INVAL;
   if (ldx % 8 != 0) return BNBX_E_ALIGN;
   if (!aligned(x, 16) || !aligned(packed, 16) || !aligned(y, 2)) return BNBX_E_ALIGN;
-  if (st->double_quant == kDqNone && !aligned(st->absmax, 4)) return BNBX_E_ALIGN;
+  if (st->double_quant == kDqNone ? !aligned(st->absmax, 4)
+                                  : !aligned(st->absmax2, 4) || !aligned(st->absmax_mean, 4))
+    return BNBX_E_ALIGN;
   if ((int64_t)N * (K / 2) >= ((int64_t)1 << 31)) return BNBX_E_UNSUPPORTED;
   return BNBX_OK;
 }

@@ -1,7 +1,11 @@
 """PyTorch custom ops and modules over the C ABI: the 4-bit linear layer as
 ``torch.ops.bnbx.linear4bit`` and a ``Linear4bit`` module that quantizes its
 weight on load; the same layer with a LoRA adapter as
-``torch.ops.bnbx.linear4bit_lora`` and ``Linear4bitLoRA``.
+``torch.ops.bnbx.linear4bit_lora`` and ``Linear4bitLoRA``; and the layers whose
+rows belong to groups: ``torch.ops.bnbx.group_rows`` (the plan),
+``torch.ops.bnbx.experts4bit`` with ``Experts4bit`` (one 4-bit weight an expert)
+and ``torch.ops.bnbx.linear4bit_adapters`` with ``Linear4bitAdapters`` (one 4-bit
+weight, one adapter a request).
 
 The pomoai.com overview (module list) has ``Linear4bit`` replacing
 ``torch.nn.Linear`` and the mlqm.cn article (section 4) loads a model in
@@ -256,3 +260,240 @@ class Linear4bitLoRA(Linear4bit):
 
     def extra_repr(self) -> str:
         return super().extra_repr() + f", rank={self.rank}, scale={self.scale}"
+
+
+# ---------------------------------------------------------------------------
+# rows that belong to groups
+# ---------------------------------------------------------------------------
+@torch.library.custom_op("bnbx::group_rows", mutates_args=())
+def group_rows(ids: torch.Tensor, groups: int) -> tuple[torch.Tensor, torch.Tensor]:
+    """The plan of int32 group ids of any shape, flattened: (offsets [groups +
+    1], order [ids.numel()]).  Rows whose id is outside 0 .. groups-1 come
+    last, in no group."""
+    plan = T.group_rows(ids.reshape(-1).contiguous(), groups)
+    return plan.offsets, plan.order
+
+
+@group_rows.register_fake
+def _(ids, groups):
+    return (ids.new_empty(groups + 1, dtype=torch.int32),
+            ids.new_empty(ids.numel(), dtype=torch.int32))
+
+
+def _rows_of(t: torch.Tensor) -> torch.Tensor:
+    """A 2-D operand as the kernels read it: contiguous rows, 16-byte aligned."""
+    if t.stride(-1) != 1 or t.stride(0) % 8 != 0 or t.data_ptr() % 16 != 0:
+        t = t.contiguous()
+    return t
+
+
+def _stack(dtype, packed, absmax, absmax2, absmax_mean, shape, quant_type) -> T.QuantizedWeight:
+    n = 1
+    for d in shape:
+        n *= d
+    return T.QuantizedWeight(n=n, shape=shape, double_quant=absmax2 is not None, packed=packed,
+                             absmax=absmax, absmax2=absmax2, absmax_mean=absmax_mean,
+                             quant_type=quant_type, dtype=dtype, dq_map=_dq_map(absmax))
+
+
+def _check_rows(name: str, t: torch.Tensor, rows: int, gather: int) -> None:
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name}: the rows must be bfloat16 or float16, not {t.dtype}")
+    if t.dim() != 2 or gather < 0 or t.shape[0] * max(gather, 1) != rows:
+        raise ValueError(f"{name}: {tuple(t.shape)} rows, each with {max(gather, 1)} of the plan's "
+                         f"{rows} places, do not match")
+
+
+@torch.library.custom_op("bnbx::experts4bit", mutates_args=())
+def experts4bit(x: torch.Tensor, packed: torch.Tensor, absmax: torch.Tensor,
+                absmax2: Optional[torch.Tensor], absmax_mean: Optional[torch.Tensor],
+                offsets: torch.Tensor, order: torch.Tensor, out_features: int, gather: int,
+                scatter: bool, quant_type: str) -> torch.Tensor:
+    """Y_i = X_i . W_hat_g^T for the places i of every group g of the plan
+    (offsets, order); the weights are one stack [groups, out_features, K].
+
+    ``gather`` 0: place i reads row i of X; ``gather`` t >= 1: row order[i] // t, X
+    having one row for every t places (top_k slots a token).  ``scatter``: the
+    result's row order[i], else row i.  Rows of no group are zero."""
+    _check_rows("experts4bit", x, order.numel(), gather)
+    groups = offsets.numel() - 1
+    q = _stack(x.dtype, packed, absmax, absmax2, absmax_mean, (groups, out_features, x.shape[1]),
+               quant_type)
+    return T.gemm_experts(_rows_of(x), q, T.RowGroups(groups, offsets, order), gather, scatter)
+
+
+@experts4bit.register_fake
+def _(x, packed, absmax, absmax2, absmax_mean, offsets, order, out_features, gather, scatter,
+      quant_type):
+    return x.new_empty(order.numel(), out_features)
+
+
+@torch.library.custom_op("bnbx::experts4bit_dx", mutates_args=())
+def experts4bit_dx(dy: torch.Tensor, packed: torch.Tensor, absmax: torch.Tensor,
+                   absmax2: Optional[torch.Tensor], absmax_mean: Optional[torch.Tensor],
+                   offsets: torch.Tensor, order: torch.Tensor, in_features: int, gather: int,
+                   scatter: bool, quant_type: str) -> torch.Tensor:
+    """dX_i = dY_i . W_hat_g in dY's dtype, one row a place (out_features % 64 ==
+    0); ``gather`` and ``scatter`` as in experts4bit."""
+    _check_rows("experts4bit_dx", dy, order.numel(), gather)
+    groups = offsets.numel() - 1
+    q = _stack(dy.dtype, packed, absmax, absmax2, absmax_mean, (groups, dy.shape[1], in_features),
+               quant_type)
+    return T.gemm_experts_dx(_rows_of(dy), q, T.RowGroups(groups, offsets, order), gather, scatter)
+
+
+@experts4bit_dx.register_fake
+def _(dy, packed, absmax, absmax2, absmax_mean, offsets, order, in_features, gather, scatter,
+      quant_type):
+    return dy.new_empty(order.numel(), in_features)
+
+
+def _experts_setup(ctx, inputs, output):
+    (x, packed, absmax, absmax2, absmax_mean, offsets, order, out_features, gather, scatter,
+     quant_type) = inputs
+    ctx.save_for_backward(packed, absmax, absmax2, absmax_mean, offsets, order)
+    ctx.args = x.shape[1], gather, scatter, quant_type
+
+
+def _experts_backward(ctx, grad):
+    dx = None
+    if ctx.needs_input_grad[0]:
+        in_features, gather, scatter, quant_type = ctx.args
+        # the forward's rows the other way round: dY is read where Y was
+        # written, dX written where X was read, one row a slot
+        dx = torch.ops.bnbx.experts4bit_dx(grad, *ctx.saved_tensors, in_features,
+                                           1 if scatter else 0, gather > 0, quant_type)
+        if gather > 1:
+            # a token's gradient: its slots' rows, added in fp32
+            dx = dx.view(-1, gather, in_features).sum(1, dtype=torch.float32).to(grad.dtype)
+    return (dx,) + (None,) * 10
+
+
+experts4bit.register_autograd(_experts_backward, setup_context=_experts_setup)
+
+
+@torch.library.custom_op("bnbx::linear4bit_adapters", mutates_args=())
+def linear4bit_adapters(x: torch.Tensor, packed: torch.Tensor, absmax: torch.Tensor,
+                        absmax2: Optional[torch.Tensor], absmax_mean: Optional[torch.Tensor],
+                        offsets: torch.Tensor, order: torch.Tensor, lora_a: torch.Tensor,
+                        lora_b: torch.Tensor, scale: torch.Tensor, out_features: int,
+                        quant_type: str) -> torch.Tensor:
+    """Y[..., N] = X . W_hat^T + s_g . (X . A_g^T) . B_g^T with the adapter of each
+    row's group in the plan (rows of X flattened; A [groups, r, K], B [groups,
+    N, r], scale float32 [groups]).  Inference only: no autograd is registered,
+    so a backward through it raises."""
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"linear4bit_adapters: x must be bfloat16 or float16, not {x.dtype}")
+    K = x.shape[-1]
+    x2 = _rows_of(x.reshape(-1, K))
+    q = _stack(x.dtype, packed, absmax, absmax2, absmax_mean, (out_features, K), quant_type)
+    y = T.linear_adapters(x2, q, T.RowGroups(offsets.numel() - 1, offsets, order),
+                          lora_a.contiguous(), lora_b.contiguous(), scale.contiguous())
+    return y.reshape(*x.shape[:-1], out_features)
+
+
+@linear4bit_adapters.register_fake
+def _(x, packed, absmax, absmax2, absmax_mean, offsets, order, lora_a, lora_b, scale, out_features,
+      quant_type):
+    return x.new_empty(*x.shape[:-1], out_features)
+
+
+class Experts4bit(Linear4bit):
+    """The linear layers of a mixture's experts, [experts, out_features,
+    in_features] in 4 bits as one tensor (blocks of 64, options as
+    ``Linear4bit``), frozen.  ``load_weight`` takes the bf16 stack.
+
+    forward(x, plan, gather, scatter) multiplies the rows of every expert by its
+    weight (``torch.ops.bnbx.experts4bit``; ``plan`` from
+    ``torch.ops.bnbx.group_rows`` of the router's choices).  An up-projection of
+    top_k choices a token: ids [tokens, top_k], ``gather=top_k``, the result's rows
+    in expert order; the down-projection of those: ``scatter=True``, the result's
+    rows in slot order [tokens * top_k].  The input gradient needs out_features
+    % 64 == 0."""
+
+    def __init__(self, experts: int, in_features: int, out_features: int, **kw):
+        if experts < 1:
+            raise ValueError("experts must be positive")
+        super().__init__(in_features, experts * out_features, **kw)
+        self.experts, self.out_features = experts, out_features
+
+    def quantized(self) -> T.QuantizedWeight:
+        return _stack(self.compute_dtype, self.packed, self.absmax, self.absmax2, self.absmax_mean,
+                      (self.experts, self.out_features, self.in_features), self.quant_type)
+
+    @torch.no_grad()
+    def load_weight(self, w: torch.Tensor) -> "Experts4bit":
+        shape = (self.experts, self.out_features, self.in_features)
+        if tuple(w.shape) != shape:
+            raise ValueError(f"weight shape {tuple(w.shape)} != {shape}")
+        w = w.to(device=self.packed.device, dtype=torch.bfloat16).contiguous()
+        T.quantize(w, self.double_quant, out=self.quantized())
+        return self
+
+    @classmethod
+    def from_linear(cls, linear, **kw):
+        raise TypeError("Experts4bit holds a stack of weights: use load_weight")
+
+    def forward(self, x: torch.Tensor, plan, gather: int = 0,
+                scatter: bool = False) -> torch.Tensor:
+        if x.dtype != self.compute_dtype:
+            raise TypeError(f"input dtype {x.dtype} != compute dtype {self.compute_dtype}")
+        offsets, order = plan
+        if offsets.numel() != self.experts + 1:
+            raise ValueError(f"a plan of {offsets.numel() - 1} groups for {self.experts} experts")
+        return torch.ops.bnbx.experts4bit(x, self.packed, self.absmax, self.absmax2,
+                                          self.absmax_mean, offsets, order, self.out_features,
+                                          gather, scatter, self.quant_type)
+
+    def extra_repr(self) -> str:
+        return f"experts={self.experts}, " + super().extra_repr()
+
+
+class Linear4bitAdapters(Linear4bit):
+    """``Linear4bit`` beside a pool of low-rank adapters, one chosen per row: Y =
+    X . W_hat^T + s_g . (X . A_g^T) . B_g^T.  The pool holds ``adapters`` slots of
+    one rank (a lower rank is padded with zero rows of A and columns of B), zero
+    at the start, set with ``load_adapter``.  forward(x, plan) takes the plan of
+    the rows' slots (``torch.ops.bnbx.group_rows``, one per batch for all its
+    layers; a row of no slot gets the 4-bit product alone).  Inference only."""
+
+    def __init__(self, in_features: int, out_features: int, adapters: int, rank: int = 16, **kw):
+        super().__init__(in_features, out_features, **kw)
+        if rank < 16 or rank > 256 or rank % 16 != 0:
+            raise ValueError("rank must be a multiple of 16 between 16 and 256")
+        if adapters < 1:
+            raise ValueError("adapters must be positive")
+        self.adapters, self.rank = adapters, rank
+        dev, dt = self.packed.device, self.compute_dtype
+        self.register_buffer("lora_a", torch.zeros(adapters, rank, in_features, dtype=dt, device=dev))
+        self.register_buffer("lora_b", torch.zeros(adapters, out_features, rank, dtype=dt,
+                                                   device=dev))
+        self.register_buffer("scale", torch.zeros(adapters, dtype=torch.float32, device=dev))
+
+    @torch.no_grad()
+    def load_adapter(self, slot: int, a: torch.Tensor, b: torch.Tensor,
+                     scale: float = 1.0) -> "Linear4bitAdapters":
+        r = a.shape[0] if a.dim() == 2 else 0
+        if not 0 <= slot < self.adapters:
+            raise ValueError(f"slot {slot} of {self.adapters}")
+        if tuple(a.shape) != (r, self.in_features) or tuple(b.shape) != (self.out_features, r) \
+                or not 1 <= r <= self.rank:
+            raise ValueError(f"adapter shapes {tuple(a.shape)}, {tuple(b.shape)} do not fit "
+                             f"{(self.rank, self.in_features)}, {(self.out_features, self.rank)}")
+        self.lora_a[slot].zero_()[:r].copy_(a)
+        self.lora_b[slot].zero_()[:, :r].copy_(b)
+        self.scale[slot] = float(scale)
+        return self
+
+    def forward(self, x: torch.Tensor, plan) -> torch.Tensor:
+        if x.dtype != self.compute_dtype:
+            raise TypeError(f"input dtype {x.dtype} != compute dtype {self.compute_dtype}")
+        offsets, order = plan
+        if offsets.numel() != self.adapters + 1:
+            raise ValueError(f"a plan of {offsets.numel() - 1} groups for {self.adapters} adapters")
+        return torch.ops.bnbx.linear4bit_adapters(
+            x, self.packed, self.absmax, self.absmax2, self.absmax_mean, offsets, order,
+            self.lora_a, self.lora_b, self.scale, self.out_features, self.quant_type)
+
+    def extra_repr(self) -> str:
+        return super().extra_repr() + f", adapters={self.adapters}, rank={self.rank}"
