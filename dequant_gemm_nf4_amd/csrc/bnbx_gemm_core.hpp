@@ -305,7 +305,7 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(
   int64_t grem = 0;   // the weight's first block in its group of scales (ROWS)
   __shared__ int yrow[ROWS ? BM : 1];   // the tile's rows of Y (ROWS)
   if constexpr (ROWS) {
-    const RowTiles<BM> tiles{rows.offsets, rows.groups, rows.rows};
+    RowTiles<BM> tiles{rows.offsets, rows.groups, rows.rows};
     const int id = xcd_item(tiles.count() * tiles_n);
     if (id < 0) return;
     const RowTile rt = tiles.find(__builtin_amdgcn_readfirstlane(id / tiles_n));

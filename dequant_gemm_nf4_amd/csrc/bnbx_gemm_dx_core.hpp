@@ -102,7 +102,7 @@ __global__ __launch_bounds__(kThreads) void gemm_dx_kernel(
   int64_t grem = 0;      // the weight's first block in its group of scales (ROWS)
   __shared__ int yrow[ROWS ? TM : 1];   // the tile's rows of dX (ROWS)
   if constexpr (ROWS) {
-    const RowTiles<TM> tiles{rows.offsets, rows.groups, rows.rows};
+    RowTiles<TM> tiles{rows.offsets, rows.groups, rows.rows};
     const int id = xcd_item(tiles.count() * tiles_k);
     if (id < 0) return;
     const RowTile rt = tiles.find(__builtin_amdgcn_readfirstlane(id / tiles_k));

@@ -15,20 +15,35 @@ __device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
                                            0x00020000);
 }
 
+// Double-quant block scale exactly as stored, fl32(fl32(q * fl32(s / 127)) +
+// mean), without a branch (one would cut the kernels' scheduling regions in
+// two).  fl32(s / 127) is the binary64 product with 1/127 rounded once more:
+// s / 127 lies at least 1/254 of a binary32 step from any midpoint of two
+// binary32 values (s is a whole number of steps, 127 odd), the product's error
+// is below 2^-28 of a step, so the second rounding is that of the quotient, for
+// subnormals too.
+__device__ __forceinline__ float rows_dq_scale(float q, float s, float mean) {
+  const float step = (float)((double)s * (1.0 / 127.0));
+  const float prod = q * step;
+  return prod + mean;
+}
+
 // Range of a resource over `bytes` bytes (at most what 32-bit offsets that
 // stay below kFar can reach).
 __device__ __forceinline__ uint32_t rsrc_bytes(int64_t bytes) {
   return bytes <= 0 ? 0u : bytes < (int64_t)kFar ? (uint32_t)bytes : kFar;
 }
 
-// Inclusive prefix sum over the wave.
+// Inclusive prefix sum over the wave, on the DPP paths (no LDS round trips):
+// within rows of 16 lanes, then lane 15 of each row into the next one, then
+// lane 31 into the upper half.
 __device__ __forceinline__ int wave_scan(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(v, o);
-    if (lane >= o) v += u;
-  }
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast:31
   return v;
 }
 
@@ -55,17 +70,21 @@ struct RowTiles {
       b = b < a ? a : b > rows ? rows : b;
     }
   }
-  __device__ __forceinline__ int count() const {
+  // The tiles of all groups; keeps the first 64 groups' part for find().
+  int a0, b0, incl0;
+  __device__ __forceinline__ int count() {
     if (offsets == nullptr) return (rows + TM - 1) / TM;
-    int n = 0;
-    for (int c = 0; c < groups; c += 64) {
+    bounds((int)(threadIdx.x & 63), a0, b0);
+    incl0 = wave_scan((b0 - a0 + TM - 1) / TM);
+    int n = __builtin_amdgcn_readlane(incl0, 63);
+    for (int c = 64; c < groups; c += 64) {
       int a, b;
       bounds(c + (int)(threadIdx.x & 63), a, b);
       n += __builtin_amdgcn_readlane(wave_scan((b - a + TM - 1) / TM), 63);
     }
-    return __builtin_amdgcn_readfirstlane(n);
+    return n;
   }
-  // Tile t < count().
+  // Tile t < count(), after count().
   __device__ __forceinline__ RowTile find(int t) const {
     RowTile r{0, 0, 0};
     if (offsets == nullptr) {
@@ -73,15 +92,12 @@ struct RowTiles {
       r.r1 = r.r0 + TM < rows ? r.r0 + TM : rows;
       return r;
     }
-    int base = 0;
-    for (int c = 0; c < groups; c += 64) {
-      int a, b;
-      bounds(c + (int)(threadIdx.x & 63), a, b);
-      const int n = (b - a + TM - 1) / TM;
-      const int incl = base + wave_scan(n);
+    int base = 0, a = a0, b = b0, incl = incl0;
+    for (int c = 0;;) {
       const uint64_t past = __ballot(incl > t);
       if (past != 0) {
         const int l = __builtin_ctzll(past);
+        const int n = (b - a + TM - 1) / TM;
         const int first = __builtin_amdgcn_readlane(incl - n, l);
         const int ga = __builtin_amdgcn_readlane(a, l), gb = __builtin_amdgcn_readlane(b, l);
         r.g = c + l;
@@ -90,8 +106,11 @@ struct RowTiles {
         return r;
       }
       base = __builtin_amdgcn_readlane(incl, 63);
+      c += 64;
+      if (c >= groups) return r;
+      bounds(c + (int)(threadIdx.x & 63), a, b);
+      incl = base + wave_scan((b - a + TM - 1) / TM);
     }
-    return r;
   }
 };
 

@@ -48,7 +48,7 @@ __global__ __launch_bounds__(WS * 64) void rows_dx_stream_kernel(RowsGemm a, int
   const int r = lane & 15, q = lane >> 4;      // MFMA layout
   const int lr = lane >> 2, lp = lane & 3;     // load layout: row, piece
 
-  const RowTiles<TM> tiles{a.offsets, a.groups, a.rows};
+  RowTiles<TM> tiles{a.offsets, a.groups, a.rows};
   const int nt = tiles.count();
   const int id = xcd_item(nt * tiles_k);
   if (id < 0) return;
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(WS * 64) void rows_dx_stream_kernel(RowsGemm a, int
       const float prod = dmap[u.q & 0xffu] * u.s;
       sc = prod + mu;
     } else if (DQ) {
-      sc = dq_scale((float)(int8_t)(uint8_t)u.q, u.s, mu);
+      sc = rows_dq_scale((float)(int8_t)(uint8_t)u.q, u.s, mu);
     } else {
       sc = __builtin_bit_cast(float, u.q);
     }

@@ -30,7 +30,7 @@ __global__ __launch_bounds__(kThreads) void rows_lora_down_kernel(RowsGemm a, Lo
   __shared__ __attribute__((aligned(16))) unsigned char stages[kWaves][1024];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const RowTiles<kTile> tiles{d.offsets, d.adapters, a.rows};
+  RowTiles<kTile> tiles{d.offsets, d.adapters, a.rows};
   const int nt = tiles.count();
   const int id = xcd_item(nt * rank_tiles);
   if (id < 0) return;

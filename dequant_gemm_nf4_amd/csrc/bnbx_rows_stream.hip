@@ -33,6 +33,8 @@
 // launches whose weight rows alone give the GPU too few waves.  With WN = 1 no
 // wave shares X and each loads its operands straight from memory, only the
 // lanes whose place exists (one token: 4 of 64).
+#include <type_traits>
+
 #include "bnbx_rows_device.hpp"
 #include "bnbx_tab16.hpp"
 
@@ -41,8 +43,7 @@ namespace {
 
 constexpr int kSlice = 256;          // k per unit
 
-
-template <int RB, int NB, int WN, int WK, bool LUT, int DQ, bool F16>
+template <int RB, int NB, int WN, int WK, bool LUT, int DQ, bool Q4, bool F16>
 __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, int tiles_n,
                                                                   LevelTable lv) {
   constexpr int TM = 16 * RB, TN = 16 * NB * WN, kThreads = WN * WK * 64;
@@ -67,7 +68,7 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   const int r = lane & 15, q = lane >> 4;      // MFMA layout
   const int lr = lane >> 2, lp = lane & 3;     // load layout: row, piece
 
-  const RowTiles<TM> tiles{a.offsets, a.groups, a.rows};
+  RowTiles<TM> tiles{a.offsets, a.groups, a.rows};
   const int nt = tiles.count();
   const int id = xcd_item(nt * tiles_n);   // fits: the grid covers it
   if (id < 0) return;
@@ -97,7 +98,7 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
 
   struct Unit {
     u32x4_t w[2];
-    uint32_t q;    // code byte, or the fp32 block maximum
+    uint32_t q;    // code byte, or the fp32 block maximum (not Q4)
     float s;       // group scale
   };
   uint32_t wrow[NB], brow[NB];
@@ -105,38 +106,81 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   for (int j = 0; j < NB; ++j) {
     const int nl = n0 + 16 * j + lr, nm = n0 + 16 * j + r;
     wrow[j] = nl < a.N ? (uint32_t)nl * rowK2 + 16u * (uint32_t)lp : kFar;
-    brow[j] = nm < a.N ? (uint32_t)nm * nkb + (uint32_t)q : kFar;
+    brow[j] = nm < a.N ? (uint32_t)nm * nkb : kFar;   // row r's first block
   }
+  // Byte offset of a block's group scale.
+  auto gidx = [&](uint32_t blk) { return ((grem + blk) >> 8) * 4u; };
   auto load_unit = [&](Unit& u, int j, int slice) {
     const bool in = slice < nslices;
     const uint32_t wo = in ? wrow[j] + (uint32_t)slice * (kSlice / 2) : kFar;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       u.w[h] = __builtin_amdgcn_raw_buffer_load_b128(rw, wo + 64u * h, 0, 2);
-    // the lane's block; past the end of the row it has no scale and no value
-    const bool bin = in && brow[j] != kFar && 4u * (uint32_t)slice + (uint32_t)q < nkb;
-    const uint32_t blk = brow[j] + 4u * (uint32_t)slice;
-    if (DQ) {
-      u.q = __builtin_amdgcn_raw_buffer_load_b8(rq, bin ? blk : kFar, 0, 0);
-      u.s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                          rg, bin ? ((grem + blk) >> 8) * 4u : kFar, 0, 0));
-    } else {
-      u.q = __builtin_amdgcn_raw_buffer_load_b32(rq, bin ? blk * 4u : kFar, 0, 0);
-      u.s = 0.0f;
+    if constexpr (!Q4) {
+      // the lane's block; past the end of the row it has no scale and no value
+      const uint32_t at = 4u * (uint32_t)slice + (uint32_t)q;
+      const bool bin = in && brow[j] != kFar && at < nkb;
+      const uint32_t blk = brow[j] + at;
+      if (DQ) {
+        u.q = __builtin_amdgcn_raw_buffer_load_b8(rq, bin ? blk : kFar, 0, 0);
+        u.s = __builtin_bit_cast(
+            float, __builtin_amdgcn_raw_buffer_load_b32(rg, bin ? gidx(blk) : kFar, 0, 0));
+      } else {
+        u.q = __builtin_amdgcn_raw_buffer_load_b32(rq, bin ? blk * 4u : kFar, 0, 0);
+        u.s = 0.0f;
+      }
     }
   };
-  auto scale_of = [&](const Unit& u, int j, int slice) {
-    const bool bin = brow[j] != kFar && 4u * (uint32_t)slice + (uint32_t)q < nkb;
-    float sc;
-    if (DQ) {
-      if (DYN) {
-        const float prod = dmap[u.q & 0xffu] * u.s;
-        sc = prod + mu;
+  // Block scale from its code (or fp32 bits) and group scale.
+  auto scale_of = [&](uint32_t code, float gs) {
+    if (DYN) {
+      const float prod = dmap[code & 0xffu] * gs;
+      return prod + mu;
+    }
+    if (DQ) return rows_dq_scale((float)(int8_t)(uint8_t)code, gs, mu);
+    return __builtin_bit_cast(float, code);
+  };
+  // Q4 (rows of a multiple of 4 blocks, codes 4-byte aligned, fp32 maxima 16):
+  // the codes of four steps in one load.  A lane loads the four codes of row r
+  // in the slice of step 4 t + q, all its bytes of that line at once (each such
+  // request costs the address path a cycle, whatever its size); step 4 t + p
+  // fetches lane (p, r)'s and takes block q's.
+  struct Quad {
+    u32x4_t q;     // code bytes (x), or four fp32 block maxima
+    float s;       // their group scale
+  };
+  auto load_quad = [&](Quad& u, int j, int s) {
+    if constexpr (Q4) {
+      const int slice = slice_of(s + q);
+      const bool bin = brow[j] != kFar && slice < nslices;
+      const uint32_t blk = brow[j] + 4u * (uint32_t)slice;
+      if (DQ) {
+        u.q[0] = __builtin_amdgcn_raw_buffer_load_b32(rq, bin ? blk : kFar, 0, 0);
+        u.s = __builtin_bit_cast(
+            float, __builtin_amdgcn_raw_buffer_load_b32(rg, bin ? gidx(blk) : kFar, 0, 0));
       } else {
-        sc = dq_scale((float)(int8_t)(uint8_t)u.q, u.s, mu);
+        u.q = __builtin_amdgcn_raw_buffer_load_b128(rq, bin ? blk * 4u : kFar, 0, 0);
+      }
+    }
+  };
+  // Scale of the lane's block in step s (ph = s % 4).
+  auto unit_scale = [&](const Unit& u, const Quad& c, int j, int s, int ph) {
+    const bool bin = brow[j] != kFar && 4u * (uint32_t)slice_of(s) + (uint32_t)q < nkb;
+    float sc;
+    if constexpr (Q4) {
+      const int from = (16 * ph + r) << 2;
+      if (DQ) {
+        const uint32_t codes = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)c.q[0]);
+        const float gs = __int_as_float(__builtin_amdgcn_ds_bpermute(from, __float_as_int(c.s)));
+        sc = scale_of(codes >> (8 * q), gs);
+      } else {
+        uint32_t v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)c.q[e]);
+        sc = __builtin_bit_cast(float, q < 2 ? (q == 0 ? v[0] : v[1]) : (q == 2 ? v[2] : v[3]));
       }
     } else {
-      sc = __builtin_bit_cast(float, u.q);
+      sc = scale_of(u.q, u.s);
     }
     return bin ? sc : 0.0f;
   };
@@ -147,6 +191,9 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   for (int p = 0; p < kAhead; ++p)
 #pragma unroll
     for (int j = 0; j < NB; ++j) load_unit(un[p][j], j, slice_of(p));
+  Quad quad[NB], quad_next[NB];   // of steps 4 t .. 4 t + 3, and of the next four
+#pragma unroll
+  for (int j = 0; j < NB; ++j) load_quad(quad_next[j], j, 0);
 
   if (LUT) lut_build(smem, lv, kThreads);
   if (DYN)
@@ -223,6 +270,15 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   const uint32_t ws0 = 16u * (uint32_t)(8 * lr + (lp ^ fold(lr)));
   const uint32_t rs0 = 16u * (uint32_t)(8 * r + ((2 * q) ^ fold(r)));
 
+  // Rows of Y of the lane's places, looked up while the first loads are in
+  // flight (-1: not written).
+  int yrow[RB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    const int place = tile.r0 + 16 * i + r;
+    yrow[i] = place < tile.r1 && x_row_of(a, place) >= 0 ? y_row_of(a, place) : -1;
+  }
+
   f32x4_t acc[NB][RB];
 #pragma unroll
   for (int j = 0; j < NB; ++j)
@@ -236,8 +292,12 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
     u32x4_t w[2];
     float sc;
   };
-  auto turn = [&](Op& o, Unit& u, int j, int s) {
-    o.sc = scale_of(u, j, slice_of(s));
+  auto turn = [&](Op& o, Unit& u, int j, int s, int ph) {   // ph = s % 4
+    if (Q4 && ph == 0) {
+      quad[j] = quad_next[j];
+      load_quad(quad_next[j], j, s + 4);
+    }
+    o.sc = unit_scale(u, quad[j], j, s, ph);
     *(u32x4_t*)(stage + ws0) = u.w[0];
     *(u32x4_t*)(stage + (ws0 ^ 64u)) = u.w[1];
     o.w[0] = *(const u32x4_t*)(stage + rs0);
@@ -248,10 +308,11 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   // Step s: `u` holds step s + 1's units, turned while step s multiplies.
   // (With register tables, step s's own: the turned ones would cost registers
   // that the accumulators need.)
-  auto step = [&](Unit (&u)[NB], int s) {
+  auto step = [&](Unit (&u)[NB], int s, auto phase) {
+    constexpr int PH = decltype(phase)::value;
     if constexpr (!LUT)
 #pragma unroll
-      for (int j = 0; j < NB; ++j) turn(op[j], u[j], j, s);
+      for (int j = 0; j < NB; ++j) turn(op[j], u[j], j, s, PH);
     Tab16 tab[LUT ? 1 : NB];
     u32x4_t w[NB][2];
     float sc[NB];
@@ -284,7 +345,7 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
       };
       look(0);
 #pragma unroll
-      for (int j = 0; j < NB; ++j) turn(op[j], u[j], j, s + 1);
+      for (int j = 0; j < NB; ++j) turn(op[j], u[j], j, s + 1, (PH + 1) & 3);
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
         if (m < 7) look(m + 1);
@@ -328,20 +389,26 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   barrier();
   if (LUT)
 #pragma unroll
-    for (int j = 0; j < NB; ++j) turn(op[j], un[0][j], j, 0);
-  // No branch around a load: the compiler's waits count the loads issued
-  // since, and would wait for all of them where it cannot tell how many.
-  auto advance = [&](Unit (&u)[NB], int s) {
+    for (int j = 0; j < NB; ++j) turn(op[j], un[0][j], j, 0, 0);
+  // No branch around a load, only out of the loop: the compiler's waits count
+  // the loads issued since, and would wait for all of them where it cannot tell
+  // how many.
+  auto advance = [&](Unit (&u)[NB], int s, auto phase) {
     load_x(slice_of(s + 1));
-    step(u, s);
+    step(u, s, phase);
     load_direct(slice_of(s + 1));
     put_x((s + 1) & 1, slice_of(s + 1));
     if (!DIRECT) barrier();
   };
-  // (Pairs of steps; a step past the last one multiplies zeros.)
-  for (int s = 0; s < nsteps; s += 2) {
-    advance(un[LUT ? 1 : 0], s);
-    advance(un[LUT ? 0 : 1], s + 1);
+  for (int s = 0;;) {
+    advance(un[LUT ? 1 : 0], s, std::integral_constant<int, 0>{});
+    if (++s >= nsteps) break;
+    advance(un[LUT ? 0 : 1], s, std::integral_constant<int, 1>{});
+    if (++s >= nsteps) break;
+    advance(un[LUT ? 1 : 0], s, std::integral_constant<int, 2>{});
+    if (++s >= nsteps) break;
+    advance(un[LUT ? 0 : 1], s, std::integral_constant<int, 3>{});
+    if (++s >= nsteps) break;
   }
   if (DIRECT) barrier();
 
@@ -442,9 +509,7 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   // Lane (q, r): place r of each 16, weight rows 4 q .. 4 q + 3 of each 16.
 #pragma unroll
   for (int i = 0; i < RB; ++i) {
-    const int place = tile.r0 + 16 * i + r;
-    if (place >= tile.r1 || x_row_of(a, place) < 0) continue;
-    const int row = y_row_of(a, place);
+    const int row = yrow[i];
     if (row < 0) continue;
     uint16_t* const yr = a.y + (int64_t)row * a.ldy;
 #pragma unroll
@@ -476,16 +541,22 @@ hipError_t launch_one(const RowsGemm& a, int quant_type, bool f16, hipStream_t s
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(WN * WK * 64), 0, stream, a, tiles_n,
                        lv);
   };
-  if (a.double_quant == kDqNone) {
-    if (f16) go(rows_stream_kernel<RB, NB, WN, WK, LUT, kDqNone, true>);
-    else go(rows_stream_kernel<RB, NB, WN, WK, LUT, kDqNone, false>);
-  } else if (a.double_quant == kDqLinear) {
-    if (f16) go(rows_stream_kernel<RB, NB, WN, WK, LUT, kDqLinear, true>);
-    else go(rows_stream_kernel<RB, NB, WN, WK, LUT, kDqLinear, false>);
-  } else {
-    if (f16) go(rows_stream_kernel<RB, NB, WN, WK, LUT, kDqDynamic, true>);
-    else go(rows_stream_kernel<RB, NB, WN, WK, LUT, kDqDynamic, false>);
-  }
+  const int nkb = a.K / 64;
+  const bool q4 =
+      nkb % 4 == 0 && ((uintptr_t)a.absmax & (a.double_quant == kDqNone ? 15 : 3)) == 0;
+  auto pick = [&](auto dq, auto quads) {
+    constexpr int DQ = decltype(dq)::value;
+    constexpr bool Q4 = decltype(quads)::value;
+    if (f16) go(rows_stream_kernel<RB, NB, WN, WK, LUT, DQ, Q4, true>);
+    else go(rows_stream_kernel<RB, NB, WN, WK, LUT, DQ, Q4, false>);
+  };
+  auto with = [&](auto dq) {
+    if (q4) pick(dq, std::true_type{});
+    else pick(dq, std::false_type{});
+  };
+  if (a.double_quant == kDqNone) with(std::integral_constant<int, kDqNone>{});
+  else if (a.double_quant == kDqLinear) with(std::integral_constant<int, kDqLinear>{});
+  else with(std::integral_constant<int, kDqDynamic>{});
   return hipGetLastError();
 }
 
