@@ -18,7 +18,8 @@
 // kOneChunk rows one workgroup does everything in one launch; more rows are cut
 // into at most kMaxChunks chunks, whose key counts go to the workspace in a
 // first launch; in the second, every workgroup adds the counts of all chunks
-// itself (groups + 1 counters a chunk, from L2) instead of waiting for a third
+// itself (groups + 1 counters a chunk, from L2, wave w the chunks w, w + 16, ..;
+// integer sums, whose order does not matter) instead of waiting for a third
 // launch to do it.
 #include "bnbx_device.hpp"
 #include "bnbx_rows.hpp"
@@ -83,6 +84,8 @@ __global__ __launch_bounds__(kThreads) void group_rows_kernel(
     int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ order) {
   __shared__ int hist[kWaves * kStride];
   __shared__ int wsum[kWaves];
+  // PHASE 2: each key's rows in all chunks, and in the chunks before this one
+  __shared__ int total[PHASE == 2 ? kStride : 1], earlier[PHASE == 2 ? kStride : 1];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int keys = groups + 1;
@@ -95,7 +98,22 @@ __global__ __launch_bounds__(kThreads) void group_rows_kernel(
   int* const mine = hist + wave * kStride;
 
   for (int k = lane; k < keys; k += 64) mine[k] = 0;
+  if (PHASE == 2)
+    for (int k = t; k < keys; k += kThreads) total[k] = earlier[k] = 0;
   __syncthreads();
+  if (PHASE == 2) {
+    for (int k = lane; k < keys; k += 64) {
+      int all = 0, before = 0;
+#pragma unroll 8
+      for (int c = wave; c < nchunks; c += kWaves) {
+        const int n = counts[(int64_t)c * keys + k];
+        all += n;
+        before += c < (int)blockIdx.x ? n : 0;
+      }
+      atomicAdd(&total[k], all);
+      atomicAdd(&earlier[k], before);
+    }
+  }
   walk(ids, i0, i1, groups, bits, [&](int, int key, int, int n, bool first) {
     if (first) mine[key] += n;
   });
@@ -118,11 +136,8 @@ __global__ __launch_bounds__(kThreads) void group_rows_kernel(
     if (PHASE == 0) {
       for (int w = 0; w < kWaves; ++w) all += hist[w * kStride + t];
     } else {
-      for (int c = 0; c < nchunks; ++c) {
-        const int n = counts[(int64_t)c * keys + t];
-        before += c < (int)blockIdx.x ? n : 0;
-        all += n;
-      }
+      all = total[t];
+      before = earlier[t];
     }
   }
   int incl = all;
@@ -150,8 +165,7 @@ __global__ __launch_bounds__(kThreads) void group_rows_kernel(
     // rows of no group: behind every group, after the earlier chunks' ones
     int at = 0;
     for (int w = 0; w < kWaves; ++w) at += wsum[w];
-    if (PHASE == 2)
-      for (int c = 0; c < (int)blockIdx.x; ++c) at += counts[(int64_t)c * keys + groups];
+    if (PHASE == 2) at += earlier[groups];
     for (int w = 0; w < kWaves; ++w) {
       const int n = hist[w * kStride + groups];
       hist[w * kStride + groups] = at;
