@@ -32,7 +32,10 @@
 // split K slice by slice; their sums meet in LDS in wave order.  WK > 1 is for
 // launches whose weight rows alone give the GPU too few waves.  With WN = 1 no
 // wave shares X and each loads its operands straight from memory, only the
-// lanes whose place exists (one token: 4 of 64).
+// lanes whose place exists (one token: 4 of 64).  16 waves over 16 places copy
+// X for two steps at once: no row twice, and half the barriers (one round of
+// 4096 deep workgroups 36.0 -> 32.8 us).
+#include <algorithm>
 #include <type_traits>
 
 #include "bnbx_rows_device.hpp"
@@ -49,19 +52,24 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   constexpr int TM = 16 * RB, TN = 16 * NB * WN, kThreads = WN * WK * 64;
   constexpr int kAhead = 2;   // units loaded ahead, per 16 weight rows
   constexpr bool DIRECT = WN == 1, DYN = DQ == kDqDynamic;
-  constexpr int kXBuf = DIRECT ? 0 : WK * TM * kSlice;   // 16-bit elements
-  constexpr int kXLoads = DIRECT ? 1 : RB * 8 / WN > 0 ? RB * 8 / WN : 1;   // 1 KB loads a wave
+  constexpr int XS = WN > RB * 8 ? 2 : 1;                // steps per X buffer
+  constexpr int kXPart = TM * kSlice;                    // 16-bit elements of one slice
+  constexpr int kXBuf = DIRECT ? 0 : XS * WK * kXPart;
+  constexpr int kXLoads = DIRECT ? 1 : XS * RB * 8 / WN;   // 1 KB loads a wave and buffer
   constexpr int kStages = WN * WK * 2048;
   constexpr int kRedBytes = (WK - 1) * WN * RB * NB * 1024;
   // LDS: the byte table (at offset 0: its addresses are v_perm results), X,
-  // the waves' stages, the dynamic map; the partial sums reuse all of it.
+  // the waves' stages, the dynamic map if there is room (else it is read from
+  // memory); the partial sums reuse all of it.
   constexpr int kLut = LUT ? kLutBytes : 0;
-  constexpr int kUsed = kLut + 2 * kXBuf * 2 + kStages + (DYN ? 1024 : 0);
+  constexpr int kBufs = kLut + 2 * kXBuf * 2 + kStages;
+  constexpr bool kMapLds = DYN && kBufs + 1024 <= 160 * 1024;
+  constexpr int kUsed = kBufs + (kMapLds ? 1024 : 0);
   constexpr int kLds = kUsed > kRedBytes ? kUsed : kRedBytes;
-  static_assert(DIRECT || RB * 8 % WN == 0 || WN > RB * 8, "X loads split evenly");
+  static_assert(DIRECT || XS * RB * 8 % WN == 0, "X loads split evenly");
   __shared__ __attribute__((aligned(256))) unsigned char smem[kLds];
 
-  float* const dmap = (float*)(smem + kLut + 2 * kXBuf * 2 + kStages);
+  const float* const dmap = kMapLds ? (const float*)(smem + kBufs) : kDynMapDev.v;
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wn = wave % WN, wk = wave / WN;
@@ -196,46 +204,48 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   for (int j = 0; j < NB; ++j) load_quad(quad_next[j], j, 0);
 
   if (LUT) lut_build(smem, lv, kThreads);
-  if (DYN)
-    for (int e = t; e < 256; e += kThreads) dmap[e] = kDynMapDev.v[e];
+  if (kMapLds)
+    for (int e = t; e < 256; e += kThreads) ((float*)(smem + kBufs))[e] = kDynMapDev.v[e];
 
   unsigned char* const stage = smem + kLut + 2 * kXBuf * 2 + wave * 2048;
   auto barrier = [] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
-  // X through LDS: the WN waves of one K part copy its slice, 2 rows an
-  // instruction (lane l: row l / 32, slot l % 32).  Rows past the tile repeat
-  // its first row (their results are never stored); chunks past K are zeros.
+  // X through LDS: the WN waves of one K part copy its slices of XS steps, 2
+  // rows an instruction (lane l: row l / 32, slot l % 32).  Rows past the tile
+  // repeat its first row (their results are never stored); chunks past K are
+  // zeros.
   uint16_t* const xs = (uint16_t*)(smem + kLut);
   const uint16_t* xp[kXLoads];
   int xk[kXLoads];
   uint32_t xslot[kXLoads];
   u32x4_t xv[kXLoads];
+  auto x_sub = [&](int i) { return XS == 1 ? 0 : (WN * i + wn) / (RB * 8); };   // step
   if (!DIRECT) {
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i) {
-      // more waves than pairs of rows: two waves copy the same rows
-      const int row = (2 * (wn * kXLoads + i) + (lane >> 5)) % TM;
+      const int row = 2 * ((XS == 1 ? wn * kXLoads + i : WN * i + wn) % (RB * 8)) + (lane >> 5);
       const int place = tile.r0 + row < tile.r1 ? tile.r0 + row : tile.r0;
       int xr = x_row_of(a, place);
       xr = xr < 0 ? 0 : xr;
       xp[i] = a.x + (int64_t)xr * a.ldx;
       xk[i] = 8 * ((lane & 31) ^ (row & 15));
-      xslot[i] = (uint32_t)((wk * TM + row) * kSlice + 8 * (lane & 31));
+      xslot[i] = (uint32_t)((x_sub(i) * WK + wk) * kXPart + row * kSlice + 8 * (lane & 31));
     }
   }
-  auto load_x = [&](int slice) {
+  auto load_x = [&](int s) {   // of steps s .. s + XS - 1
     if (DIRECT) return;
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i) {
-      const int k = slice * kSlice + xk[i];
+      const int k = slice_of(s + x_sub(i)) * kSlice + xk[i];
       xv[i] = *(const u32x4_t*)(xp[i] + (k < a.K ? k : 0));
     }
   };
-  auto put_x = [&](int buf, int slice) {
+  auto put_x = [&](int buf, int s) {
     if (DIRECT) return;
-    const bool tail = (slice + 1) * kSlice > a.K;   // uniform
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i) {
+      const int slice = slice_of(s + x_sub(i));
+      const bool tail = (slice + 1) * kSlice > a.K;   // uniform
       if (tail && slice * kSlice + xk[i] >= a.K) xv[i] = u32x4_t{0u, 0u, 0u, 0u};
       *(u32x4_t*)(xs + buf * kXBuf + xslot[i]) = xv[i];
     }
@@ -323,7 +333,7 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
       w[j][0] = op[j].w[0];
       w[j][1] = op[j].w[1];
     }
-    const uint16_t* xb = xs + (s & 1) * kXBuf + wk * TM * kSlice;
+    const uint16_t* xb = xs + (PH / XS & 1) * kXBuf + ((PH % XS) * WK + wk) * kXPart;
     if constexpr (LUT) {
       // Table reads (and X) of MFMA m + 1 go out before the products of m.
       float2 l2[2][NB][4];
@@ -383,9 +393,9 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
     }
   };
 
-  load_x(slice_of(0));
+  load_x(0);
   load_direct(slice_of(0));
-  put_x(0, slice_of(0));
+  put_x(0, 0);
   barrier();
   if (LUT)
 #pragma unroll
@@ -394,11 +404,14 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   // the loads issued since, and would wait for all of them where it cannot tell
   // how many.
   auto advance = [&](Unit (&u)[NB], int s, auto phase) {
-    load_x(slice_of(s + 1));
+    constexpr int PH = decltype(phase)::value;
+    if (PH % XS == 0) load_x(s + XS);
     step(u, s, phase);
     load_direct(slice_of(s + 1));
-    put_x((s + 1) & 1, slice_of(s + 1));
-    if (!DIRECT) barrier();
+    if (PH % XS == XS - 1) {
+      put_x(((PH + 1) / XS) & 1, s + 1);
+      if (!DIRECT) barrier();
+    }
   };
   for (int s = 0;;) {
     advance(un[LUT ? 1 : 0], s, std::integral_constant<int, 0>{});
@@ -410,7 +423,7 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
     advance(un[LUT ? 0 : 1], s, std::integral_constant<int, 3>{});
     if (++s >= nsteps) break;
   }
-  if (DIRECT) barrier();
+  if (DIRECT || XS > 1) barrier();
 
   // Low-rank term: the adapters whose places meet the tile, each in steps of
   // 32 ranks, shared out over the WK waves.  XA's two planes and, for fp16, B
@@ -567,24 +580,51 @@ hipError_t launch_rows_stream(const RowsGemm& a, int quant_type, bool f16, int c
   const int groups = a.offsets == nullptr ? 1 : (a.groups < a.rows ? a.groups : a.rows);
   const int mean_rows = (a.rows + groups - 1) / groups;
   const int rb = mean_rows <= 16 ? 1 : mean_rows <= 32 ? 2 : 4;
+  const int nslices = (a.K + kSlice - 1) / kSlice;
   // Row tiles the launch is likely to have, times 16-row weight slabs.
   const int64_t tm = 16 * rb;
   const int64_t slabs = (int64_t)groups * ((mean_rows + tm - 1) / tm) * ((a.N + 15) / 16);
-  // Few slabs (16 weight rows): one workgroup a slab, all its waves on K, up
-  // to two workgroups a CU; then 8 slabs a workgroup and K in two, while one
-  // round of them does; else 16 slabs a workgroup.  Measured on stacks of
-  // 4096 x 4096 and 14336 x 4096 in us: 512 slabs 17.7 / 22.4 / 35.5; 2048
-  // slabs 42.1 / 25.2 / 37.5; 7168 slabs 134 / 93 / 79.
+  // Waves split K where the slabs alone do not fill the GPU: the more of them
+  // share a workgroup's rows (WN), the better they use it, the more of them
+  // split K (WK), the fewer steps it takes.  Each form's time is its rounds of
+  // workgroups (one a CU) times one workgroup's: `ends` for its start and end
+  // and `step` a step, in us, fitted to kernel times over N = 512 .. 32768 and
+  // K = 1024 .. 14336 (within 10 %).  For instance 16 places, K = 4096, forms
+  // (WN, WK) = (2, 4), (4, 4), (8, 2), (16, 1): N = 8192 13.1 / 15.8 / 21.8 /
+  // 32.6; N = 16384 23.4 / 17.3 / 22.4 / 33.2; N = 24576 34.0 / 30.1 / 23.4 /
+  // 33.8.
+  auto cost = [&](int wn, int wk, double ends, double step) {
+    const int64_t wgs = (slabs + wn - 1) / wn;
+    const int steps = (nslices + wk - 1) / wk;
+    return (double)((wgs + cus - 1) / cus) * (ends + step * steps);
+  };
   if (rb == 1) {
-    if (slabs <= 2 * (int64_t)cus) return launch_one<1, 1, 1, 8, true>(a, quant_type, f16, stream);
-    if (slabs <= 8 * (int64_t)cus) return launch_one<1, 1, 8, 2, true>(a, quant_type, f16, stream);
+    // Up to 4 places: operands of X straight from memory, K in eight.  One
+    // place, 4096 x 4096: 8.4, against 11.9 with (2, 4); with 16 places 14.5
+    // against 12.1.
+    if (mean_rows <= 4 && slabs <= 2 * (int64_t)cus)
+      return launch_one<1, 1, 1, 8, true>(a, quant_type, f16, stream);
+    const double t2 = cost(2, 4, 6.5, 1.4), t4 = cost(4, 4, 6.5, 2.2),
+                 t8 = cost(8, 2, 6.5, 1.85), t16 = cost(16, 1, 6.5, 1.65);
+    const double least = std::min(std::min(t2, t4), std::min(t8, t16));
+    if (t2 <= least) return launch_one<1, 1, 2, 4, true>(a, quant_type, f16, stream);
+    if (t4 <= least) return launch_one<1, 1, 4, 4, true>(a, quant_type, f16, stream);
+    if (t8 <= least) return launch_one<1, 1, 8, 2, true>(a, quant_type, f16, stream);
     return launch_one<1, 1, 16, 1, true>(a, quant_type, f16, stream);
   }
   if (rb == 2) {
-    if (slabs <= 2 * (int64_t)cus) return launch_one<2, 1, 1, 8, true>(a, quant_type, f16, stream);
-    if (slabs <= 8 * (int64_t)cus) return launch_one<2, 1, 8, 1, true>(a, quant_type, f16, stream);
+    const double t2 = cost(2, 2, 7.0, 1.15), t4 = cost(4, 2, 6.5, 1.5),
+                 t8 = cost(8, 1, 6.5, 1.35), t16 = cost(16, 1, 7.5, 2.15);
+    const double least = std::min(std::min(t2, t4), std::min(t8, t16));
+    if (t2 <= least) return launch_one<2, 1, 2, 2, true>(a, quant_type, f16, stream);
+    if (t4 <= least) return launch_one<2, 1, 4, 2, true>(a, quant_type, f16, stream);
+    if (t8 <= least) return launch_one<2, 1, 8, 1, true>(a, quant_type, f16, stream);
     return launch_one<2, 1, 16, 1, true>(a, quant_type, f16, stream);
   }
+  // 64 places, K = 4096, forms (2, 2), (4, 2), (8, 1): N = 8192 23.7 / 25.4 /
+  // 35.9; N = 16384 45.0 / 27.5 / 37.2; N = 24576 66.8 / 50.0 / 38.7.
+  if (slabs <= 2 * (int64_t)cus) return launch_one<4, 1, 2, 2, false>(a, quant_type, f16, stream);
+  if (slabs <= 4 * (int64_t)cus) return launch_one<4, 1, 4, 2, false>(a, quant_type, f16, stream);
   return launch_one<4, 1, 8, 1, false>(a, quant_type, f16, stream);
 }
 
