@@ -83,6 +83,16 @@ def test_larger(m, adapters, rank, n, k, run, dtype):
     run_case(random_ids(m, adapters, m + n, run), adapters, rank, n, k, dtype=dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m,rank,n,k", [
+    (7, 48, 9000, 320), (7, 48, 15000, 1088), (12, 16, 30000, 256), (12, 80, 60000, 320),
+    (25, 48, 5000, 1088), (25, 80, 13000, 576), (25, 48, 25000, 256), (25, 16, 50000, 320),
+    (60, 80, 6000, 320), (60, 48, 13000, 576), (60, 48, 30000, 256)])
+def test_wide(m, rank, n, k, dtype):
+    """Many weight rows: the ranks shared out over one to eight waves."""
+    run_case(random_ids(m, 6, m + n), 6, rank, n, k, dtype=dtype)
+
+
 @pytest.mark.parametrize("m", [3, 50, 700])
 def test_one_adapter_for_all_and_none_at_all(m):
     run_case([0] * m, 1, 32, 200, 256)

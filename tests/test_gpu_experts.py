@@ -1,6 +1,8 @@
 """bnbx_gemm_nf4_experts (4-bit products grouped by expert) against binary64
 products on the dequantized weights, element by element."""
 
+import dataclasses
+
 import pytest
 import torch
 
@@ -82,6 +84,33 @@ def test_slots_of_tokens(topk):
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_larger(counts, n, k, dtype):
     run_case(counts, n, k, none=1, dtype=dtype)
+
+
+@pytest.mark.parametrize("dq,quant,dtype", TYPES)
+@pytest.mark.parametrize("k", [320, 512, 1088])
+@pytest.mark.parametrize("counts,n", [
+    ([6, 5, 9], 2000), ([6, 5, 9], 4200), ([6, 5, 9], 10000), ([6, 5, 9], 17000),
+    ([20, 25], 3000), ([20, 25], 7000), ([20, 25], 14000), ([20, 25], 30000),
+    ([50, 40], 3001), ([50, 40], 7000), ([50, 40], 17000)])
+def test_wide(counts, n, k, dq, quant, dtype):
+    """Few rows a group and many weight rows: every way to share them and K out
+    among waves, with row lengths of a multiple of four blocks and others."""
+    run_case(counts, n, k, none=1, dq=dq, quant=quant, dtype=dtype)
+
+
+@pytest.mark.parametrize("dq", ["linear", None])
+@pytest.mark.parametrize("rows", [1, 9, 24, 60, 900])
+def test_block_scales_at_any_address(rows, dq):
+    """Block codes and maxima that start at an element's own alignment only."""
+    q, _ = stack(2, 300, 1024, 41, dq)
+    plan = device_plan(ids_of([rows, 1], 42), 2)
+    x = rand((rows + 1, 1024), 43)
+    ref = T.gemm_experts(x, q, plan)
+    odd = torch.cat((q.absmax[:1], q.absmax))[1:]
+    assert odd.data_ptr() % 16 != 0
+    y = T.gemm_experts(x, dataclasses.replace(q, absmax=odd), plan)
+    torch.cuda.synchronize()
+    assert torch.equal(y, ref)
 
 
 def test_all_rows_of_no_group_leave_the_output():
