@@ -79,19 +79,19 @@ double rounds_of(const RowsGemm& a, int cols, int tm, int tn, int slots, double 
 // places x 256 columns, one a CU) take about 1.5 us per 64 k, those of the
 // streaming form (64 places x 128 columns, two a CU) about 1.0 us, each with a
 // full GPU.  Measured, 8 groups of N = K = 4096: 64 rows a group 69 us streaming
-// / 101 us tiled, 160 rows 122 / 105; one group, 333 rows, N = 4096, K = 11008:
-// 127 / 265.
+// / 106 us tiled, 160 rows 101 / 104, 256 rows 158 / 110; one group, 333 rows,
+// N = 4096, K = 11008: 93 / 229.
 bool prefer_tiles(const RowsGemm& a, int cus) {
   if (a.rows <= 32 * (int64_t)(a.offsets == nullptr ? 1 : a.groups)) return false;
   return 1.5 * rounds_of(a, a.N, 256, 256, cus, 0.5) < rounds_of(a, a.N, 64, 128, 2 * cus, 0.5);
 }
 
 // The same for the input gradient: 256 x 256 tiles at 2.0 us per 64 weight
-// rows, the streaming form's 32 places x 128 columns at 0.44 us.  Measured, 8
-// groups of N = K = 4096: 50 rows a group 53 us streaming / 128 us tiled, 128
-// rows 126 / 129, 256 rows 218 / 133.
+// rows, the streaming form's 32 places x 128 columns at 0.38 us.  Measured, 8
+// groups of N = K = 4096: 50 rows a group 49 us streaming / 126 us tiled, 128
+// rows 116 / 129, 160 rows 136 / 128, 256 rows 209 / 134.
 bool prefer_dx_tiles(const RowsGemm& a, int cus) {
-  return 4.5 * rounds_of(a, a.K, 256, 256, cus, 0.25) < rounds_of(a, a.K, 32, 128, cus, 0.25);
+  return 5.2 * rounds_of(a, a.K, 256, 256, cus, 0.25) < rounds_of(a, a.K, 32, 128, cus, 0.25);
 }
 
 // The products of both operators: the tiled form, or the streaming form (also
