@@ -231,6 +231,8 @@ class RowGroups:
                            ("order", self.order, self.order.numel())):
             if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous():
                 raise ValueError(f"plan: {name} must be a contiguous int32 vector of {n}")
+        if self.order.numel() >= 2 ** 31:
+            raise ValueError("plan: rows are numbered in 31 bits")
         if self.offsets.device != self.order.device:
             raise ValueError("plan: offsets and order are on different devices")
 
@@ -253,6 +255,8 @@ def _check_matrix(name: str, t: torch.Tensor, cols: int, dtype, device) -> None:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if t.stride(1) != 1 and t.numel() > 0:
         raise ValueError(f"{name} must have contiguous rows")
+    if t.shape[0] >= 2 ** 31:
+        raise ValueError(f"{name}: rows are numbered in 31 bits")
 
 
 def _ld(t: torch.Tensor) -> int:
@@ -264,11 +268,28 @@ def _ld(t: torch.Tensor) -> int:
 _HERE = contextlib.nullcontext()
 
 
-def _on(device):
-    """The device of the data as the current one, for the launch."""
+def _on(device, stream):
+    """The device of the data as the current one, for the launch, and a given
+    stream as its current stream: what is allocated or cleared for the call then
+    belongs to the stream that runs it."""
     if device.type != "cuda":
         raise ValueError(f"the data must be on a GPU, not on {device}")
-    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if stream is None:
+        return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device) if stream
+                  else torch.cuda.default_stream(device))
+    if stream.device != device:
+        raise ValueError(f"the stream is of {stream.device}, the data on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _scratch(workspace: torch.Tensor | None, nbytes: int, device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous and on {device}")
+    return workspace
 
 
 def empty_row_groups(rows: int, groups: int, device="cuda") -> RowGroups:
@@ -284,16 +305,17 @@ def group_rows(ids: torch.Tensor, groups: int, out: RowGroups | None = None,
     if ids.dtype != torch.int32 or ids.shape != (rows,) or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int32 vector")
     device = ids.device
-    plan = out if out is not None else empty_row_groups(rows, groups, device)
-    if plan.groups != groups or plan.rows != rows or plan.order.device != device:
+    if rows >= 2 ** 31:
+        raise ValueError("ids: rows are numbered in 31 bits")
+    if out is not None and (out.groups != groups or out.rows != rows
+                            or out.order.device != device):
         raise ValueError("out: a plan of other sizes, or on another device")
-    with _on(device):
+    with _on(device, stream):
+        plan = out if out is not None else empty_row_groups(rows, groups, device)
         nbytes = bnbx_group_rows_workspace_bytes(rows, groups)
-        if nbytes and workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        bnbx_group_rows(ids, rows, groups, plan.offsets, plan.order,
-                        workspace if nbytes else None,
-                        workspace.numel() * workspace.element_size() if nbytes else 0, stream)
+        ws = _scratch(workspace, nbytes, device) if nbytes else None
+        bnbx_group_rows(ids, rows, groups, plan.offsets, plan.order, ws,
+                        ws.numel() * ws.element_size() if nbytes else 0, stream)
     return plan
 
 
@@ -312,13 +334,14 @@ def _rows_product(call, name: str, t: torch.Tensor, q: QuantizedWeight, rows: Ro
     device = q.packed.device
     _check_matrix(name, t, cin, q.dtype, device)
     _check_plan(rows, device)
-    y = out if out is not None else torch.zeros(rows.rows, cout, dtype=q.dtype, device=device)
-    _check_matrix("out", y, cout, q.dtype, device)
+    if out is not None:
+        _check_matrix("out", out, cout, q.dtype, device)
     if gather < 0:
         raise ValueError("gather must be 0 or the slots per row")
-    if t.shape[0] * max(gather, 1) < rows.rows or y.shape[0] < rows.rows:
+    if t.shape[0] * max(gather, 1) < rows.rows or (out is not None and out.shape[0] < rows.rows):
         raise ValueError("fewer rows than the plan has places")
-    with _on(device):
+    with _on(device, stream):
+        y = out if out is not None else torch.zeros(rows.rows, cout, dtype=q.dtype, device=device)
         call(t, _ld(t), t.shape[0], q.packed, q.state, rows.desc, q.shape[1], q.shape[2], gather,
              int(scatter), y, _ld(y), y.shape[0], stream)
     return y
@@ -374,17 +397,17 @@ def linear_adapters(x: torch.Tensor, q: QuantizedWeight, rows: RowGroups, lora_a
         raise ValueError(f"the adapters must be on {device}")
     if lora_a.stride(2) != 1 or lora_b.stride(2) != 1 or (groups > 1 and scale.stride(0) != 1):
         raise ValueError("the adapters must have contiguous rows")
-    y = out if out is not None else torch.empty(rows.rows, N, dtype=q.dtype, device=device)
-    _check_matrix("out", y, N, q.dtype, device)
-    if y.shape[0] != rows.rows:
-        raise ValueError(f"out has {y.shape[0]} rows, the plan {rows.rows}")
+    if out is not None:
+        _check_matrix("out", out, N, q.dtype, device)
+        if out.shape[0] != rows.rows:
+            raise ValueError(f"out has {out.shape[0]} rows, the plan {rows.rows}")
     desc = AdaptersDesc(lora_a.data_ptr(), lora_b.data_ptr(), scale.data_ptr(), _row(lora_a),
                         lora_a.stride(0) if groups > 1 else 0, _row(lora_b),
                         lora_b.stride(0) if groups > 1 else 0, r)
-    with _on(device):
-        nbytes = bnbx_gemm_nf4_adapters_workspace_bytes(rows.rows, r)
-        if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with _on(device, stream):
+        y = out if out is not None else torch.empty(rows.rows, N, dtype=q.dtype, device=device)
+        workspace = _scratch(workspace, bnbx_gemm_nf4_adapters_workspace_bytes(rows.rows, r),
+                             device)
         bnbx_gemm_nf4_adapters(x, _ld(x), q.packed, q.state, rows.desc, N, K, desc, y, _ld(y),
                                workspace, workspace.numel() * workspace.element_size(), stream)
     return y

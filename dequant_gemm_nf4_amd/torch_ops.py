@@ -281,10 +281,11 @@ def _(ids, groups):
 
 
 def _rows_of(t: torch.Tensor) -> torch.Tensor:
-    """A 2-D operand as the kernels read it: contiguous rows, 16-byte aligned."""
-    if t.stride(-1) != 1 or t.stride(0) % 8 != 0 or t.data_ptr() % 16 != 0:
+    """A 2-D operand as the kernels read it: contiguous rows of their own (not
+    one row expanded), 16-byte aligned."""
+    if t.stride(-1) != 1 or t.stride(0) % 8 != 0 or t.stride(0) < t.shape[1]:
         t = t.contiguous()
-    return t
+    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 def _stack(dtype, packed, absmax, absmax2, absmax_mean, shape, quant_type) -> T.QuantizedWeight:

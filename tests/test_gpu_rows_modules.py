@@ -107,6 +107,61 @@ def test_token_gradient_is_the_sum_over_its_slots():
     assert torch.all((dx.double() - want).abs() <= 2.0 ** -8 * (size + want.abs()) * 1.02 + 1e-9)
 
 
+def test_expanded_and_unaligned_rows():
+    """One row expanded to all places, as input and as the gradient that a sum
+    over the rows hands back, and rows that start off 16 bytes."""
+    groups, d, n, rows = 3, 128, 192, 21
+    m = experts(groups, d, n, 21)
+    plan = torch.ops.bnbx.group_rows(torch.arange(rows, dtype=torch.int32, device="cuda") % groups,
+                                     groups)
+    one = rand((1, d), 22)
+    x = one.expand(rows, d)
+    assert torch.equal(m(x, plan, gather=1), m(x.contiguous(), plan, gather=1))
+    flat = torch.cat((one[0, :1], x.reshape(-1)))[1:].view(rows, d)
+    assert flat.data_ptr() % 16 != 0
+    assert torch.equal(m(flat, plan, gather=1), m(x.contiguous(), plan, gather=1))
+    x = rand((rows, d), 23).requires_grad_()
+    y = m(x, plan, gather=1, scatter=True)
+    v = rand((n,), 24)
+    (dx,) = torch.autograd.grad(y, x, v.expand(rows, n), retain_graph=True)
+    (ref,) = torch.autograd.grad(y, x, v.expand(rows, n).contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(dx, ref) and dx.abs().max() > 0
+    q = Linear4bitAdapters(d, n, 2, device="cuda").load_weight(rand((n, d), 25, 0.05))
+    q.load_adapter(1, rand((16, d), 26), rand((n, 16), 27))
+    plan = torch.ops.bnbx.group_rows(torch.ones(rows, dtype=torch.int32, device="cuda"), 2)
+    x = one.expand(rows, d)
+    assert torch.equal(q(x, plan), q(x.contiguous(), plan))
+
+
+def test_a_given_stream_runs_all_of_a_call():
+    """What a call allocates and clears runs on the stream it is given, not on
+    the busy current one."""
+    m = experts(2, 128, 64, 31)
+    q = m.quantized()
+    x = rand((40, 128), 32)
+    ids = torch.tensor([0, 1, -1, 1] * 10, dtype=torch.int32, device="cuda")
+    plan = T.group_rows(ids, 2)
+    ref = T.gemm_experts(x, q, plan, gather=1, scatter=True)
+    back = T.gemm_experts_dx(ref, q, plan, gather=1, scatter=True)
+    w = T.quantize(rand((64, 128), 33, 0.05), True)
+    a, b, scale = rand((2, 16, 128), 34), rand((2, 64, 16), 35), torch.ones(2, device="cuda")
+    low = T.linear_adapters(x, w, plan, a, b, scale)
+    big = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        for _ in range(8):
+            big = big @ big * 1e-3   # the current stream has work in front
+        made = T.group_rows(ids, 2, stream=stream)
+        y = T.gemm_experts(x, q, made, gather=1, scatter=True, stream=stream)
+        dx = T.gemm_experts_dx(y, q, made, gather=1, scatter=True, stream=stream)
+        z = T.linear_adapters(x, w, made, a, b, scale, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(made.order, plan.order)
+        assert torch.equal(y, ref) and torch.equal(dx, back) and torch.equal(z, low)
+
+
 def test_opcheck_and_compiled_equal_eager():
     m = Mixture(4, 128, 192, 2)
     ids, weights = routing(30, 4, 2, 21)

@@ -97,6 +97,8 @@ EXPERT_CASES = [
     (dict(st=state(4 * 128 * 128, absmax2=None)), INVAL),
     (dict(st=state(4 * 128 * 128, absmax2=D + 2)), ALIGN),
     (dict(st=state(4 * 128 * 128, dq=0, absmax=C + 2)), ALIGN),
+    # more tiles than the kernels count, were the groups to overlap
+    (dict(plan=plan(rows=2**31 - 1, groups=1024), st=state(1024 * 128 * 128)), UNSUP),
     # a weight past 32-bit offsets
     (dict(N=1 << 16, K=1 << 16, ldx=1 << 16, ldy=1 << 16, st=state(4 << 32)), UNSUP),
 ]
@@ -183,6 +185,27 @@ def test_a_plan_checks_its_arrays():
                            (torch.zeros(4, **i32), torch.zeros(6, dtype=torch.int64))):
         with pytest.raises(ValueError):
             T.RowGroups(3, offsets, order)
+
+
+def test_a_workspace_is_checked():
+    device = torch.device("meta")
+    assert T._scratch(None, 64, device).numel() == 64
+    given = torch.empty(16, device="meta")
+    assert T._scratch(given, 64, device) is given
+    for bad in (torch.empty(16), torch.empty(8, 8, device="meta")[:, :2]):
+        with pytest.raises(ValueError):
+            T._scratch(bad, 64, device)
+
+
+def test_rows_past_31_bits_are_refused():
+    with pytest.raises(ValueError):
+        T.RowGroups(1, torch.empty(2, dtype=torch.int32, device="meta"),
+                    torch.empty(2**31, dtype=torch.int32, device="meta"))
+    with pytest.raises(ValueError):
+        T.group_rows(torch.empty(2**31, dtype=torch.int32, device="meta"), 1)
+    with pytest.raises(ValueError):
+        T._check_matrix("x", torch.empty(2**31, 64, dtype=torch.bfloat16, device="meta"), 64,
+                        torch.bfloat16, torch.device("meta"))
 
 
 def test_group_rows_checks():
