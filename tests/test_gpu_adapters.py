@@ -104,6 +104,11 @@ def test_rows_alternate_between_all_adapters():
     run_case([i % 64 for i in range(640)], 64, 16, 300, 512)
 
 
+def test_most_adapters():
+    """1024 adapters, most without a row."""
+    run_case(random_ids(300, 1024, 51), 1024, 16, 48, 128)
+
+
 def test_no_rows():
     q, _ = stack(0, 64, 128, 5)
     y = T.linear_adapters(rand((0, 128), 1), q, device_plan([], 2), rand((2, 16, 128), 2),

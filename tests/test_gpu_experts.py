@@ -124,6 +124,11 @@ def test_all_rows_of_no_group_leave_the_output():
     assert torch.all(zero == 0)
 
 
+def test_most_groups():
+    """1024 groups: tiles found past the first 64 groups, several in some."""
+    run_case([2, 0, 0, 1] * 128 + [0] * 500 + [40] * 11 + [3], 48, 128, none=9)
+
+
 def test_no_rows():
     q, _ = stack(3, 64, 128, 5)
     plan = device_plan([], 3)

@@ -66,6 +66,11 @@ def test_larger(counts, n, k, dtype):
     run_case(counts, n, k, none=1, dtype=dtype)
 
 
+def test_most_groups():
+    """1024 groups: tiles found past the first 64 groups, several in some."""
+    run_case([2, 0, 0, 1] * 128 + [0] * 500 + [40] * 11 + [3], 64, 128, none=9)
+
+
 def test_against_differences_of_the_forward():
     """d/dx <dy, f(x)> along single inputs of a row: the forward is linear, so
     the difference of two forwards a unit apart, in binary64 over its 16-bit
