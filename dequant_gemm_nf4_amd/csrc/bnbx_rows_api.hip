@@ -3,6 +3,7 @@
 #include "../../include/bnbx_rows.h"
 #include "bnbx_checks.hpp"
 #include "bnbx_rows.hpp"
+#include "bnbx_rows_form.hpp"
 
 namespace bnbx {
 static_assert(kMaxGroups == BNBX_ROWS_MAX_GROUPS, "groups of a plan");
@@ -66,41 +67,13 @@ RowsGemm rows_gemm(const uint16_t* x, int64_t ldx, int x_rows, const uint8_t* pa
   return a;
 }
 
-// Rounds of workgroups that a launch over grouped rows takes on a GPU with
-// `slots` of them, from what the host knows: tiles of tm places and tn of the
-// `cols` columns, a group's last tile half full (and one tile at least); a
-// launch ends `late` rounds after its tiles have filled the GPU on average.
-double rounds_of(const RowsGemm& a, int cols, int tm, int tn, int slots, double late) {
-  const double groups = a.offsets == nullptr ? 1 : (a.groups < a.rows ? a.groups : a.rows);
-  double tiles = a.offsets == nullptr ? (a.rows + tm - 1) / tm : (double)a.rows / tm + 0.5 * groups;
-  tiles = tiles < groups ? groups : tiles;
-  const double r = tiles * ((cols + tn - 1) / tn) / slots + late;
-  return r < 1.0 ? 1.0 : r;
-}
-
-// Whether the tiled form is likely to be the faster one.  Its workgroups (256
-// places x 256 columns, one a CU) take about 1.5 us per 64 k, those of the
-// streaming form (64 places x 128 columns, two a CU) about 1.0 us, each with a
-// full GPU.  Measured, 8 groups of N = K = 4096: 64 rows a group 69 us streaming
-// / 106 us tiled, 160 rows 101 / 104, 256 rows 158 / 110; one group, 333 rows,
-// N = 4096, K = 11008: 93 / 229.
-bool prefer_tiles(const RowsGemm& a, int cus) {
-  if (a.rows <= 32 * (int64_t)(a.offsets == nullptr ? 1 : a.groups)) return false;
-  return 1.5 * rounds_of(a, a.N, 256, 256, cus, 0.5) < rounds_of(a, a.N, 64, 128, 2 * cus, 0.5);
-}
-
-// The same for the input gradient: 256 x 256 tiles at 2.0 us per 64 weight
-// rows, the streaming form's 32 places x 128 columns at 0.38 us.  Measured, 8
-// groups of N = K = 4096: 50 rows a group 49 us streaming / 126 us tiled, 128
-// rows 116 / 129, 160 rows 136 / 128, 256 rows 209 / 134.
-bool prefer_dx_tiles(const RowsGemm& a, int cus) {
-  return 5.2 * rounds_of(a, a.K, 256, 256, cus, 0.25) < rounds_of(a, a.K, 32, 128, cus, 0.25);
-}
+// The groups of a product as the choice of form counts them.
+int groups_of(const RowsGemm& a) { return a.offsets == nullptr ? 0 : a.groups; }
 
 // The products of both operators: the tiled form, or the streaming form (also
 // for an X past 32-bit offsets).
 hipError_t launch_rows(const RowsGemm& a, int quant_type, bool f16, int cus, hipStream_t hs) {
-  if (prefer_tiles(a, cus)) {
+  if (prefer_tiles(a.rows, groups_of(a), a.N, cus)) {
     const hipError_t e = a.lora.offsets != nullptr ? launch_rows_gemm_lora(a, quant_type, f16, hs)
                                                    : launch_rows_gemm(a, quant_type, f16, hs);
     if (e != hipErrorNotSupported) return e;
@@ -170,7 +143,7 @@ int bnbx_gemm_nf4_experts_dx(const uint16_t* dy, int64_t lddy, int dy_rows,
                                lddx, dx_rows);
   const bool f16 = st->compute_dtype == BNBX_DTYPE_F16;
   hipError_t e = hipErrorNotSupported;
-  if (prefer_dx_tiles(a, rows_cus()))
+  if (prefer_dx_tiles(a.rows, groups_of(a), a.K, rows_cus()))
     e = launch_rows_dx(a, st->quant_type, f16, (hipStream_t)stream);
   if (e == hipErrorNotSupported)
     e = launch_rows_dx_stream(a, st->quant_type, f16, (hipStream_t)stream);
