@@ -153,10 +153,13 @@ __device__ __forceinline__ Tab16 make_tab(const LevelTable& lv, float sc) {
 // values B is split into two bf16 parts, exactly (the product of both low
 // parts, 2^-17 of the term, is left out).
 //
-// Infinities and NaN of B would turn the other rows' zeros into NaN, so they
-// are left out of the products; returns whether the wave met any (then
-// rows_lora_odd adds their terms to their own rows).  The loop has
-// no branch around a product: with one, the accumulators spilled.
+// Infinities and NaN of B would turn the other rows' zeros into NaN, so the
+// products take 2^-126 with their sign instead (an infinite XA keeps its
+// infinity and its sign by it, and a finite one adds at most 4 to a sum that
+// is not finite in the end); returns whether the wave met any (then
+// rows_lora_odd adds their terms to their own rows).  With fp16 values an
+// infinite XA is left out of the products with B's low part, which may be zero.
+// The loop has no branch around a product: with one, the accumulators spilled.
 struct LoraSegs {
   int n, g[BM], s0[BM], s1[BM];   // adapters that meet the tile, rows [s0, s1) of it
 };
@@ -199,8 +202,6 @@ __device__ __forceinline__ bool rows_lora_term(f32x16_t (&acc)[8][2], const Lora
     bo[j] = n0 + 32 * j + col < N
                 ? (uint32_t)(n0 + 32 * j + col) * (uint32_t)lo.ldb * 2u + 16u * half
                 : kFar;
-  // exponent bits of a pair, all ones in a half that is not finite
-  constexpr uint32_t kExp = F16 ? 0x7c007c00u : 0x7f807f80u;
   uint32_t odd = 0;
   const int steps = r >> 4;
   const int total = __builtin_amdgcn_readfirstlane(segs.n) * steps;
@@ -222,25 +223,29 @@ __device__ __forceinline__ bool rows_lora_term(f32x16_t (&acc)[8][2], const Lora
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       bh[j] = __builtin_amdgcn_raw_buffer_load_b128(rb, bo[j], 2u * (uint32_t)k, 0);
+      if (F16) split_f16(bh[j], bh[j], bl[j]);
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
-        uint32_t v = bh[j][d];
-        const bool lo16 = (v & kExp & 0xffffu) == (kExp & 0xffffu);
-        const bool hi16 = (v & kExp & 0xffff0000u) == (kExp & 0xffff0000u);
-        odd |= lo16 || hi16 ? 1u : 0u;
-        v &= (lo16 ? 0xffff0000u : 0xffffffffu) & (hi16 ? 0xffffu : 0xffffffffu);
-        bh[j][d] = v;
+        const uint32_t v = bh[j][d], m = finite_halves(v);
+        odd |= ~m;
+        bh[j][d] = (m & v) | (~m & ((v & 0x80008000u) | 0x00800080u));
+        if (F16) bl[j][d] &= m;
       }
-      if (F16) split_f16(bh[j], bh[j], bl[j]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         acc[i][j] = mfma_32x32x16<false>(xh[i], bh[j], acc[i][j]);
         acc[i][j] = mfma_32x32x16<false>(xl[i], bh[j], acc[i][j]);
-        if (F16) acc[i][j] = mfma_32x32x16<false>(xh[i], bl[j], acc[i][j]);
       }
+      if (F16) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) xh[i][d] &= finite_halves(xh[i][d]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = mfma_32x32x16<false>(xh[i], bl[j], acc[i][j]);
+      }
+    }
     k += 16;
     if (k >= r) {
       k = 0;
@@ -252,14 +257,17 @@ __device__ __forceinline__ bool rows_lora_term(f32x16_t (&acc)[8][2], const Lora
 
 // What rows_lora_term leaves out, for columns n0 .. n0 + 63 of the stored
 // tile: the products of XA with the infinities and NaN of the row's adapter's
-// B (a sum that is not finite: added to the rounded Y it gives what it would
-// have given before the rounding).  Rare, so one lane walks one column.
+// B.  Their sum is not finite, so added to the rounded Y it gives what it would
+// have given before the rounding, but for a Y that is infinite by its rounding
+// only: `inf` has a bit for every accumulator of the wave that is not finite
+// (as gemm_kernel's epilogue holds them).  Rare, so one lane walks one column.
 template <bool F16>
 __device__ __forceinline__ void rows_lora_odd(const LoraRows& lo, int m0, int M, int n0, int N,
-                                              const int* yrow, uint16_t* y, int64_t ldy) {
+                                              const int* yrow, const uint64_t* inf, uint16_t* y,
+                                              int64_t ldy) {
   // the wave's own stores of Y, which other lanes made, before reading it
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
-  const int n = n0 + (int)(threadIdx.x & 63);
+  const int lane = threadIdx.x & 63, n = n0 + lane;
   if (n >= N) return;
   for (int g = 0; g < lo.adapters; ++g) {
     int p0 = lo.offsets[g], p1 = lo.offsets[g + 1];
@@ -267,18 +275,27 @@ __device__ __forceinline__ void rows_lora_odd(const LoraRows& lo, int m0, int M,
     p1 = p1 < M ? p1 : M;
     if (p0 >= p1) continue;
     const uint16_t* const b = lo.b + (int64_t)g * lo.stride_b + (int64_t)n * lo.ldb;
-    for (int k = 0; k < lo.r; ++k) {
-      const float v = F16 ? (float)__builtin_bit_cast(_Float16, b[k]) : bf16lo_to_f32(b[k]);
-      if (__builtin_isfinite(v)) continue;
-      for (int p = p0; p < p1; ++p) {
-        const int row = yrow[p - m0];
-        if (row < 0) continue;
+    auto value = [&](int k) {
+      return F16 ? (float)__builtin_bit_cast(_Float16, b[k]) : bf16lo_to_f32(b[k]);
+    };
+    int k0 = 0;
+    while (k0 < lo.r && __builtin_isfinite(value(k0))) ++k0;
+    if (k0 == lo.r) continue;
+    for (int p = p0; p < p1; ++p) {
+      const int row = yrow[p - m0];
+      if (row < 0) continue;
+      float term = 0.0f;
+      for (int k = k0; k < lo.r; ++k) {
+        const float v = value(k);
+        if (__builtin_isfinite(v)) continue;
         const uint16_t* const xa = lo.xa + (int64_t)p * 2 * lo.r + k;
-        const float term = (bf16lo_to_f32(xa[0]) + bf16lo_to_f32(xa[lo.r])) * v;
-        uint16_t* const o = y + (int64_t)row * ldy + n;
-        const float was = F16 ? (float)__builtin_bit_cast(_Float16, *o) : bf16lo_to_f32(*o);
-        *o = f32_to_16<F16>(was + term);
+        term += (bf16lo_to_f32(xa[0]) + bf16lo_to_f32(xa[lo.r])) * v;
       }
+      uint16_t* const o = y + (int64_t)row * ldy + n;
+      float was = F16 ? (float)__builtin_bit_cast(_Float16, *o) : bf16lo_to_f32(*o);
+      const int t = p - m0, acc = ((t >> 5) * 2 + (lane >> 5)) * 16 + 4 * ((t >> 3) & 3) + (t & 3);
+      if (!((inf[acc] >> (32 * ((t >> 2) & 1) + (lane & 31))) & 1)) was = 0.0f;
+      *o = f32_to_16<F16>(was + term);
     }
   }
 }
@@ -649,6 +666,9 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(
   int lane_e;
   asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(lane_e));
   const int col_e = lane_e & 31, half_e = lane_e >> 5;
+  // The wave's accumulators that are not finite, one bit each (LORA with ROWS,
+  // read by rows_lora_odd); the X buffers are free behind the last step's barrier.
+  [[maybe_unused]] uint64_t* const inf = (uint64_t*)As0 + wave * 256;
 
   // D layout of a 32x32 MFMA tile: lane l, value v -> column l%32,
   // row 8*(v/4) + 4*(l/32) + v%4.
@@ -670,13 +690,17 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(
         } else if constexpr (ROWS) {
           const int row = yrow[r - m0];
           if (row >= 0 && c < N) y[(int64_t)row * ldy + c] = f32_to_16<F16>(acc[i][j][v]);
+          if (LORA && odd) {
+            const uint64_t mask = __ballot(!__builtin_isfinite(acc[i][j][v]));
+            if (lane_e == 0) inf[(i * 2 + j) * 16 + v] = mask;
+          }
         } else {
           if (r < M && c < N) y[(int64_t)r * ldy + c] = f32_to_16<F16>(acc[i][j][v]);
         }
       }
     }
   if constexpr (LORA && ROWS)
-    if (odd) rows_lora_odd<F16>(rows.lora, m0, M, n0 + wave * 64, N, yrow, y, ldy);
+    if (odd) rows_lora_odd<F16>(rows.lora, m0, M, n0 + wave * 64, N, yrow, inf, y, ldy);
 }
 
 }  // namespace

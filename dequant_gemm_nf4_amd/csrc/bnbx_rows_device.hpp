@@ -160,7 +160,8 @@ __device__ __forceinline__ float2 lut_pair(const unsigned char* lds, uint32_t d,
 
 // Eight binary16 values as two bf16 operands, hi + lo, exactly: binary16 has
 // 11 significant bits, bf16 8, and the rest fits lo (bf16 reaches far below
-// binary16's subnormals).
+// binary16's subnormals).  An infinity or NaN leaves NaN in lo: the caller masks
+// it.
 __device__ __forceinline__ void split_f16(u32x4_t v, u32x4_t& hi, u32x4_t& lo) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -171,6 +172,13 @@ __device__ __forceinline__ void split_f16(u32x4_t v, u32x4_t& hi, u32x4_t& lo) {
     const float ra = a - bf16lo_to_f32(h), rb = b - bf16hi_to_f32(h);
     lo[k] = pack_bf16x2(ra, rb);
   }
+}
+
+// Ones in the halves of a bf16 pair that are neither infinite nor NaN.
+__device__ __forceinline__ uint32_t finite_halves(uint32_t v) {
+  const uint32_t lo = (v & 0x7f80u) == 0x7f80u ? 0u : 0xffffu;
+  const uint32_t hi = (v & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u;
+  return lo | hi;
 }
 
 }  // namespace bnbx

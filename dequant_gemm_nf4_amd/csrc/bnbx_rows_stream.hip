@@ -433,7 +433,10 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   // split into two bf16 parts (11 bits: exact) keep the term's error at 2^-16
   // of it; products run in bf16 for the range.  Each adapter's term is summed
   // apart and added to its own places only, so one adapter's infinities never
-  // reach another request's row.
+  // reach another request's row.  An infinity is in the high parts alone: the
+  // low part of an infinite XA is zero, and the products with a low part take
+  // zero for an infinity or NaN of the other operand (infinity times a low
+  // part of zero, or of the other sign, would turn the term into NaN).
   if (a.lora.offsets != nullptr) {
     const LoraRows& lo = a.lora;
     int seg = 0;
@@ -458,7 +461,7 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
         for (int k = 0; k < lo.r; k += 32, ++seg) {
           if (seg % WK != wk) continue;   // uniform in the wave
           const int k8 = k + 8 * q;
-          u32x4_t bh[NB], bl[NB];
+          u32x4_t bh[NB], bf[NB], bl[NB];   // bf: bh's finite values
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
             const int n = n0 + 16 * j + r;
@@ -466,6 +469,12 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
             if (k8 < lo.r && n < a.N) v = *(const u32x4_t*)(bb + (int64_t)n * lo.ldb + k8);
             bh[j] = v;
             if (F16) split_f16(v, bh[j], bl[j]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t m = finite_halves(bh[j][e]);
+              bf[j][e] = bh[j][e] & m;
+              if (F16) bl[j][e] &= m;
+            }
           }
 #pragma unroll
           for (int i = 0; i < RB; ++i) {
@@ -476,11 +485,15 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
               xh = *(const u32x4_t*)xa;
               xl = *(const u32x4_t*)(xa + lo.r);
             }
+            u32x4_t xf = xh;   // xh's finite values
+            if (F16)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) xf[e] &= finite_halves(xh[e]);
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
               term[j][i] = mfma_16x16x32<false>(bh[j], xh, term[j][i]);
-              term[j][i] = mfma_16x16x32<false>(bh[j], xl, term[j][i]);
-              if (F16) term[j][i] = mfma_16x16x32<false>(bl[j], xh, term[j][i]);
+              term[j][i] = mfma_16x16x32<false>(bf[j], xl, term[j][i]);
+              if (F16) term[j][i] = mfma_16x16x32<false>(bl[j], xf, term[j][i]);
             }
           }
         }

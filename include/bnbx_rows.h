@@ -131,7 +131,9 @@ BNBX_ROWS_API size_t bnbx_gemm_nf4_adapters_workspace_bytes(int rows, int r);
  * any number of them, and must list every row in `order`: a row it does not
  * list is not written.  Values are of st->compute_dtype; both products
  * accumulate in fp32, X . A_g^T keeps 16 significant bits, and Y is rounded
- * once.  An adapter with infinities or NaN reaches its own rows only.
+ * once.  An adapter with infinities or NaN reaches its own rows only, and gives
+ * them what the formula gives: a signed infinity, or NaN for 0 . inf and
+ * inf - inf.
  *   x, packed, st, N, K  as bnbx_gemm_nf4 (st->n = N * K)
  *   y          device, row m at y + m*ldy; ldy >= N (written)
  *   workspace  device, >= bnbx_gemm_nf4_adapters_workspace_bytes(...) bytes,
