@@ -154,12 +154,11 @@ __device__ __forceinline__ Tab16 make_tab(const LevelTable& lv, float sc) {
 // parts, 2^-17 of the term, is left out).
 //
 // Infinities and NaN of B would turn the other rows' zeros into NaN, so the
-// products take 2^-126 with their sign instead (an infinite XA keeps its
-// infinity and its sign by it, and a finite one adds at most 4 to a sum that
-// is not finite in the end); returns whether the wave met any (then
-// rows_lora_odd adds their terms to their own rows).  With fp16 values an
-// infinite XA is left out of the products with B's low part, which may be zero.
-// The loop has no branch around a product: with one, the accumulators spilled.
+// products take +-2^-126 instead (an infinite XA keeps its infinity and its
+// sign by it, and a finite one adds at most 4 to a sum that is not finite in
+// the end); returns whether the wave met any (then rows_lora_odd adds their
+// terms to their own rows).  No branch around a product: with one, the
+// accumulators spilled.
 struct LoraSegs {
   int n, g[BM], s0[BM], s1[BM];   // adapters that meet the tile, rows [s0, s1) of it
 };
@@ -202,7 +201,7 @@ __device__ __forceinline__ bool rows_lora_term(f32x16_t (&acc)[8][2], const Lora
     bo[j] = n0 + 32 * j + col < N
                 ? (uint32_t)(n0 + 32 * j + col) * (uint32_t)lo.ldb * 2u + 16u * half
                 : kFar;
-  uint32_t odd = 0;
+  uint64_t any = 0;   // lanes that met one
   const int steps = r >> 4;
   const int total = __builtin_amdgcn_readfirstlane(segs.n) * steps;
   int sg = 0, k = 0;
@@ -220,39 +219,42 @@ __device__ __forceinline__ bool rows_lora_term(f32x16_t (&acc)[8][2], const Lora
       xh[i] = __builtin_amdgcn_raw_buffer_load_b128(ra, xo, 2u * (uint32_t)k, 0);
       xl[i] = __builtin_amdgcn_raw_buffer_load_b128(ra, xo, 2u * (uint32_t)(r + k), 0);
     }
+    uint32_t odd = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       bh[j] = __builtin_amdgcn_raw_buffer_load_b128(rb, bo[j], 2u * (uint32_t)k, 0);
       if (F16) split_f16(bh[j], bh[j], bl[j]);
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const uint32_t v = bh[j][d], m = finite_halves(v);
-        odd |= ~m;
-        bh[j][d] = (m & v) | (~m & ((v & 0x80008000u) | 0x00800080u));
-        if (F16) bl[j][d] &= m;
-      }
+      for (int d = 0; d < 4; ++d) odd |= odd_halves(bh[j][d]);
     }
+    // 2048 rows beside 8192 x 8192, rank 256, with this branch and without:
+    // bf16 368 / 384 us, fp16 389 / 372
+    const uint64_t met = __ballot(odd != 0);
+    if (F16 || __builtin_expect(met != 0, false)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          bh[j][d] = tame_halves(bh[j][d], odd_halves(bh[j][d]));
+          if (F16) bl[j][d] = tame_halves(bl[j][d], odd_halves(bl[j][d]));
+        }
+    }
+    any |= met;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         acc[i][j] = mfma_32x32x16<false>(xh[i], bh[j], acc[i][j]);
         acc[i][j] = mfma_32x32x16<false>(xl[i], bh[j], acc[i][j]);
+        if (F16) acc[i][j] = mfma_32x32x16<false>(xh[i], bl[j], acc[i][j]);
       }
-      if (F16) {
-#pragma unroll
-        for (int d = 0; d < 4; ++d) xh[i][d] &= finite_halves(xh[i][d]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mfma_32x32x16<false>(xh[i], bl[j], acc[i][j]);
-      }
-    }
     k += 16;
     if (k >= r) {
       k = 0;
       ++sg;
     }
   }
-  return __ballot(odd != 0) != 0;
+  return any != 0;
 }
 
 // What rows_lora_term leaves out, for columns n0 .. n0 + 63 of the stored
@@ -260,10 +262,10 @@ __device__ __forceinline__ bool rows_lora_term(f32x16_t (&acc)[8][2], const Lora
 // B.  Their sum is not finite, so added to the rounded Y it gives what it would
 // have given before the rounding, but for a Y that is infinite by its rounding
 // only: `inf` has a bit for every accumulator of the wave that is not finite
-// (as gemm_kernel's epilogue holds them).  Rare, so one lane walks one column.
+// (16 bits a lane and 32 x 32 tile).  Rare, so one lane walks one column.
 template <bool F16>
 __device__ __forceinline__ void rows_lora_odd(const LoraRows& lo, int m0, int M, int n0, int N,
-                                              const int* yrow, const uint64_t* inf, uint16_t* y,
+                                              const int* yrow, const uint16_t* inf, uint16_t* y,
                                               int64_t ldy) {
   // the wave's own stores of Y, which other lanes made, before reading it
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
@@ -293,8 +295,8 @@ __device__ __forceinline__ void rows_lora_odd(const LoraRows& lo, int m0, int M,
       }
       uint16_t* const o = y + (int64_t)row * ldy + n;
       float was = F16 ? (float)__builtin_bit_cast(_Float16, *o) : bf16lo_to_f32(*o);
-      const int t = p - m0, acc = ((t >> 5) * 2 + (lane >> 5)) * 16 + 4 * ((t >> 3) & 3) + (t & 3);
-      if (!((inf[acc] >> (32 * ((t >> 2) & 1) + (lane & 31))) & 1)) was = 0.0f;
+      const int t = p - m0, tile = (t >> 5) * 2 + (lane >> 5), v = 4 * ((t >> 3) & 3) + (t & 3);
+      if (!((inf[tile * 64 + 32 * ((t >> 2) & 1) + (lane & 31)] >> v) & 1)) was = 0.0f;
       *o = f32_to_16<F16>(was + term);
     }
   }
@@ -666,9 +668,6 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(
   int lane_e;
   asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(lane_e));
   const int col_e = lane_e & 31, half_e = lane_e >> 5;
-  // The wave's accumulators that are not finite, one bit each (LORA with ROWS,
-  // read by rows_lora_odd); the X buffers are free behind the last step's barrier.
-  [[maybe_unused]] uint64_t* const inf = (uint64_t*)As0 + wave * 256;
 
   // D layout of a 32x32 MFMA tile: lane l, value v -> column l%32,
   // row 8*(v/4) + 4*(l/32) + v%4.
@@ -690,17 +689,28 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(
         } else if constexpr (ROWS) {
           const int row = yrow[r - m0];
           if (row >= 0 && c < N) y[(int64_t)row * ldy + c] = f32_to_16<F16>(acc[i][j][v]);
-          if (LORA && odd) {
-            const uint64_t mask = __ballot(!__builtin_isfinite(acc[i][j][v]));
-            if (lane_e == 0) inf[(i * 2 + j) * 16 + v] = mask;
-          }
         } else {
           if (r < M && c < N) y[(int64_t)r * ldy + c] = f32_to_16<F16>(acc[i][j][v]);
         }
       }
     }
-  if constexpr (LORA && ROWS)
-    if (odd) rows_lora_odd<F16>(rows.lora, m0, M, n0 + wave * 64, N, yrow, inf, y, ldy);
+  if constexpr (LORA && ROWS) {
+    if (__builtin_expect(odd, false)) {
+      // 16 bits a lane and tile: its accumulators that are not finite (the X
+      // buffers are free behind the last step's barrier)
+      uint16_t* const inf = As0 + wave * 1024;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t bits = 0;
+#pragma unroll
+          for (int v = 0; v < 16; ++v) bits |= __builtin_isfinite(acc[i][j][v]) ? 0u : 1u << v;
+          inf[(i * 2 + j) * 64 + lane_e] = (uint16_t)bits;
+        }
+      rows_lora_odd<F16>(rows.lora, m0, M, n0 + wave * 64, N, yrow, inf, y, ldy);
+    }
+  }
 }
 
 }  // namespace

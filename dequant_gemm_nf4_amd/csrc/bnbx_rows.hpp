@@ -14,8 +14,8 @@ hipError_t launch_group_rows(const int32_t* ids, int rows, int groups, int32_t* 
 
 // Low-rank term of the adapters product, Y_i += XA_i . B_g^T for the places
 // i of adapter g.  XA is held as two bf16 planes (hi + lo, together 16
-// significant bits of the fp32 sum) per place: place i's hi plane at
-// xa + 2 i r, its lo plane r further.
+// significant bits of the fp32 sum; bnbx_rows_lora.hip says how infinities are
+// held) per place: place i's hi plane at xa + 2 i r, its lo plane r further.
 struct LoraRows {
   const int32_t* offsets;   // the adapters' bounds, null: no low-rank term
   int adapters;

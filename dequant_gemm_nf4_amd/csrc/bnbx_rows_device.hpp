@@ -160,8 +160,8 @@ __device__ __forceinline__ float2 lut_pair(const unsigned char* lds, uint32_t d,
 
 // Eight binary16 values as two bf16 operands, hi + lo, exactly: binary16 has
 // 11 significant bits, bf16 8, and the rest fits lo (bf16 reaches far below
-// binary16's subnormals).  An infinity or NaN leaves NaN in lo: the caller masks
-// it.
+// binary16's subnormals).  An infinity or NaN leaves NaN in lo, which the
+// caller replaces.
 __device__ __forceinline__ void split_f16(u32x4_t v, u32x4_t& hi, u32x4_t& lo) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -174,11 +174,16 @@ __device__ __forceinline__ void split_f16(u32x4_t v, u32x4_t& hi, u32x4_t& lo) {
   }
 }
 
-// Ones in the halves of a bf16 pair that are neither infinite nor NaN.
-__device__ __forceinline__ uint32_t finite_halves(uint32_t v) {
-  const uint32_t lo = (v & 0x7f80u) == 0x7f80u ? 0u : 0xffffu;
-  const uint32_t hi = (v & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u;
-  return lo | hi;
+// The top bits of the halves of a bf16 pair that are infinite or NaN (there,
+// and only there, one more in the exponent carries into the sign's place).
+__device__ __forceinline__ uint32_t odd_halves(uint32_t v) {
+  return ((v & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+// The pair with +-2^-126, by their sign, in the halves of `odd` (of
+// odd_halves).  As a partner of an infinity it leaves the infinity its sign.
+__device__ __forceinline__ uint32_t tame_halves(uint32_t v, uint32_t odd) {
+  const uint32_t m = (odd << 1) - (odd >> 15);   // all bits of those halves
+  return (v & ~m) | (((v & 0x80008000u) | 0x00800080u) & m);
 }
 
 }  // namespace bnbx

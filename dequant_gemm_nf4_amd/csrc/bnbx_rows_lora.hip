@@ -2,7 +2,10 @@
 //   XA_i = s_g (X_i . A_g^T)   (A_g [r, K], fp32 accumulation),
 // stored as two bf16 planes, hi = bf16(XA) and lo = bf16(XA - hi): together 16
 // significant bits, in bf16's range, so that neither compute type costs the
-// low-rank term accuracy or range before it joins the 4-bit product.
+// low-rank term accuracy or range before it joins the 4-bit product.  An
+// infinity or NaN is held in lo, beside hi = +-2^-126: of the up-projection's
+// products hi . B, lo . B and (fp16, B's own low part) hi . B_lo, the last must
+// not see it (B_lo may be zero), and the first gives an infinite B its sign.
 //
 // Bound: reading the adapters' A (a decode batch reads a new A for nearly every
 // row) or X (a prefill), and at one token the latency of one dependent load
@@ -112,10 +115,12 @@ __global__ __launch_bounds__(kThreads) void rows_lora_down_kernel(RowsGemm a, Lo
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) sum += red[w][c][l][v];
       const float o = s * sum;
-      const uint16_t hi = f32_to_bf16(o);
-      const float hf = bf16lo_to_f32(hi);
-      // an infinite hi stands alone (inf - inf would make the term NaN)
-      const uint16_t lo = __builtin_isfinite(hf) ? f32_to_bf16(o - hf) : (uint16_t)0;
+      uint16_t hi = f32_to_bf16(o);
+      uint16_t lo = f32_to_bf16(o - bf16lo_to_f32(hi));
+      if ((hi & 0x7f80) == 0x7f80) {   // infinite or NaN: in the lo plane
+        lo = hi;
+        hi = (uint16_t)((hi & 0x8000) | 0x0080);
+      }
       uint16_t* const out = xa + (int64_t)p * 2 * d.r + rank;
       out[0] = hi;
       out[d.r] = lo;

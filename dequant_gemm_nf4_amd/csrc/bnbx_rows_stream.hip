@@ -433,10 +433,9 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   // split into two bf16 parts (11 bits: exact) keep the term's error at 2^-16
   // of it; products run in bf16 for the range.  Each adapter's term is summed
   // apart and added to its own places only, so one adapter's infinities never
-  // reach another request's row.  An infinity is in the high parts alone: the
-  // low part of an infinite XA is zero, and the products with a low part take
-  // zero for an infinity or NaN of the other operand (infinity times a low
-  // part of zero, or of the other sign, would turn the term into NaN).
+  // reach another request's row.  An infinite or NaN B meets XA's high part as
+  // it is, and the low part, which may be zero or of the other sign, as
+  // +-2^-126.
   if (a.lora.offsets != nullptr) {
     const LoraRows& lo = a.lora;
     int seg = 0;
@@ -461,39 +460,47 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
         for (int k = 0; k < lo.r; k += 32, ++seg) {
           if (seg % WK != wk) continue;   // uniform in the wave
           const int k8 = k + 8 * q;
-          u32x4_t bh[NB], bf[NB], bl[NB];   // bf: bh's finite values
+          // every load before the first use of one
+          u32x4_t bh[NB], bt[NB], bl[NB], xh[RB], xl[RB];   // bt: bh for xl
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
             const int n = n0 + 16 * j + r;
-            u32x4_t v = {0u, 0u, 0u, 0u};
-            if (k8 < lo.r && n < a.N) v = *(const u32x4_t*)(bb + (int64_t)n * lo.ldb + k8);
-            bh[j] = v;
-            if (F16) split_f16(v, bh[j], bl[j]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t m = finite_halves(bh[j][e]);
-              bf[j][e] = bh[j][e] & m;
-              if (F16) bl[j][e] &= m;
-            }
+            bh[j] = u32x4_t{0u, 0u, 0u, 0u};
+            if (k8 < lo.r && n < a.N) bh[j] = *(const u32x4_t*)(bb + (int64_t)n * lo.ldb + k8);
           }
 #pragma unroll
           for (int i = 0; i < RB; ++i) {
             const int place = tile.r0 + 16 * i + r;
-            u32x4_t xh = {0u, 0u, 0u, 0u}, xl = {0u, 0u, 0u, 0u};
+            xh[i] = xl[i] = u32x4_t{0u, 0u, 0u, 0u};
             if (k8 < lo.r && place < tile.r1 && place >= s0 && place < s1) {
               const uint16_t* xa = lo.xa + (int64_t)place * 2 * lo.r + k8;
-              xh = *(const u32x4_t*)xa;
-              xl = *(const u32x4_t*)(xa + lo.r);
+              xh[i] = *(const u32x4_t*)xa;
+              xl[i] = *(const u32x4_t*)(xa + lo.r);
             }
-            u32x4_t xf = xh;   // xh's finite values
-            if (F16)
+          }
 #pragma unroll
-              for (int e = 0; e < 4; ++e) xf[e] &= finite_halves(xh[e]);
+          for (int j = 0; j < NB; ++j) {
+            if (F16) split_f16(bh[j], bh[j], bl[j]);
+            bt[j] = bh[j];
+            uint32_t odd = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) odd |= odd_halves(bh[j][e]);
+            if (__builtin_expect(__ballot(odd != 0) != 0, false)) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                bt[j][e] = tame_halves(bh[j][e], odd_halves(bh[j][e]));
+                // (a low part is NaN where the value is not finite)
+                if (F16) bl[j][e] = tame_halves(bl[j][e], odd_halves(bl[j][e]));
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < RB; ++i) {
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
-              term[j][i] = mfma_16x16x32<false>(bh[j], xh, term[j][i]);
-              term[j][i] = mfma_16x16x32<false>(bf[j], xl, term[j][i]);
-              if (F16) term[j][i] = mfma_16x16x32<false>(bl[j], xf, term[j][i]);
+              term[j][i] = mfma_16x16x32<false>(bh[j], xh[i], term[j][i]);
+              term[j][i] = mfma_16x16x32<false>(bt[j], xl[i], term[j][i]);
+              if (F16) term[j][i] = mfma_16x16x32<false>(bl[j], xh[i], term[j][i]);
             }
           }
         }
