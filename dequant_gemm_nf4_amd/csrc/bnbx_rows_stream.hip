@@ -460,16 +460,11 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
         for (int k = 0; k < lo.r; k += 32, ++seg) {
           if (seg % WK != wk) continue;   // uniform in the wave
           const int k8 = k + 8 * q;
-          // every load before the first use of one
+          // XA's loads go out before the first use of B, but with 64 places,
+          // where their registers would cost the second workgroup of the CU
+          constexpr bool kEarly = RB <= 2;
           u32x4_t bh[NB], bt[NB], bl[NB], xh[RB], xl[RB];   // bt: bh for xl
-#pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            const int n = n0 + 16 * j + r;
-            bh[j] = u32x4_t{0u, 0u, 0u, 0u};
-            if (k8 < lo.r && n < a.N) bh[j] = *(const u32x4_t*)(bb + (int64_t)n * lo.ldb + k8);
-          }
-#pragma unroll
-          for (int i = 0; i < RB; ++i) {
+          auto load_xa = [&](int i) {
             const int place = tile.r0 + 16 * i + r;
             xh[i] = xl[i] = u32x4_t{0u, 0u, 0u, 0u};
             if (k8 < lo.r && place < tile.r1 && place >= s0 && place < s1) {
@@ -477,7 +472,16 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
               xh[i] = *(const u32x4_t*)xa;
               xl[i] = *(const u32x4_t*)(xa + lo.r);
             }
+          };
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            const int n = n0 + 16 * j + r;
+            bh[j] = u32x4_t{0u, 0u, 0u, 0u};
+            if (k8 < lo.r && n < a.N) bh[j] = *(const u32x4_t*)(bb + (int64_t)n * lo.ldb + k8);
           }
+          if (kEarly)
+#pragma unroll
+            for (int i = 0; i < RB; ++i) load_xa(i);
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
             if (F16) split_f16(bh[j], bh[j], bl[j]);
@@ -496,6 +500,7 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
           }
 #pragma unroll
           for (int i = 0; i < RB; ++i) {
+            if (!kEarly) load_xa(i);
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
               term[j][i] = mfma_16x16x32<false>(bh[j], xh[i], term[j][i]);
