@@ -73,9 +73,11 @@ int groups_of(const RowsGemm& a) { return a.offsets == nullptr ? 0 : a.groups; }
 // The products of both operators: the tiled form, or the streaming form (also
 // for an X past 32-bit offsets).
 hipError_t launch_rows(const RowsGemm& a, int quant_type, bool f16, int cus, hipStream_t hs) {
-  if (prefer_tiles(a.rows, groups_of(a), a.N, cus)) {
-    const hipError_t e = a.lora.offsets != nullptr ? launch_rows_gemm_lora(a, quant_type, f16, hs)
-                                                   : launch_rows_gemm(a, quant_type, f16, hs);
+  const bool low_rank = a.lora.offsets != nullptr;
+  if (prefer_tiles(a.rows, groups_of(a), a.N, a.K, a.lora.adapters, low_rank ? a.lora.r : 0,
+                   cus)) {
+    const hipError_t e = low_rank ? launch_rows_gemm_lora(a, quant_type, f16, hs)
+                                  : launch_rows_gemm(a, quant_type, f16, hs);
     if (e != hipErrorNotSupported) return e;
   }
   return launch_rows_stream(a, quant_type, f16, cus, hs);

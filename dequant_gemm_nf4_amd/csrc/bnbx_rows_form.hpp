@@ -1,6 +1,6 @@
 // Which form a product over grouped rows takes, from what the host knows: the
-// plan's rows, its groups (0: all rows are one group), the output columns and
-// the GPU's compute units.  Plain host code with no HIP in it, so that a test
+// plan's rows, its groups (0: all rows are one group), the output columns, the
+// low-rank term and the GPU's compute units.  Plain host code with no HIP in it, so that a test
 // can ask which form its sizes reach.
 #pragma once
 
@@ -19,16 +19,38 @@ inline double rounds_of(int rows, int groups, int cols, int tm, int tn, int slot
   return r < 1.0 ? 1.0 : r;
 }
 
+// Adapters that meet a tile of tm places: `adapters` of them in use alike (the
+// host does not know which have rows), the places in their order.
+inline double segments_of(int rows, int adapters, int tm) {
+  const double used = adapters < rows ? adapters : rows;
+  const double met = 1.0 + tm * used / rows, most = used < tm ? used : tm;
+  return met < most ? met : most;
+}
+
 // Whether the tiled form is likely to be the faster one.  Its workgroups (256
 // places x 256 columns, one a CU) take about 1.5 us per 64 k, those of the
 // streaming form (64 places x 128 columns, two a CU) about 1.0 us, each with a
 // full GPU.  Measured, 8 groups of N = K = 4096: 64 rows a group 69 us streaming
 // / 106 us tiled, 160 rows 101 / 104, 256 rows 158 / 110; one group, 333 rows,
 // N = 4096, K = 11008: 93 / 229.
-inline bool prefer_tiles(int rows, int groups, int N, int cus) {
+//
+// With a low-rank term of `rank` (0: none) every adapter that meets a tile adds
+// about 1.55 us per 16 ranks to a tiled workgroup (two or three products a
+// 32 x 32 tile, each behind its loads) and 0.8 us per 32 ranks to a streaming
+// one: over 300 to 4096 rows, 1 to 300 adapters, ranks 16 to 256 and four
+// weights the form chosen is at most 10 % slower than the other.  Measured, 600
+// rows, N = 11008, K = 4096, 64 adapters: rank 16 141 us streaming / 143 tiled,
+// rank 256 338 / 736; 2048 rows, N = K = 8192: 8 adapters of rank 64 544 / 282,
+// 64 of rank 256 743 / 518.
+inline bool prefer_tiles(int rows, int groups, int N, int K, int adapters, int rank, int cus) {
   if (rows <= 32 * (long long)(groups == 0 ? 1 : groups)) return false;
-  return 1.5 * rounds_of(rows, groups, N, 256, 256, cus, 0.5) <
-         rounds_of(rows, groups, N, 64, 128, 2 * cus, 0.5);
+  double tiled = 1.5 * (K / 64), streaming = K / 64;
+  if (rank > 0) {
+    tiled += 1.55 * segments_of(rows, adapters, 256) * (rank / 16);
+    streaming += 0.8 * segments_of(rows, adapters, 64) * ((rank + 31) / 32);
+  }
+  return tiled * rounds_of(rows, groups, N, 256, 256, cus, 0.5) <
+         streaming * rounds_of(rows, groups, N, 64, 128, 2 * cus, 0.5);
 }
 
 // The same for the input gradient: 256 x 256 tiles at 2.0 us per 64 weight

@@ -22,9 +22,9 @@ DX_LAYOUT = ([200, 0, 3, 500], 128, 8256)
 # (rows, groups) of N = 9001 and, of 700 rows, the input gradient of K = 8192
 PLAIN = [(700, 2), (700, 3), (601, 2)]
 # (rows, adapters, rank, N, K)
-ADAPTERS = [(600, 5, 16, 9001, 64), (513, 3, 48, 9101, 320), (700, 20, 128, 8450, 256),
-            (600, 2, 256, 9001, 1088), (577, 300, 32, 9001, 192)]
-ADAPTERS_BROKEN = (600, 3, 32, 9001, 192)
+ADAPTERS = [(1500, 5, 16, 9001, 64), (1281, 3, 48, 9101, 320), (2500, 20, 128, 8450, 1024),
+            (2000, 2, 256, 9001, 1088), (3000, 300, 16, 9001, 1088)]
+ADAPTERS_BROKEN = (2000, 3, 32, 9001, 192)
 
 
 def load(folder: str) -> ctypes.CDLL:
@@ -32,8 +32,9 @@ def load(folder: str) -> ctypes.CDLL:
     src, lib = os.path.join(folder, "form.cpp"), os.path.join(folder, "form.so")
     with open(src, "w") as f:
         f.write('#include "bnbx_rows_form.hpp"\n'
-                'extern "C" int tiles(int rows, int groups, int n, int cus) {\n'
-                '  return bnbx::prefer_tiles(rows, groups, n, cus);\n}\n'
+                'extern "C" int tiles(int rows, int groups, int n, int k, int adapters, int rank, '
+                'int cus) {\n'
+                '  return bnbx::prefer_tiles(rows, groups, n, k, adapters, rank, cus);\n}\n'
                 'extern "C" int dx_tiles(int rows, int groups, int k, int cus) {\n'
                 '  return bnbx::prefer_dx_tiles(rows, groups, k, cus);\n}\n')
     subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", "-I",

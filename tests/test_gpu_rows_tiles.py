@@ -51,6 +51,16 @@ def test_adapters(m, pool, rank, n, k, dq, quant, dtype):
     adapters.run_case(ids, pool, rank, n, k, dq, quant, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_hundreds_of_adapters_in_one_tile(dtype):
+    """All but one of the adapters with a single row."""
+    m, pool, rank, n, k = F.ADAPTERS[-1]
+    ids = torch.zeros(m, dtype=torch.int64)
+    ids[torch.randperm(m, generator=torch.Generator().manual_seed(1))[:pool - 1]] = \
+        torch.arange(1, pool)
+    adapters.run_case(ids, pool, rank, n, k, dtype=dtype)
+
+
 @pytest.mark.parametrize("dq", ["linear", "dynamic", None])
 def test_block_scales_at_any_address(dq):
     """Block codes and maxima that start at an element's own alignment only."""
@@ -171,7 +181,7 @@ def test_a_broken_adapter_stays_its_own(dtype):
 @pytest.mark.parametrize("op", ["experts", "experts_dx", "adapters"])
 def test_captured_and_replayed_with_new_plans(op):
     counts, n, k = F.DX_LAYOUT if op == "experts_dx" else F.EXPERTS_LAYOUT
-    rows, groups = 700, 3
+    rows, groups = F.ADAPTERS_BROKEN[0] if op == "adapters" else 700, 3
     q, w = stack(0 if op == "adapters" else groups, n, k, 21)
     width = n if op == "experts_dx" else k
     x = rand((rows, width), 22)
