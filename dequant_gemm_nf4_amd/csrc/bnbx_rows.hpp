@@ -6,6 +6,7 @@
 namespace bnbx {
 
 constexpr int kMaxGroups = 1024;   // BNBX_ROWS_MAX_GROUPS
+constexpr int kXcds = 8;
 
 // bnbx_group_rows: workspace bytes and launch.
 size_t group_rows_workspace_bytes(int rows, int groups);
@@ -49,6 +50,18 @@ struct RowsGemm {
   LoraRows lora;
 };
 
+// Workgroups of a launch over tiles of tm places, `across` to a row tile (the most
+// tiles there can be, a multiple of kXcds); 0: more than one launch takes, which
+// counts threads in 32 bits.
+inline unsigned rows_grid(int rows, int groups, int tm, int across, int threads) {
+  const int64_t tiles = (int64_t)rows / tm + (groups < rows ? groups : rows);
+  const int64_t grid = (tiles * across + kXcds - 1) / kXcds * kXcds;
+  return grid * threads < ((int64_t)1 << 32) ? (unsigned)grid : 0;
+}
+
+// The launches below return hipErrorNotSupported, before anything is enqueued,
+// for a call that they do not take; without `launch` that is all they do.
+
 // The adapters' down-projections into xa's planes (bnbx_rows_lora.hip).
 struct LoraDown {
   const int32_t* offsets;
@@ -59,18 +72,18 @@ struct LoraDown {
   const float* scale;       // [adapters]
 };
 hipError_t launch_rows_lora_down(const RowsGemm& a, const LoraDown& d, bool f16, int cus,
-                                 uint16_t* xa, hipStream_t stream);
+                                 uint16_t* xa, hipStream_t stream, bool launch);
 
 // Streaming form: row tiles of 16, 32 or 64 places (bnbx_rows_stream.hip).
 hipError_t launch_rows_stream(const RowsGemm& a, int quant_type, bool f16, int cus,
-                              hipStream_t stream);
+                              hipStream_t stream, bool launch);
 
 // Tiled form: row tiles of 256 places (bnbx_rows_gemm.hip), and with a
-// low-rank term (bnbx_rows_gemm_lora.hip).  hipErrorNotSupported where X does
-// not fit 32-bit offsets.
-hipError_t launch_rows_gemm(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream);
-hipError_t launch_rows_gemm_lora(const RowsGemm& a, int quant_type, bool f16,
-                                 hipStream_t stream);
+// low-rank term (bnbx_rows_gemm_lora.hip).  Not for an X past 32-bit offsets.
+hipError_t launch_rows_gemm(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream,
+                            bool launch);
+hipError_t launch_rows_gemm_lora(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream,
+                                 bool launch);
 
 // dX_i = dY_i . W_hat_g: x is dY [x_rows, N], y is dX [y_rows, K]; N a
 // multiple of 64 (bnbx_rows_dx.hip).

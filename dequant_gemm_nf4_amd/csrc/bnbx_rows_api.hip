@@ -72,15 +72,16 @@ int groups_of(const RowsGemm& a) { return a.offsets == nullptr ? 0 : a.groups; }
 
 // The products of both operators: the tiled form, or the streaming form (also
 // for an X past 32-bit offsets).
-hipError_t launch_rows(const RowsGemm& a, int quant_type, bool f16, int cus, hipStream_t hs) {
+hipError_t launch_rows(const RowsGemm& a, int quant_type, bool f16, int cus, hipStream_t hs,
+                       bool launch) {
   const bool low_rank = a.lora.offsets != nullptr;
   if (prefer_tiles(a.rows, groups_of(a), a.N, a.K, a.lora.adapters, low_rank ? a.lora.r : 0,
                    cus)) {
-    const hipError_t e = low_rank ? launch_rows_gemm_lora(a, quant_type, f16, hs)
-                                  : launch_rows_gemm(a, quant_type, f16, hs);
+    const hipError_t e = low_rank ? launch_rows_gemm_lora(a, quant_type, f16, hs, launch)
+                                  : launch_rows_gemm(a, quant_type, f16, hs, launch);
     if (e != hipErrorNotSupported) return e;
   }
-  return launch_rows_stream(a, quant_type, f16, cus, hs);
+  return launch_rows_stream(a, quant_type, f16, cus, hs, launch);
 }
 
 int rows_status(hipError_t e) {
@@ -127,7 +128,7 @@ int bnbx_gemm_nf4_experts(const uint16_t* x, int64_t ldx, int x_rows, const uint
   const RowsGemm a = rows_gemm(x, ldx, x_rows, packed, st, plan, N, K, gather, scatter, y, ldy,
                                y_rows);
   return rows_status(launch_rows(a, st->quant_type, st->compute_dtype == BNBX_DTYPE_F16,
-                                 rows_cus(), (hipStream_t)stream));
+                                 rows_cus(), (hipStream_t)stream, true));
 }
 
 int bnbx_gemm_nf4_experts_dx(const uint16_t* dy, int64_t lddy, int dy_rows,
@@ -180,16 +181,22 @@ int bnbx_gemm_nf4_adapters(const uint16_t* x, int64_t ldx, const uint8_t* packed
   const bool f16 = st->compute_dtype == BNBX_DTYPE_F16;
   const int cus = rows_cus();
   hipStream_t hs = (hipStream_t)stream;
-  RowsGemm a = rows_gemm(x, ldx, plan->rows, packed, st, plan, N, K, 1, 1, y, ldy, plan->rows);
+  const RowsGemm a =
+      rows_gemm(x, ldx, plan->rows, packed, st, plan, N, K, 1, 1, y, ldy, plan->rows);
   const LoraDown d{plan->offsets, plan->groups, ad->r, ad->lora_a, ad->lda, ad->stride_a,
                    ad->scale};
-  const hipError_t e = launch_rows_lora_down(a, d, f16, cus, (uint16_t*)workspace, hs);
-  if (e != hipSuccess) return rows_status(e);
-  a.offsets = nullptr;   // the shared weight: one group of all rows
-  a.groups = 1;
-  a.lora = LoraRows{plan->offsets, plan->groups, ad->r, (const uint16_t*)workspace, ad->lora_b,
+  RowsGemm b = a;
+  b.offsets = nullptr;   // the shared weight: one group of all rows
+  b.groups = 1;
+  b.lora = LoraRows{plan->offsets, plan->groups, ad->r, (const uint16_t*)workspace, ad->lora_b,
                     ad->ldb, ad->stride_b};
-  return rows_status(launch_rows(a, st->quant_type, f16, cus, hs));
+  // nothing is enqueued unless both launches fit
+  for (const bool launch : {false, true}) {
+    hipError_t e = launch_rows_lora_down(a, d, f16, cus, (uint16_t*)workspace, hs, launch);
+    if (e == hipSuccess) e = launch_rows(b, st->quant_type, f16, cus, hs, launch);
+    if (e != hipSuccess) return rows_status(e);
+  }
+  return BNBX_OK;
 }
 
 }  // extern "C"

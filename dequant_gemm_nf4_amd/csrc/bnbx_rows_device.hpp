@@ -8,7 +8,6 @@ namespace bnbx {
 
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 constexpr uint32_t kFar = 0x80000000u;   // an offset past every buffer resource
-constexpr int kXcds = 8;
 
 __device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes,

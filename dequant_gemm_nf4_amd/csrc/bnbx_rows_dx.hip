@@ -17,13 +17,12 @@ hipError_t launch_rows_dx(const RowsGemm& a, int quant_type, bool f16, hipStream
   // 32-bit offsets into dY: all of it where rows are looked up, one tile else
   const int64_t reach = a.gather > 0 ? a.x_rows : TM;
   if (reach * a.ldx * 2 >= kLimit) return hipErrorNotSupported;
-  const int tiles_k = (a.K + TK - 1) / TK;
-  const int64_t most = a.rows / TM + (a.groups < a.rows ? a.groups : a.rows);   // row tiles
-  const int64_t grid = (most * tiles_k + kXcds - 1) / kXcds * kXcds;
-  if (grid > 0x7fffffff) return hipErrorNotSupported;
+  const int tiles_k = (a.K - 1) / TK + 1;
+  const unsigned grid = rows_grid(a.rows, a.groups, TM, tiles_k, kThreads);
+  if (grid == 0) return hipErrorNotSupported;
   const LevelTable& lv = level_table(quant_type);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), 0, stream, a.x, a.ldx,
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), 0, stream, a.x, a.ldx,
                        a.packed, a.absmax, a.absmax2, a.mean, a.rows, a.N, a.K, a.y, a.ldy, 0,
                        tiles_k, lv, a);
   };

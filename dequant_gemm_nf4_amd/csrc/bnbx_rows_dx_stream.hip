@@ -252,13 +252,12 @@ __global__ __launch_bounds__(WS * 64) void rows_dx_stream_kernel(RowsGemm a, int
 
 template <int RB, int WS>
 hipError_t launch_one(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream) {
-  const int tiles_k = (a.K + kCols - 1) / kCols;
-  const int64_t most = a.rows / (16 * RB) + (a.groups < a.rows ? a.groups : a.rows);
-  const int64_t grid = (most * tiles_k + kXcds - 1) / kXcds * kXcds;
-  if (grid > 0x7fffffff) return hipErrorNotSupported;
+  const int tiles_k = (a.K - 1) / kCols + 1;
+  const unsigned grid = rows_grid(a.rows, a.groups, 16 * RB, tiles_k, WS * 64);
+  if (grid == 0) return hipErrorNotSupported;
   const LevelTable& lv = level_table(quant_type);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(WS * 64), 0, stream, a, tiles_k, lv);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(WS * 64), 0, stream, a, tiles_k, lv);
   };
   if (a.double_quant == kDqNone) {
     if (f16) go(rows_dx_stream_kernel<RB, WS, kDqNone, true>);

@@ -7,21 +7,22 @@
 
 namespace bnbx {
 
-hipError_t launch_rows_gemm(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream) {
+hipError_t launch_rows_gemm(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream,
+                            bool launch) {
   const int64_t kLimit = (int64_t)1 << 31;
   if ((int64_t)a.N * (a.K / 2) >= kLimit) return hipErrorNotSupported;
   // 32-bit offsets into X: all of it where rows are looked up, one tile else
   const int64_t reach = a.gather > 0 ? a.x_rows : BM;
   if (reach * a.ldx * 2 >= kLimit) return hipErrorNotSupported;
-  const int tiles_n = (a.N + BN - 1) / BN;
-  const int64_t most = a.rows / BM + (a.groups < a.rows ? a.groups : a.rows);   // row tiles
-  const int64_t grid = (most * tiles_n + kXcds - 1) / kXcds * kXcds;
-  if (grid > 0x7fffffff) return hipErrorNotSupported;
+  const int tiles_n = (a.N - 1) / BN + 1;
+  const unsigned grid = rows_grid(a.rows, a.groups, BM, tiles_n, kThreads);
+  if (grid == 0) return hipErrorNotSupported;
+  if (!launch) return hipSuccess;
   const LevelTable& lv = level_table(quant_type);
   // Four block codes per dword load, as in the ungrouped GEMM.
   const bool q4 = a.double_quant && (a.K / 64) % 4 == 0 && ((uintptr_t)a.absmax & 3) == 0;
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), 0, stream, a.x, a.ldx,
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), 0, stream, a.x, a.ldx,
                        a.packed, a.absmax, a.absmax2, a.mean, a.rows, a.N, a.K, a.y, a.ldy, 0,
                        tiles_n, lv, LoraArgs{}, SplitArgs{}, a);
   };

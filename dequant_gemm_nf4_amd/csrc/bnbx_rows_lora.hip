@@ -131,17 +131,18 @@ __global__ __launch_bounds__(kThreads) void rows_lora_down_kernel(RowsGemm a, Lo
 }  // namespace
 
 hipError_t launch_rows_lora_down(const RowsGemm& a, const LoraDown& d, bool f16, int cus,
-                                 uint16_t* xa, hipStream_t stream) {
+                                 uint16_t* xa, hipStream_t stream, bool launch) {
   const int64_t most = a.rows / kTile + (d.adapters < a.rows ? d.adapters : a.rows);
   // Four rank tiles a workgroup read X once for 64 ranks; one a workgroup
   // while the row tiles alone leave CUs idle.
   const bool wide = most >= cus;
   const int rt = wide ? 4 : 1;
   const int rank_tiles = (d.r + 16 * rt - 1) / (16 * rt);
-  const int64_t grid = (most * rank_tiles + kXcds - 1) / kXcds * kXcds;
-  if (grid > 0x7fffffff) return hipErrorNotSupported;
+  const unsigned grid = rows_grid(a.rows, d.adapters, kTile, rank_tiles, kThreads);
+  if (grid == 0) return hipErrorNotSupported;
+  if (!launch) return hipSuccess;
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), 0, stream, a, d, rank_tiles,
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), 0, stream, a, d, rank_tiles,
                        xa);
   };
   if (f16) {

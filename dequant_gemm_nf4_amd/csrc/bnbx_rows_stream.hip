@@ -571,15 +571,16 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
 }
 
 template <int RB, int NB, int WN, int WK, bool LUT>
-hipError_t launch_one(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream) {
+hipError_t launch_one(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream,
+                      bool launch) {
   constexpr int TM = 16 * RB, TN = 16 * NB * WN;
-  const int tiles_n = (a.N + TN - 1) / TN;
-  const int64_t most = a.rows / TM + (a.groups < a.rows ? a.groups : a.rows);   // row tiles
-  const int64_t grid = (most * tiles_n + kXcds - 1) / kXcds * kXcds;
-  if (grid > 0x7fffffff) return hipErrorNotSupported;
+  const int tiles_n = (a.N - 1) / TN + 1;
+  const unsigned grid = rows_grid(a.rows, a.groups, TM, tiles_n, WN * WK * 64);
+  if (grid == 0) return hipErrorNotSupported;
+  if (!launch) return hipSuccess;
   const LevelTable& lv = level_table(quant_type);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(WN * WK * 64), 0, stream, a, tiles_n,
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(WN * WK * 64), 0, stream, a, tiles_n,
                        lv);
   };
   const int nkb = a.K / 64;
@@ -604,7 +605,7 @@ hipError_t launch_one(const RowsGemm& a, int quant_type, bool f16, hipStream_t s
 }  // namespace
 
 hipError_t launch_rows_stream(const RowsGemm& a, int quant_type, bool f16, int cus,
-                              hipStream_t stream) {
+                              hipStream_t stream, bool launch) {
   const int groups = a.offsets == nullptr ? 1 : (a.groups < a.rows ? a.groups : a.rows);
   const int mean_rows = (a.rows + groups - 1) / groups;
   const int rb = mean_rows <= 16 ? 1 : mean_rows <= 32 ? 2 : 4;
@@ -631,29 +632,29 @@ hipError_t launch_rows_stream(const RowsGemm& a, int quant_type, bool f16, int c
     // place, 4096 x 4096: 8.4, against 11.9 with (2, 4); with 16 places 14.5
     // against 12.1.
     if (mean_rows <= 4 && slabs <= 2 * (int64_t)cus)
-      return launch_one<1, 1, 1, 8, true>(a, quant_type, f16, stream);
+      return launch_one<1, 1, 1, 8, true>(a, quant_type, f16, stream, launch);
     const double t2 = cost(2, 4, 6.5, 1.4), t4 = cost(4, 4, 6.5, 2.2),
                  t8 = cost(8, 2, 6.5, 1.85), t16 = cost(16, 1, 6.5, 1.65);
     const double least = std::min(std::min(t2, t4), std::min(t8, t16));
-    if (t2 <= least) return launch_one<1, 1, 2, 4, true>(a, quant_type, f16, stream);
-    if (t4 <= least) return launch_one<1, 1, 4, 4, true>(a, quant_type, f16, stream);
-    if (t8 <= least) return launch_one<1, 1, 8, 2, true>(a, quant_type, f16, stream);
-    return launch_one<1, 1, 16, 1, true>(a, quant_type, f16, stream);
+    if (t2 <= least) return launch_one<1, 1, 2, 4, true>(a, quant_type, f16, stream, launch);
+    if (t4 <= least) return launch_one<1, 1, 4, 4, true>(a, quant_type, f16, stream, launch);
+    if (t8 <= least) return launch_one<1, 1, 8, 2, true>(a, quant_type, f16, stream, launch);
+    return launch_one<1, 1, 16, 1, true>(a, quant_type, f16, stream, launch);
   }
   if (rb == 2) {
     const double t2 = cost(2, 2, 7.0, 1.15), t4 = cost(4, 2, 6.5, 1.5),
                  t8 = cost(8, 1, 6.5, 1.35), t16 = cost(16, 1, 7.5, 2.15);
     const double least = std::min(std::min(t2, t4), std::min(t8, t16));
-    if (t2 <= least) return launch_one<2, 1, 2, 2, true>(a, quant_type, f16, stream);
-    if (t4 <= least) return launch_one<2, 1, 4, 2, true>(a, quant_type, f16, stream);
-    if (t8 <= least) return launch_one<2, 1, 8, 1, true>(a, quant_type, f16, stream);
-    return launch_one<2, 1, 16, 1, true>(a, quant_type, f16, stream);
+    if (t2 <= least) return launch_one<2, 1, 2, 2, true>(a, quant_type, f16, stream, launch);
+    if (t4 <= least) return launch_one<2, 1, 4, 2, true>(a, quant_type, f16, stream, launch);
+    if (t8 <= least) return launch_one<2, 1, 8, 1, true>(a, quant_type, f16, stream, launch);
+    return launch_one<2, 1, 16, 1, true>(a, quant_type, f16, stream, launch);
   }
   // 64 places, K = 4096, forms (2, 2), (4, 2), (8, 1): N = 8192 23.7 / 25.4 /
   // 35.9; N = 16384 45.0 / 27.5 / 37.2; N = 24576 66.8 / 50.0 / 38.7.
-  if (slabs <= 2 * (int64_t)cus) return launch_one<4, 1, 2, 2, false>(a, quant_type, f16, stream);
-  if (slabs <= 4 * (int64_t)cus) return launch_one<4, 1, 4, 2, false>(a, quant_type, f16, stream);
-  return launch_one<4, 1, 8, 1, false>(a, quant_type, f16, stream);
+  if (slabs <= 2 * (int64_t)cus) return launch_one<4, 1, 2, 2, false>(a, quant_type, f16, stream, launch);
+  if (slabs <= 4 * (int64_t)cus) return launch_one<4, 1, 4, 2, false>(a, quant_type, f16, stream, launch);
+  return launch_one<4, 1, 8, 1, false>(a, quant_type, f16, stream, launch);
 }
 
 int rows_cus() {

@@ -135,6 +135,25 @@ def test_calls_without_rows_do_nothing():
                                 None, 0, 0)
 
 
+BIG = dict(lda=64, stride_a=16 * 64, ldb=16, stride_b=4096 * 16)
+
+
+@pytest.mark.parametrize("rows,groups,n", [
+    # more workgroups than a launch counts threads for (2^23 of 512), X past the
+    # 32-bit offsets of the tiled form
+    (2**24, 1, 4096), (2**24, 3, 8000)])
+def test_more_rows_than_a_launch_takes(rows, groups, n):
+    st, one = state(groups * n * 64), state(n * 64)
+    p = plan(rows=rows, groups=groups)
+    assert status_of(bnbx.bnbx_gemm_nf4_experts, A, 64, rows, B, st, p, n, 64, 1, 1, D, n, rows,
+                     0) == UNSUP
+    n64 = -(-n // 64) * 64
+    assert status_of(bnbx.bnbx_gemm_nf4_experts_dx, A, 64, rows, B, state(groups * n64 * 64), p, 64,
+                     n64, 1, 1, D, n64, rows, 0) == UNSUP
+    assert status_of(bnbx.bnbx_gemm_nf4_adapters, A, 64, B, one, p, n, 64, adapters(**BIG), D, n,
+                     E, 2**40, 0) == UNSUP
+
+
 def adapters(**kw):
     f = dict(lora_a=A + 65536, lora_b=B + 65536, scale=C + 65536, lda=128, stride_a=16 * 128,
              ldb=16, stride_b=128 * 16, r=16)
