@@ -6,6 +6,7 @@
 namespace bnbx {
 
 constexpr int kMaxGroups = 1024;   // BNBX_ROWS_MAX_GROUPS
+constexpr int kMaxRows = INT32_MAX - 511;   // place numbers of a last tile stay in 31 bits
 constexpr int kXcds = 8;
 
 // bnbx_group_rows: workspace bytes and launch.

@@ -14,8 +14,9 @@ int check_plan(const bnbx_row_groups* p) {
   if (p->rows > 0 && p->order == nullptr) return BNBX_E_INVAL;
   if (p->groups > BNBX_ROWS_MAX_GROUPS) return BNBX_E_UNSUPPORTED;
   if (!aligned(p->offsets, 4) || !aligned(p->order, 4)) return BNBX_E_ALIGN;
-  // the kernels count tiles of 16 places or more in 32 bits, and groups of a
-  // wrong plan may overlap
+  // the kernels count places to the end of a last tile and tiles of 16 places or
+  // more in 32 bits, and groups of a wrong plan may overlap
+  if (p->rows > kMaxRows) return BNBX_E_UNSUPPORTED;
   if (((int64_t)p->rows / 16 + 1) * p->groups >= ((int64_t)1 << 31)) return BNBX_E_UNSUPPORTED;
   return BNBX_OK;
 }

@@ -44,8 +44,9 @@ typedef struct {
   const int32_t* offsets; /* device int32[groups + 1], 0 <= ascending <= rows  */
   const int32_t* order;   /* device int32[rows]: the row at each place         */
   int32_t groups;         /* 1 .. BNBX_ROWS_MAX_GROUPS                         */
-  int32_t rows;           /* >= 0; products take (rows / 16 + 1) * groups < 2^31
-                             (else BNBX_E_UNSUPPORTED)                         */
+  int32_t rows;           /* >= 0; products take rows <= 2^31 - 512 and
+                             (rows / 16 + 1) * groups < 2^31 (else
+                             BNBX_E_UNSUPPORTED)                               */
 } bnbx_row_groups;
 
 /* Bytes of device workspace bnbx_group_rows needs; 0 for few rows (one

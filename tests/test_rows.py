@@ -139,6 +139,8 @@ BIG = dict(lda=64, stride_a=16 * 64, ldb=16, stride_b=4096 * 16)
 
 
 @pytest.mark.parametrize("rows,groups,n", [
+    # a last tile would pass 31 bits: every row in one group, or in two
+    (2**31 - 1, 1, 16), (2**31 - 256, 2, 16),
     # more workgroups than a launch counts threads for (2^23 of 512), X past the
     # 32-bit offsets of the tiled form
     (2**24, 1, 4096), (2**24, 3, 8000)])
