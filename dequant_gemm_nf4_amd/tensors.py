@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import contextlib
 import dataclasses
+import math
 
 import torch
 
@@ -44,6 +45,24 @@ class QuantizedWeight:
     quant_type: str = "nf4"
     dtype: torch.dtype = torch.bfloat16
     dq_map: str = "linear"
+
+    def __post_init__(self):
+        # the kernels read all that the shape says
+        n, device = math.prod(self.shape), self.packed.device
+        blocks = -(-n // BLOCKSIZE)
+        if n != self.n:
+            raise ValueError(f"the weight's n is {self.n}, its shape {self.shape}")
+        scales = (torch.float32 if not self.double_quant else
+                  torch.uint8 if self.dq_map == "dynamic" else torch.int8)
+        parts = [("packed", self.packed, torch.uint8, n // 2), ("absmax", self.absmax, scales, blocks)]
+        if self.double_quant:
+            parts += [("absmax2", self.absmax2, torch.float32, -(-blocks // GROUP)),
+                      ("absmax_mean", self.absmax_mean, torch.float32, 1)]
+        for name, t, dtype, count in parts:
+            if (t is None or t.dtype is not dtype or t.numel() < count or t.device != device
+                    or not t.is_contiguous()):
+                raise ValueError(f"the weight's {name} must be {count} contiguous {dtype} on "
+                                 f"{device} for its shape {self.shape}")
 
     @property
     def state(self) -> Nf4State:

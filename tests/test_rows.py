@@ -2,6 +2,7 @@
 refusal on the host before a launch (the pointers are never dereferenced), the
 torch-tensor layer's checks, and the ops' and modules' shapes on meta tensors."""
 
+import dataclasses
 import os
 import re
 import subprocess
@@ -266,6 +267,52 @@ def test_experts_checks(fn, width, out):
         fn(x, q, p, out=torch.zeros(6, out))
     with pytest.raises(ValueError, match="GPU"):
         fn(x, q, p)
+
+
+def test_a_weight_holds_what_its_shape_says():
+    """The kernels read all of a weight's shape: buffers of fewer elements,
+    other types or views are refused."""
+    bf = dict(dtype=torch.bfloat16)
+    x, p, a, b, s = (torch.zeros(6, 128, **bf), cpu_plan(), torch.zeros(3, 16, 128, **bf),
+                     torch.zeros(3, 64, 16, **bf), torch.ones(3))
+    for dq, dq_map in ((True, "linear"), (True, "dynamic"), (False, "linear")):
+        whole = T.empty_quantized((3, 64, 128), dq, "cpu", dq_map=dq_map)
+        one = T.empty_quantized((64, 128), dq, "cpu", dq_map=dq_map)
+        for q, call in ((whole, lambda q: T.gemm_experts(x, q, p)),
+                        (whole, lambda q: T.gemm_experts_dx(x[:, :64], q, p)),
+                        (one, lambda q: T.linear_adapters(x, q, p, a, b, s))):
+            with pytest.raises(ValueError, match="GPU"):
+                call(q)
+            bad = [dict(packed=q.packed[:-1]), dict(packed=q.packed.view(torch.int8)),
+                   dict(absmax=q.absmax[:-1]), dict(absmax=q.absmax.to(torch.float64)),
+                   dict(packed=torch.zeros(2 * q.packed.numel(), dtype=torch.uint8)[::2])]
+            if dq:
+                bad += [dict(absmax2=q.absmax2[:0]), dict(absmax2=None), dict(absmax_mean=None),
+                        dict(absmax_mean=q.absmax_mean.double()), dict(absmax=q.absmax.float()),
+                        dict(absmax2=q.absmax2.to("meta"))]
+            for kw in bad:
+                with pytest.raises(ValueError, match="the weight's"):
+                    call(dataclasses.replace(q, **kw))
+
+
+def test_rows_wider_than_the_weight_are_refused():
+    """The ops take K (N for the gradient) from the rows: a layer given wider ones
+    would read past its weight."""
+    m, p = Experts4bit(3, 128, 64, device="cpu"), cpu_plan()
+    wide = torch.zeros(6, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="the weight's"):
+        m(wide, (p.offsets, p.order), gather=1)
+    with pytest.raises(ValueError, match="the weight's"):
+        torch.ops.bnbx.experts4bit_dx(wide, m.packed, m.absmax, m.absmax2, m.absmax_mean, p.offsets,
+                                      p.order, 128, 1, False, "nf4")
+    layer = Linear4bitAdapters(128, 64, adapters=3, device="cpu")
+    with pytest.raises(ValueError, match="the weight's"):
+        layer(wide, (p.offsets, p.order))
+    plain = torch_ops.Linear4bit(128, 64, device="cpu")
+    with pytest.raises(ValueError, match="the weight's"):
+        plain(wide)
+    with pytest.raises(ValueError, match="the weight's"):
+        torch.ops.bnbx.linear4bit_dx(wide, m.packed, m.absmax, m.absmax2, m.absmax_mean, 128, "nf4")
 
 
 def test_adapters_checks():
