@@ -49,10 +49,10 @@ namespace {
 
 constexpr int kSlice = 256;          // k per unit
 
-template <int RB, int NB, int WN, int WK, bool LUT, int DQ, bool Q4, bool F16>
+template <int RB, int WN, int WK, bool LUT, int DQ, bool Q4, bool F16>
 __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, int tiles_n,
                                                                   LevelTable lv) {
-  constexpr int TM = 16 * RB, TN = 16 * NB * WN, kThreads = WN * WK * 64;
+  constexpr int TM = 16 * RB, TN = 16 * WN, kThreads = WN * WK * 64;
   constexpr int kAhead = 2;   // units loaded ahead, per 16 weight rows
   constexpr bool DIRECT = WN == 1, DYN = DQ == kDqDynamic;
   constexpr int XS = WN > RB * 8 ? 2 : 1;                // steps per X buffer
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   constexpr int kXBuf = DIRECT ? 0 : XS * WK * kXPart;
   constexpr int kXLoads = DIRECT ? 1 : XS * RB * 8 / WN;   // 1 KB loads a wave and buffer
   constexpr int kStages = WN * WK * 2048;
-  constexpr int kRedBytes = (WK - 1) * WN * RB * NB * 1024;
+  constexpr int kRedBytes = (WK - 1) * WN * RB * 1024;
   // LDS: the byte table (at offset 0: its addresses are v_perm results), X,
   // the waves' stages, the dynamic map if there is room (else it is read from
   // memory); the partial sums reuse all of it.
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   // meet in one L2
   const int tn = __builtin_amdgcn_readfirstlane((int)((uint32_t)id / (uint32_t)nt));
   const RowTile tile = tiles.find(id - tn * nt);
-  const int n0 = tn * TN + wn * 16 * NB;
+  const int n0 = tn * TN + wn * 16;
 
   const float mu = DQ ? *a.mean : 0.0f;
   const uint32_t rowK2 = (uint32_t)a.K >> 1, nkb = (uint32_t)a.K >> 6;
@@ -112,26 +112,22 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
     uint32_t q;    // code byte, or the fp32 block maximum (not Q4)
     float s;       // group scale
   };
-  uint32_t wrow[NB], brow[NB];
-#pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    const int nl = n0 + 16 * j + lr, nm = n0 + 16 * j + r;
-    wrow[j] = nl < a.N ? (uint32_t)nl * rowK2 + 16u * (uint32_t)lp : kFar;
-    brow[j] = nm < a.N ? (uint32_t)nm * nkb : kFar;   // row r's first block
-  }
+  const int nl = n0 + lr, nm = n0 + r;
+  const uint32_t wrow = nl < a.N ? (uint32_t)nl * rowK2 + 16u * (uint32_t)lp : kFar;
+  const uint32_t brow = nm < a.N ? (uint32_t)nm * nkb : kFar;   // row r's first block
   // Byte offset of a block's group scale.
   auto gidx = [&](uint32_t blk) { return ((grem + blk) >> 8) * 4u; };
-  auto load_unit = [&](Unit& u, int j, int slice) {
+  auto load_unit = [&](Unit& u, int slice) {
     const bool in = slice < nslices;
-    const uint32_t wo = in ? wrow[j] + (uint32_t)slice * (kSlice / 2) : kFar;
+    const uint32_t wo = in ? wrow + (uint32_t)slice * (kSlice / 2) : kFar;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       u.w[h] = __builtin_amdgcn_raw_buffer_load_b128(rw, wo + 64u * h, 0, 2);
     if constexpr (!Q4) {
       // the lane's block; past the end of the row it has no scale and no value
       const uint32_t at = 4u * (uint32_t)slice + (uint32_t)q;
-      const bool bin = in && brow[j] != kFar && at < nkb;
-      const uint32_t blk = brow[j] + at;
+      const bool bin = in && brow != kFar && at < nkb;
+      const uint32_t blk = brow + at;
       if (DQ) {
         u.q = __builtin_amdgcn_raw_buffer_load_b8(rq, bin ? blk : kFar, 0, 0);
         u.s = __builtin_bit_cast(
@@ -160,11 +156,11 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
     u32x4_t q;     // code bytes (x), or four fp32 block maxima
     float s;       // their group scale
   };
-  auto load_quad = [&](Quad& u, int j, int s) {
+  auto load_quad = [&](Quad& u, int s) {
     if constexpr (Q4) {
       const int slice = slice_of(s + q);
-      const bool bin = brow[j] != kFar && slice < nslices;
-      const uint32_t blk = brow[j] + 4u * (uint32_t)slice;
+      const bool bin = brow != kFar && slice < nslices;
+      const uint32_t blk = brow + 4u * (uint32_t)slice;
       if (DQ) {
         u.q[0] = __builtin_amdgcn_raw_buffer_load_b32(rq, bin ? blk : kFar, 0, 0);
         u.s = __builtin_bit_cast(
@@ -175,8 +171,8 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
     }
   };
   // Scale of the lane's block in step s (ph = s % 4).
-  auto unit_scale = [&](const Unit& u, const Quad& c, int j, int s, int ph) {
-    const bool bin = brow[j] != kFar && 4u * (uint32_t)slice_of(s) + (uint32_t)q < nkb;
+  auto unit_scale = [&](const Unit& u, const Quad& c, int s, int ph) {
+    const bool bin = brow != kFar && 4u * (uint32_t)slice_of(s) + (uint32_t)q < nkb;
     float sc;
     if constexpr (Q4) {
       const int from = (16 * ph + r) << 2;
@@ -197,14 +193,12 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   };
 
   // Units of the first steps go out before the rows of X are looked up.
-  Unit un[kAhead][NB];
+  Unit un[kAhead];
 #pragma unroll
   for (int p = 0; p < kAhead; ++p)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) load_unit(un[p][j], j, slice_of(p));
-  Quad quad[NB], quad_next[NB];   // of steps 4 t .. 4 t + 3, and of the next four
-#pragma unroll
-  for (int j = 0; j < NB; ++j) load_quad(quad_next[j], j, 0);
+    load_unit(un[p], slice_of(p));
+  Quad quad, quad_next;   // of steps 4 t .. 4 t + 3, and of the next four
+  load_quad(quad_next, 0);
 
   if (LUT) lut_build(smem, lv, kThreads);
   if (kMapLds)
@@ -292,11 +286,9 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
     yrow[i] = place < tile.r1 && x_row_of(a, place) >= 0 ? y_row_of(a, place) : -1;
   }
 
-  f32x4_t acc[NB][RB];
+  f32x4_t acc[RB];
 #pragma unroll
-  for (int j = 0; j < NB; ++j)
-#pragma unroll
-    for (int i = 0; i < RB; ++i) acc[j][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < RB; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
   const uint32_t lcol = 8u * (uint32_t)(lane & 31);
   // A unit in the MFMA layout: block q of row r, with its scale (or, for 64
@@ -305,51 +297,38 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
     u32x4_t w[2];
     float sc;
   };
-  auto turn = [&](Op& o, Unit& u, int j, int s, int ph) {   // ph = s % 4
+  auto turn = [&](Op& o, Unit& u, int s, int ph) {   // ph = s % 4
     if (Q4 && ph == 0) {
-      quad[j] = quad_next[j];
-      load_quad(quad_next[j], j, s + 4);
+      quad = quad_next;
+      load_quad(quad_next, s + 4);
     }
-    o.sc = unit_scale(u, quad[j], j, s, ph);
+    o.sc = unit_scale(u, quad, s, ph);
     *(u32x4_t*)(stage + ws0) = u.w[0];
     *(u32x4_t*)(stage + (ws0 ^ 64u)) = u.w[1];
     o.w[0] = *(const u32x4_t*)(stage + rs0);
     o.w[1] = *(const u32x4_t*)(stage + (rs0 ^ 16u));
-    load_unit(u, j, slice_of(s + kAhead));
+    load_unit(u, slice_of(s + kAhead));
   };
-  Op op[NB];
-  // Step s: `u` holds step s + 1's units, turned while step s multiplies.
+  Op op;
+  // Step s: `u` holds step s + 1's unit, turned while step s multiplies.
   // (With register tables, step s's own: the turned ones would cost registers
   // that the accumulators need.)
-  auto step = [&](Unit (&u)[NB], int s, auto phase) {
+  auto step = [&](Unit& u, int s, auto phase) {
     constexpr int PH = decltype(phase)::value;
-    if constexpr (!LUT)
-#pragma unroll
-      for (int j = 0; j < NB; ++j) turn(op[j], u[j], j, s, PH);
-    Tab16 tab[LUT ? 1 : NB];
-    u32x4_t w[NB][2];
-    float sc[NB];
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      if constexpr (!LUT) tab[j] = make_tab16_any<F16>(lv, op[j].sc);
-      sc[j] = op[j].sc;
-      w[j][0] = op[j].w[0];
-      w[j][1] = op[j].w[1];
-    }
+    if constexpr (!LUT) turn(op, u, s, PH);
+    Tab16 tab;
+    if constexpr (!LUT) tab = make_tab16_any<F16>(lv, op.sc);
+    const float sc = op.sc;
+    const u32x4_t w[2] = {op.w[0], op.w[1]};
     const uint16_t* xb = xs + (PH / XS & 1) * kXBuf + ((PH % XS) * WK + wk) * kXPart;
     if constexpr (LUT) {
       // Table reads (and X) of MFMA m + 1 go out before the products of m.
-      float2 l2[2][NB][4];
+      float2 l2[2][4];
       u32x4_t xo[2][RB];
       auto look = [&](int m) {
+        const uint32_t d = w[m >> 2][m & 3];
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const uint32_t d = w[j][m >> 2][m & 3];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            l2[m & 1][j][e] = lut_pair(smem, d, lcol, e);
-          }
-        }
+        for (int e = 0; e < 4; ++e) l2[m & 1][e] = lut_pair(smem, d, lcol, e);
         if (!DIRECT)
 #pragma unroll
           for (int i = 0; i < RB; ++i)
@@ -357,41 +336,33 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
                 *(const u32x4_t*)(xb + (16 * i + r) * kSlice + 8 * ((8 * q + m) ^ r));
       };
       look(0);
-#pragma unroll
-      for (int j = 0; j < NB; ++j) turn(op[j], u[j], j, s + 1, (PH + 1) & 3);
+      turn(op, u, s + 1, (PH + 1) & 3);
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
         if (m < 7) look(m + 1);
         __builtin_amdgcn_sched_barrier(0);
+        u32x4_t wo;
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          u32x4_t wo;
+        for (int e = 0; e < 4; ++e)
+          wo[e] = pack16x2<F16>(l2[m & 1][e].x * sc, l2[m & 1][e].y * sc);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            wo[e] = pack16x2<F16>(l2[m & 1][j][e].x * sc[j], l2[m & 1][j][e].y * sc[j]);
-#pragma unroll
-          for (int i = 0; i < RB; ++i)
-            acc[j][i] = mfma_16x16x32<F16>(wo, DIRECT ? dx[DIRECT ? i : 0][m] : xo[m & 1][i],
-                                           acc[j][i]);
-        }
+        for (int i = 0; i < RB; ++i)
+          acc[i] = mfma_16x16x32<F16>(wo, DIRECT ? dx[DIRECT ? i : 0][m] : xo[m & 1][i], acc[i]);
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
+      static_assert(LUT || !DIRECT, "operands of X from memory go with the byte table");
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
         u32x4_t xo[RB];
 #pragma unroll
         for (int i = 0; i < RB; ++i)
-          xo[i] = DIRECT ? dx[DIRECT ? i : 0][m]
-                         : *(const u32x4_t*)(xb + (16 * i + r) * kSlice + 8 * ((8 * q + m) ^ r));
+          xo[i] = *(const u32x4_t*)(xb + (16 * i + r) * kSlice + 8 * ((8 * q + m) ^ r));
+        uint32_t o[4];
+        decode8(w[m >> 2][m & 3], tab, o);
+        const u32x4_t wo = {o[0], o[1], o[2], o[3]};
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          uint32_t o[4];
-          decode8(w[j][m >> 2][m & 3], tab[j], o);
-          const u32x4_t wo = {o[0], o[1], o[2], o[3]};
-#pragma unroll
-          for (int i = 0; i < RB; ++i) acc[j][i] = mfma_16x16x32<F16>(wo, xo[i], acc[j][i]);
-        }
+        for (int i = 0; i < RB; ++i) acc[i] = mfma_16x16x32<F16>(wo, xo[i], acc[i]);
       }
     }
   };
@@ -400,13 +371,11 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
   load_direct(slice_of(0));
   put_x(0, 0);
   barrier();
-  if (LUT)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) turn(op[j], un[0][j], j, 0, 0);
+  if (LUT) turn(op, un[0], 0, 0);
   // No branch around a load, only out of the loop: the compiler's waits count
   // the loads issued since, and would wait for all of them where it cannot tell
   // how many.
-  auto advance = [&](Unit (&u)[NB], int s, auto phase) {
+  auto advance = [&](Unit& u, int s, auto phase) {
     constexpr int PH = decltype(phase)::value;
     if (PH % XS == 0) load_x(s + XS);
     step(u, s, phase);
@@ -452,18 +421,16 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
         hit &= hit - 1;
         const int s0 = __builtin_amdgcn_readlane(b0, l), s1 = __builtin_amdgcn_readlane(b1, l);
         const uint16_t* bb = lo.b + (int64_t)(c + l) * lo.stride_b;
-        f32x4_t term[NB][RB];
+        f32x4_t term[RB];
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
-#pragma unroll
-          for (int i = 0; i < RB; ++i) term[j][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < RB; ++i) term[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         for (int k = 0; k < lo.r; k += 32, ++seg) {
           if (seg % WK != wk) continue;   // uniform in the wave
           const int k8 = k + 8 * q;
           // XA's loads go out before the first use of B, but with 64 places,
           // where their registers would cost the second workgroup of the CU
           constexpr bool kEarly = RB <= 2;
-          u32x4_t bh[NB], bt[NB], bl[NB], xh[RB], xl[RB];   // bt: bh for xl
+          u32x4_t xh[RB], xl[RB];
           auto load_xa = [&](int i) {
             const int place = tile.r0 + 16 * i + r;
             xh[i] = xl[i] = u32x4_t{0u, 0u, 0u, 0u};
@@ -473,40 +440,31 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
               xl[i] = *(const u32x4_t*)(xa + lo.r);
             }
           };
-#pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            const int n = n0 + 16 * j + r;
-            bh[j] = u32x4_t{0u, 0u, 0u, 0u};
-            if (k8 < lo.r && n < a.N) bh[j] = *(const u32x4_t*)(bb + (int64_t)n * lo.ldb + k8);
-          }
+          const int n = n0 + r;
+          u32x4_t bh = {0u, 0u, 0u, 0u}, bl;
+          if (k8 < lo.r && n < a.N) bh = *(const u32x4_t*)(bb + (int64_t)n * lo.ldb + k8);
           if (kEarly)
 #pragma unroll
             for (int i = 0; i < RB; ++i) load_xa(i);
+          if (F16) split_f16(bh, bh, bl);
+          u32x4_t bt = bh;   // bh for xl
+          uint32_t odd = 0;
 #pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            if (F16) split_f16(bh[j], bh[j], bl[j]);
-            bt[j] = bh[j];
-            uint32_t odd = 0;
+          for (int e = 0; e < 4; ++e) odd |= odd_halves(bh[e]);
+          if (__builtin_expect(__ballot(odd != 0) != 0, false)) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) odd |= odd_halves(bh[j][e]);
-            if (__builtin_expect(__ballot(odd != 0) != 0, false)) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                bt[j][e] = tame_halves(bh[j][e], odd_halves(bh[j][e]));
-                // (a low part is NaN where the value is not finite)
-                if (F16) bl[j][e] = tame_halves(bl[j][e], odd_halves(bl[j][e]));
-              }
+            for (int e = 0; e < 4; ++e) {
+              bt[e] = tame_halves(bh[e], odd_halves(bh[e]));
+              // (a low part is NaN where the value is not finite)
+              if (F16) bl[e] = tame_halves(bl[e], odd_halves(bl[e]));
             }
           }
 #pragma unroll
           for (int i = 0; i < RB; ++i) {
             if (!kEarly) load_xa(i);
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-              term[j][i] = mfma_16x16x32<false>(bh[j], xh[i], term[j][i]);
-              term[j][i] = mfma_16x16x32<false>(bt[j], xl[i], term[j][i]);
-              if (F16) term[j][i] = mfma_16x16x32<false>(bl[j], xh[i], term[j][i]);
-            }
+            term[i] = mfma_16x16x32<false>(bh, xh[i], term[i]);
+            term[i] = mfma_16x16x32<false>(bt, xl[i], term[i]);
+            if (F16) term[i] = mfma_16x16x32<false>(bl, xh[i], term[i]);
           }
         }
 #pragma unroll
@@ -514,9 +472,7 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
           const int place = tile.r0 + 16 * i + r;
           const bool own = place >= s0 && place < s1;
 #pragma unroll
-          for (int j = 0; j < NB; ++j)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) acc[j][i][v] = own ? acc[j][i][v] + term[j][i][v] : acc[j][i][v];
+          for (int v = 0; v < 4; ++v) acc[i][v] = own ? acc[i][v] + term[i][v] : acc[i][v];
         }
       }
     }
@@ -528,22 +484,18 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
     f32x4_t* const red = (f32x4_t*)smem;
     if (wk > 0) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
-#pragma unroll
-        for (int i = 0; i < RB; ++i)
-          red[(((wk - 1) * WN + wn) * NB * RB + j * RB + i) * 64 + lane] = acc[j][i];
+      for (int i = 0; i < RB; ++i)
+        red[(((wk - 1) * WN + wn) * RB + i) * 64 + lane] = acc[i];
     }
     __syncthreads();
     if (wk > 0) return;
 #pragma unroll
     for (int p = 0; p < WK - 1; ++p)
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
+      for (int i = 0; i < RB; ++i) {
+        const f32x4_t v = red[((p * WN + wn) * RB + i) * 64 + lane];
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-          const f32x4_t v = red[((p * WN + wn) * NB * RB + j * RB + i) * 64 + lane];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[j][i][e] += v[e];
+        for (int e = 0; e < 4; ++e) acc[i][e] += v[e];
         }
   }
 
@@ -553,27 +505,24 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
     const int row = yrow[i];
     if (row < 0) continue;
     uint16_t* const yr = a.y + (int64_t)row * a.ldy;
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int n = n0 + 16 * j + 4 * q;
-      const uint32_t p0 = pack16x2<F16>(acc[j][i][0], acc[j][i][1]);
-      const uint32_t p1 = pack16x2<F16>(acc[j][i][2], acc[j][i][3]);
-      if (n + 3 < a.N && ((uintptr_t)(yr + n) & 7) == 0) {
-        *(uint2*)(yr + n) = make_uint2(p0, p1);
-      } else {
-        if (n < a.N) yr[n] = (uint16_t)p0;
-        if (n + 1 < a.N) yr[n + 1] = (uint16_t)(p0 >> 16);
-        if (n + 2 < a.N) yr[n + 2] = (uint16_t)p1;
-        if (n + 3 < a.N) yr[n + 3] = (uint16_t)(p1 >> 16);
-      }
+    const int n = n0 + 4 * q;
+    const uint32_t p0 = pack16x2<F16>(acc[i][0], acc[i][1]);
+    const uint32_t p1 = pack16x2<F16>(acc[i][2], acc[i][3]);
+    if (n + 3 < a.N && ((uintptr_t)(yr + n) & 7) == 0) {
+      *(uint2*)(yr + n) = make_uint2(p0, p1);
+    } else {
+      if (n < a.N) yr[n] = (uint16_t)p0;
+      if (n + 1 < a.N) yr[n + 1] = (uint16_t)(p0 >> 16);
+      if (n + 2 < a.N) yr[n + 2] = (uint16_t)p1;
+      if (n + 3 < a.N) yr[n + 3] = (uint16_t)(p1 >> 16);
     }
   }
 }
 
-template <int RB, int NB, int WN, int WK, bool LUT>
+template <int RB, int WN, int WK, bool LUT>
 hipError_t launch_one(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream,
                       bool launch) {
-  constexpr int TM = 16 * RB, TN = 16 * NB * WN;
+  constexpr int TM = 16 * RB, TN = 16 * WN;
   const int tiles_n = (a.N - 1) / TN + 1;
   const unsigned grid = rows_grid(a.rows, a.groups, TM, tiles_n, WN * WK * 64);
   if (grid == 0) return hipErrorNotSupported;
@@ -589,8 +538,8 @@ hipError_t launch_one(const RowsGemm& a, int quant_type, bool f16, hipStream_t s
   auto pick = [&](auto dq, auto quads) {
     constexpr int DQ = decltype(dq)::value;
     constexpr bool Q4 = decltype(quads)::value;
-    if (f16) go(rows_stream_kernel<RB, NB, WN, WK, LUT, DQ, Q4, true>);
-    else go(rows_stream_kernel<RB, NB, WN, WK, LUT, DQ, Q4, false>);
+    if (f16) go(rows_stream_kernel<RB, WN, WK, LUT, DQ, Q4, true>);
+    else go(rows_stream_kernel<RB, WN, WK, LUT, DQ, Q4, false>);
   };
   auto with = [&](auto dq) {
     if (q4) pick(dq, std::true_type{});
@@ -632,29 +581,29 @@ hipError_t launch_rows_stream(const RowsGemm& a, int quant_type, bool f16, int c
     // place, 4096 x 4096: 8.4, against 11.9 with (2, 4); with 16 places 14.5
     // against 12.1.
     if (mean_rows <= 4 && slabs <= 2 * (int64_t)cus)
-      return launch_one<1, 1, 1, 8, true>(a, quant_type, f16, stream, launch);
+      return launch_one<1, 1, 8, true>(a, quant_type, f16, stream, launch);
     const double t2 = cost(2, 4, 6.5, 1.4), t4 = cost(4, 4, 6.5, 2.2),
                  t8 = cost(8, 2, 6.5, 1.85), t16 = cost(16, 1, 6.5, 1.65);
     const double least = std::min(std::min(t2, t4), std::min(t8, t16));
-    if (t2 <= least) return launch_one<1, 1, 2, 4, true>(a, quant_type, f16, stream, launch);
-    if (t4 <= least) return launch_one<1, 1, 4, 4, true>(a, quant_type, f16, stream, launch);
-    if (t8 <= least) return launch_one<1, 1, 8, 2, true>(a, quant_type, f16, stream, launch);
-    return launch_one<1, 1, 16, 1, true>(a, quant_type, f16, stream, launch);
+    if (t2 <= least) return launch_one<1, 2, 4, true>(a, quant_type, f16, stream, launch);
+    if (t4 <= least) return launch_one<1, 4, 4, true>(a, quant_type, f16, stream, launch);
+    if (t8 <= least) return launch_one<1, 8, 2, true>(a, quant_type, f16, stream, launch);
+    return launch_one<1, 16, 1, true>(a, quant_type, f16, stream, launch);
   }
   if (rb == 2) {
     const double t2 = cost(2, 2, 7.0, 1.15), t4 = cost(4, 2, 6.5, 1.5),
                  t8 = cost(8, 1, 6.5, 1.35), t16 = cost(16, 1, 7.5, 2.15);
     const double least = std::min(std::min(t2, t4), std::min(t8, t16));
-    if (t2 <= least) return launch_one<2, 1, 2, 2, true>(a, quant_type, f16, stream, launch);
-    if (t4 <= least) return launch_one<2, 1, 4, 2, true>(a, quant_type, f16, stream, launch);
-    if (t8 <= least) return launch_one<2, 1, 8, 1, true>(a, quant_type, f16, stream, launch);
-    return launch_one<2, 1, 16, 1, true>(a, quant_type, f16, stream, launch);
+    if (t2 <= least) return launch_one<2, 2, 2, true>(a, quant_type, f16, stream, launch);
+    if (t4 <= least) return launch_one<2, 4, 2, true>(a, quant_type, f16, stream, launch);
+    if (t8 <= least) return launch_one<2, 8, 1, true>(a, quant_type, f16, stream, launch);
+    return launch_one<2, 16, 1, true>(a, quant_type, f16, stream, launch);
   }
   // 64 places, K = 4096, forms (2, 2), (4, 2), (8, 1): N = 8192 23.7 / 25.4 /
   // 35.9; N = 16384 45.0 / 27.5 / 37.2; N = 24576 66.8 / 50.0 / 38.7.
-  if (slabs <= 2 * (int64_t)cus) return launch_one<4, 1, 2, 2, false>(a, quant_type, f16, stream, launch);
-  if (slabs <= 4 * (int64_t)cus) return launch_one<4, 1, 4, 2, false>(a, quant_type, f16, stream, launch);
-  return launch_one<4, 1, 8, 1, false>(a, quant_type, f16, stream, launch);
+  if (slabs <= 2 * (int64_t)cus) return launch_one<4, 2, 2, false>(a, quant_type, f16, stream, launch);
+  if (slabs <= 4 * (int64_t)cus) return launch_one<4, 4, 2, false>(a, quant_type, f16, stream, launch);
+  return launch_one<4, 8, 1, false>(a, quant_type, f16, stream, launch);
 }
 
 int rows_cus() {
