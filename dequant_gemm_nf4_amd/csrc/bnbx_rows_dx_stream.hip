@@ -32,11 +32,16 @@ namespace {
 
 constexpr int kCols = 128, kUnit = 32;
 constexpr int kAhead = 2;   // units loaded ahead
+// 32 places a tile and 8 waves a workgroup at every size.  Measured on 8 experts
+// of 4096 x 4096 in us, 8 / 50 / 128 rows a group: 16 places 27.9 / 81.9 / 176,
+// 32 places 29.1 / 53.3 / 126, 64 places 43.7 / 88.6 / 142 (its accumulators
+// spill); 16 waves spill, 4 waves 39.0 / 51.0 / 121.  (With the block scale
+// formed without a branch, this form now takes 26 / 49 / 116.)
+constexpr int RB = 2, TM = 16 * RB, WS = 8;
 
-template <int RB, int WS, int DQ, bool F16>
+template <int DQ, bool F16>
 __global__ __launch_bounds__(WS * 64) void rows_dx_stream_kernel(RowsGemm a, int tiles_k,
                                                                  LevelTable lv) {
-  constexpr int TM = 16 * RB;
   constexpr bool DYN = DQ == kDqDynamic;
   constexpr int kAcc = 8 * RB;                      // f32x4 a lane
   // LDS: the byte table (at offset 0), two scale sets and a stage a wave, the
@@ -250,38 +255,28 @@ __global__ __launch_bounds__(WS * 64) void rows_dx_stream_kernel(RowsGemm a, int
   }
 }
 
-template <int RB, int WS>
-hipError_t launch_one(const RowsGemm& a, int quant_type, bool f16, hipStream_t stream) {
+}  // namespace
+
+hipError_t launch_rows_dx_stream(const RowsGemm& a, int quant_type, bool f16,
+                                 hipStream_t stream) {
   const int tiles_k = (a.K - 1) / kCols + 1;
-  const unsigned grid = rows_grid(a.rows, a.groups, 16 * RB, tiles_k, WS * 64);
+  const unsigned grid = rows_grid(a.rows, a.groups, TM, tiles_k, WS * 64);
   if (grid == 0) return hipErrorNotSupported;
   const LevelTable& lv = level_table(quant_type);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(WS * 64), 0, stream, a, tiles_k, lv);
   };
   if (a.double_quant == kDqNone) {
-    if (f16) go(rows_dx_stream_kernel<RB, WS, kDqNone, true>);
-    else go(rows_dx_stream_kernel<RB, WS, kDqNone, false>);
+    if (f16) go(rows_dx_stream_kernel<kDqNone, true>);
+    else go(rows_dx_stream_kernel<kDqNone, false>);
   } else if (a.double_quant == kDqLinear) {
-    if (f16) go(rows_dx_stream_kernel<RB, WS, kDqLinear, true>);
-    else go(rows_dx_stream_kernel<RB, WS, kDqLinear, false>);
+    if (f16) go(rows_dx_stream_kernel<kDqLinear, true>);
+    else go(rows_dx_stream_kernel<kDqLinear, false>);
   } else {
-    if (f16) go(rows_dx_stream_kernel<RB, WS, kDqDynamic, true>);
-    else go(rows_dx_stream_kernel<RB, WS, kDqDynamic, false>);
+    if (f16) go(rows_dx_stream_kernel<kDqDynamic, true>);
+    else go(rows_dx_stream_kernel<kDqDynamic, false>);
   }
   return hipGetLastError();
-}
-
-}  // namespace
-
-hipError_t launch_rows_dx_stream(const RowsGemm& a, int quant_type, bool f16,
-                                 hipStream_t stream) {
-  // 32 places a tile and 8 waves a workgroup at every size.  Measured on 8
-  // experts of 4096 x 4096 in us, 8 / 50 / 128 rows a group: 16 places 27.9 /
-  // 81.9 / 176, 32 places 29.1 / 53.3 / 126, 64 places 43.7 / 88.6 / 142 (its
-  // accumulators spill); 16 waves spill, 4 waves 39.0 / 51.0 / 121.  (With the
-  // block scale formed without a branch, this form now takes 26 / 49 / 116.)
-  return launch_one<2, 8>(a, quant_type, f16, stream);
 }
 
 }  // namespace bnbx
