@@ -129,14 +129,6 @@ struct SplitArgs {
   float* part;
 };
 
-struct NoRows {};
-
-// What the row map says of X, for code that also compiles without one.
-__device__ __forceinline__ int gather_of(const RowsGemm& a) { return a.gather; }
-__device__ __forceinline__ int gather_of(const NoRows&) { return 0; }
-__device__ __forceinline__ int x_rows_of(const RowsGemm& a, int) { return a.x_rows; }
-__device__ __forceinline__ int x_rows_of(const NoRows&, int m) { return m; }
-
 // Over grouped rows one kernel serves both quant types.
 template <bool ROWS, bool FP4, bool F16>
 __device__ __forceinline__ Tab16 make_tab(const LevelTable& lv, float sc) {

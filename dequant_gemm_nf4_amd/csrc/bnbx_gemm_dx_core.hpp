@@ -54,14 +54,6 @@ constexpr int kThreads = 512;     // 8 waves, two per SIMD
 constexpr int kTile = 256 * TN;   // 16-bit elements per LDS tile (128-byte rows)
 constexpr int kCopies = 8;        // byte-table copies, interleaved per entry (lane & 7)
 
-struct NoRows {};
-
-// What the row map says of X, for code that also compiles without one.
-__device__ __forceinline__ int gather_of(const RowsGemm& a) { return a.gather; }
-__device__ __forceinline__ int gather_of(const NoRows&) { return 0; }
-__device__ __forceinline__ int x_rows_of(const RowsGemm& a, int) { return a.x_rows; }
-__device__ __forceinline__ int x_rows_of(const NoRows&, int m) { return m; }
-
 // Byte offset of 16-bit element (row r, column c) in a rotated tile.
 __device__ __forceinline__ uint32_t tile_off(int r, int c) {
   return (uint32_t)(r * (TN * 2) + (((c >> 3) ^ ((r >> 1) & 7)) << 4) + ((c & 7) << 1));

@@ -138,6 +138,14 @@ __device__ __forceinline__ int y_row_of(const RowsGemm& a, int place) {
   return row >= 0 && row < a.y_rows ? row : -1;
 }
 
+// In place of a RowsGemm in kernels that serve both kinds of rows: X's rows are
+// the places, m of them.
+struct NoRows {};
+__device__ __forceinline__ int gather_of(const RowsGemm& a) { return a.gather; }
+__device__ __forceinline__ int gather_of(const NoRows&) { return 0; }
+__device__ __forceinline__ int x_rows_of(const RowsGemm& a, int) { return a.x_rows; }
+__device__ __forceinline__ int x_rows_of(const NoRows&, int m) { return m; }
+
 // The byte -> fp32 level pair table in LDS (64 KB at LDS offset 0): entry e,
 // (level of the high nibble, level of the low one), in 32 copies side by side,
 // 256 bytes an entry, so that one v_perm forms a read's address and b64 reads
