@@ -272,19 +272,27 @@ __device__ __forceinline__ void rows_lora_odd(const LoraRows& lo, int m0, int M,
     auto value = [&](int k) {
       return F16 ? (float)__builtin_bit_cast(_Float16, b[k]) : bf16lo_to_f32(b[k]);
     };
-    int k0 = 0;
-    while (k0 < lo.r && __builtin_isfinite(value(k0))) ++k0;
-    if (k0 == lo.r) continue;
+    uint64_t odd[kMaxLoraRank / 64];   // the ranks whose value is not finite
+    bool any = false;
+#pragma unroll
+    for (int w = 0; w < kMaxLoraRank / 64; ++w) {
+      odd[w] = 0;
+      for (int k = 64 * w; k < lo.r && k < 64 * w + 64; ++k)
+        if (!__builtin_isfinite(value(k))) odd[w] |= 1ull << (k & 63);
+      any |= odd[w] != 0;
+    }
+    if (!any) continue;
     for (int p = p0; p < p1; ++p) {
       const int row = yrow[p - m0];
       if (row < 0) continue;
       float term = 0.0f;
-      for (int k = k0; k < lo.r; ++k) {
-        const float v = value(k);
-        if (__builtin_isfinite(v)) continue;
-        const uint16_t* const xa = lo.xa + (int64_t)p * 2 * lo.r + k;
-        term += (bf16lo_to_f32(xa[0]) + bf16lo_to_f32(xa[lo.r])) * v;
-      }
+#pragma unroll
+      for (int w = 0; w < kMaxLoraRank / 64; ++w)
+        for (uint64_t m = odd[w]; m != 0 && term == term; m &= m - 1) {   // NaN stays
+          const int k = 64 * w + __builtin_ctzll(m);
+          const uint16_t* const xa = lo.xa + (int64_t)p * 2 * lo.r + k;
+          term += (bf16lo_to_f32(xa[0]) + bf16lo_to_f32(xa[lo.r])) * value(k);
+        }
       uint16_t* const o = y + (int64_t)row * ldy + n;
       float was = F16 ? (float)__builtin_bit_cast(_Float16, *o) : bf16lo_to_f32(*o);
       const int t = p - m0, tile = (t >> 5) * 2 + (lane >> 5), v = 4 * ((t >> 3) & 3) + (t & 3);
