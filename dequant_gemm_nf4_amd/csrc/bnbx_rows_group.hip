@@ -14,7 +14,8 @@
 // its place.
 //
 // Bound: latency at every size here (4 bytes read and 4 written a row; the
-// launch, the dependent passes and, for many chunks, a second launch).  Up to
+// launch, the dependent passes and, for many chunks, a second launch, which
+// counts its rows once more before it places them).  Up to
 // kOneChunk rows one workgroup does everything in one launch; more rows are cut
 // into at most kMaxChunks chunks, whose key counts go to the workspace in a
 // first launch; in the second, every workgroup adds the counts of all chunks

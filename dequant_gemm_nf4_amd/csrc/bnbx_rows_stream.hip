@@ -4,8 +4,9 @@
 // stored (the products run on the same 16-bit values bnbx_dequantize_nf4
 // gives), fp32 accumulation, one rounding of Y.
 //
-// Bound: the LDS (table, X and stage reads) and the vector work of the dequant,
-// about equally; then the start and end of a workgroup (6 - 7 us of a round).
+// Bound: a wave's table reads, vector work and matrix instructions wait on each
+// other (with 16 waves on a CU, over the time it has a workgroup: vector units 61
+// % busy, LDS 66 %); then the start and end of a workgroup (6 - 7 us of a round).
 // The packed weights stream once per row tile (RB x 16 places).  Measured: 32
 // rows in 8 groups of 14336 x 4096 (241 MB) 70 us a call, 3.4 TB/s; 16 rows of
 // one 11008 x 4096 weight 16 us; 566 rows in 16 groups of 4096 x 11008 225 us.

@@ -365,7 +365,8 @@ def _experts_backward(ctx, grad):
         dx = torch.ops.bnbx.experts4bit_dx(grad, *ctx.saved_tensors, in_features,
                                            1 if scatter else 0, gather > 0, quant_type)
         if gather > 1:
-            # a token's gradient: its slots' rows, added in fp32
+            # a token's gradient: its slots' rows, each rounded to 16 bits by the
+            # product (half a step of it), added in fp32
             dx = dx.view(-1, gather, in_features).sum(1, dtype=torch.float32).to(grad.dtype)
     return (dx,) + (None,) * 10
 

@@ -85,7 +85,10 @@ BNBX_ROWS_API int bnbx_group_rows(const int32_t* ids, int rows, int groups, int3
  *   plan    host descriptor; plan->rows = 0 is a call that does nothing
  *   N, K    of one weight; K a multiple of 64; N * K below 2^32
  *   y       device, y_rows rows at y + row*ldy; ldy >= N (written)
- * Any number of rows a group, none included.  Errors: BNBX_E_INVAL,
+ * Any number of rows a group, none included.  X of 2 GiB and more (x_rows * ldx * 2
+ * bytes) with gather >= 1 takes a form of about half the rate where many rows a
+ * group would take the fastest one; split the rows over calls there.  y must not
+ * overlap x.  Errors: BNBX_E_INVAL,
  * BNBX_E_ALIGN, BNBX_E_UNSUPPORTED (a weight too large for 32-bit offsets, more
  * than BNBX_ROWS_MAX_GROUPS groups, more output tiles than one launch takes). */
 BNBX_ROWS_API int bnbx_gemm_nf4_experts(const uint16_t* x, int64_t ldx, int x_rows,
@@ -98,7 +101,8 @@ BNBX_ROWS_API int bnbx_gemm_nf4_experts(const uint16_t* x, int64_t ldx, int x_ro
  * group g,   dX[row_x(i)] = dY[row_y(i)] . W_hat_g,   dY [dy_rows, N], dX
  * [dx_rows, K], with row_y(i) = order[i] / gather or i and row_x(i) = order[i] or
  * i as above.  Where the forward gathered with top_k, call with scatter 1: dX
- * then has a row per slot, and a token's gradient is the sum of its slots' rows.
+ * then has a row per slot, rounded to 16 bits, and a token's gradient is the sum
+ * of its slots' rows.
  * The other arguments, what is left untouched and the errors as above (lddy for
  * ldx, lddx for ldy), except: N a multiple of 64 (else BNBX_E_UNSUPPORTED). */
 BNBX_ROWS_API int bnbx_gemm_nf4_experts_dx(const uint16_t* dy, int64_t lddy, int dy_rows,
@@ -132,11 +136,12 @@ BNBX_ROWS_API size_t bnbx_gemm_nf4_adapters_workspace_bytes(int rows, int r);
  * any number of them, and must list every row in `order`: a row it does not
  * list is not written.  Values are of st->compute_dtype; both products
  * accumulate in fp32, X . A_g^T keeps 16 significant bits, and Y is rounded
- * once.  An adapter with infinities or NaN reaches its own rows only, and gives
+ * once.  X of 2 GiB and more runs at about half the rate (as with gather above).
+ * An adapter with infinities or NaN reaches its own rows only, and gives
  * them what the formula gives: a signed infinity, or NaN for 0 . inf and
  * inf - inf.
  *   x, packed, st, N, K  as bnbx_gemm_nf4 (st->n = N * K)
- *   y          device, row m at y + m*ldy; ldy >= N (written)
+ *   y          device, row m at y + m*ldy; ldy >= N (written); must not overlap x
  *   workspace  device, >= bnbx_gemm_nf4_adapters_workspace_bytes(...) bytes,
  *              16-byte aligned; scratch
  * Errors: as bnbx_gemm_nf4_experts, and BNBX_E_WORKSPACE. */
