@@ -37,11 +37,12 @@ inline double segments_of(int rows, int adapters, int tm) {
 // With a low-rank term of `rank` (0: none) every adapter that meets a tile adds
 // about 1.55 us per 16 ranks to a tiled workgroup (two or three products a
 // 32 x 32 tile, each behind its loads) and 0.8 us per 32 ranks to a streaming
-// one: over 300 to 4096 rows, 1 to 300 adapters, ranks 16 to 256 and four
-// weights the form chosen is at most 10 % slower than the other.  Measured, 600
-// rows, N = 11008, K = 4096, 64 adapters: rank 16 141 us streaming / 143 tiled,
-// rank 256 338 / 736; 2048 rows, N = K = 8192: 8 adapters of rank 64 544 / 282,
-// 64 of rank 256 743 / 518.
+// one.  Over 15000 drawn sizes of 150 to 2048 rows the form chosen takes 0.4 %
+// more than the faster of the two where the rows' adapters change often and 0.9 %
+// where few of the pool are in use (7 % and 1.8 % without the term), 2 % of them
+// more than 10 %, one 1.9 times.  Measured, 600 rows, N = 11008, K = 4096, 64
+// adapters: rank 16 141 us streaming / 143 tiled, rank 256 338 / 736; 2048 rows,
+// N = K = 8192: 8 adapters of rank 64 544 / 282, 64 of rank 256 743 / 518.
 inline bool prefer_tiles(int rows, int groups, int N, int K, int adapters, int rank, int cus) {
   if (rows <= 32 * (long long)(groups == 0 ? 1 : groups)) return false;
   double tiled = 1.5 * (K / 64), streaming = K / 64;

@@ -428,9 +428,10 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
         for (int k = 0; k < lo.r; k += 32, ++seg) {
           if (seg % WK != wk) continue;   // uniform in the wave
           const int k8 = k + 8 * q;
-          // XA's loads go out before the first use of B, but with 64 places,
-          // where their registers would cost the second workgroup of the CU
-          constexpr bool kEarly = RB <= 2;
+          // XA's loads go out before the first use of B, for two row blocks at
+          // most: all four of 64 places at once would cost the registers of the
+          // second workgroup of a CU, none 5 % (22 sizes of up to 64 adapters)
+          constexpr int kEarly = RB <= 2 ? RB : 2;
           u32x4_t xh[RB], xl[RB];
           auto load_xa = [&](int i) {
             const int place = tile.r0 + 16 * i + r;
@@ -444,9 +445,8 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
           const int n = n0 + r;
           u32x4_t bh = {0u, 0u, 0u, 0u}, bl;
           if (k8 < lo.r && n < a.N) bh = *(const u32x4_t*)(bb + (int64_t)n * lo.ldb + k8);
-          if (kEarly)
 #pragma unroll
-            for (int i = 0; i < RB; ++i) load_xa(i);
+          for (int i = 0; i < kEarly; ++i) load_xa(i);
           if (F16) split_f16(bh, bh, bl);
           u32x4_t bt = bh;   // bh for xl
           uint32_t odd = 0;
@@ -462,7 +462,7 @@ __global__ __launch_bounds__(WN* WK * 64) void rows_stream_kernel(RowsGemm a, in
           }
 #pragma unroll
           for (int i = 0; i < RB; ++i) {
-            if (!kEarly) load_xa(i);
+            if (i >= kEarly) load_xa(i);
             term[i] = mfma_16x16x32<false>(bh, xh[i], term[i]);
             term[i] = mfma_16x16x32<false>(bt, xl[i], term[i]);
             if (F16) term[i] = mfma_16x16x32<false>(bl, xh[i], term[i]);
