@@ -35,20 +35,22 @@ inline double segments_of(int rows, int adapters, int tm) {
 // N = 4096, K = 11008: 93 / 229.
 //
 // With a low-rank term of `rank` (0: none) every adapter that meets a tile adds
-// about 1.55 us per 16 ranks to a tiled workgroup (two or three products a
-// 32 x 32 tile, each behind its loads) and 0.8 us per 32 ranks to a streaming
-// one.  Over 15000 drawn sizes of 150 to 2048 rows the form chosen takes 0.4 %
-// more than the faster of the two where the rows' adapters change often and 0.9 %
-// where few of the pool are in use (7 % and 1.8 % without the term), 2 % of them
-// more than 10 %, one 1.9 times.  Measured, 600 rows, N = 11008, K = 4096, 64
-// adapters: rank 16 141 us streaming / 143 tiled, rank 256 338 / 736; 2048 rows,
-// N = K = 8192: 8 adapters of rank 64 544 / 282, 64 of rank 256 743 / 518.
+// work: two or three products a 32 x 32 tile and 16 ranks, each behind its loads,
+// in a tiled workgroup, and less in a streaming one.  Counted as 1.0 us per 16
+// ranks against 0.6 us per 32, the form chosen takes 0.5 % more than the faster of
+// the two over 10600 drawn sizes of 150 to 2048 rows whose adapters change often
+// and 0.7 % over 5100 with few of the pool in use (5.7 % and 1.8 % without the
+// term); 2 % of all are more than 10 % off, at worst 1.9 times.  With 1.55 and
+// 0.8 us, nearer to measured times, the first is 0.45 %, the second 0.9 %.
+// Measured, 600 rows, N = 11008, K = 4096, 64 adapters: rank 16 141 us streaming
+// / 143 tiled, rank 256 338 / 736; 2048 rows, N = K = 8192: 8 adapters of rank 64
+// 544 / 282, 64 of rank 256 743 / 518.
 inline bool prefer_tiles(int rows, int groups, int N, int K, int adapters, int rank, int cus) {
   if (rows <= 32 * (long long)(groups == 0 ? 1 : groups)) return false;
   double tiled = 1.5 * (K / 64), streaming = K / 64;
   if (rank > 0) {
-    tiled += 1.55 * segments_of(rows, adapters, 256) * (rank / 16);
-    streaming += 0.8 * segments_of(rows, adapters, 64) * ((rank + 31) / 32);
+    tiled += 1.0 * segments_of(rows, adapters, 256) * (rank / 16);
+    streaming += 0.6 * segments_of(rows, adapters, 64) * ((rank + 31) / 32);
   }
   return tiled * rounds_of(rows, groups, N, 256, 256, cus, 0.5) <
          streaming * rounds_of(rows, groups, N, 64, 128, 2 * cus, 0.5);
