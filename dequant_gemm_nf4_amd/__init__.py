@@ -34,6 +34,11 @@ __all__ = [
     "RowGroupsDesc", "bnbx_group_rows_workspace_bytes", "bnbx_group_rows",
     "bnbx_gemm_nf4_experts", "bnbx_gemm_nf4_experts_dx", "AdaptersDesc",
     "bnbx_gemm_nf4_adapters_workspace_bytes", "bnbx_gemm_nf4_adapters",
+    "int8_library_path", "int8_lib", "INT8_EXPORTED_SYMBOLS", "BNBX_DTYPE_F32",
+    "BNBX_INT8_MAX_COLS", "Int8RowsDesc", "bnbx_quantize_rows_int8", "bnbx_dequantize_rows_int8",
+    "bnbx_gemm_int8_workspace_bytes", "bnbx_gemm_int8", "bnbx_linear_int8_workspace_bytes",
+    "bnbx_linear_int8", "bnbx_gemm_int8_dx_workspace_bytes", "bnbx_gemm_int8_dx",
+    "bnbx_gemm_int8_dw_workspace_bytes", "bnbx_gemm_int8_dw",
 ]
 
 BNBX_OK = 0
@@ -74,6 +79,16 @@ ROWS_EXPORTED_SYMBOLS = (
     "bnbx_group_rows_workspace_bytes", "bnbx_group_rows", "bnbx_gemm_nf4_experts",
     "bnbx_gemm_nf4_experts_dx", "bnbx_gemm_nf4_adapters_workspace_bytes",
     "bnbx_gemm_nf4_adapters",
+)
+
+# libbnbx_int8.so (include/bnbx_int8.h)
+BNBX_DTYPE_F32 = 2
+BNBX_INT8_MAX_COLS = 131071
+INT8_EXPORTED_SYMBOLS = (
+    "bnbx_quantize_rows_int8", "bnbx_dequantize_rows_int8", "bnbx_gemm_int8_workspace_bytes",
+    "bnbx_gemm_int8", "bnbx_linear_int8_workspace_bytes", "bnbx_linear_int8",
+    "bnbx_gemm_int8_dx_workspace_bytes", "bnbx_gemm_int8_dx",
+    "bnbx_gemm_int8_dw_workspace_bytes", "bnbx_gemm_int8_dw",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -155,6 +170,19 @@ class AdaptersDesc(ctypes.Structure):
         ("ldb", ctypes.c_int64),
         ("stride_b", ctypes.c_int64),
         ("r", ctypes.c_int32),
+    ]
+
+
+class Int8RowsDesc(ctypes.Structure):
+    """bnbx_int8_rows: rows of 8-bit codes (device pointers)."""
+
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("ld", ctypes.c_int64),
+        ("rows", ctypes.c_int32),
+        ("cols", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
     ]
 
 
@@ -260,6 +288,46 @@ def rows_lib() -> ctypes.CDLL:
                                          ctypes.POINTER(AdaptersDesc), vp, i64, vp, sz, vp]
     L.bnbx_gemm_nf4_adapters.restype = i32
     _rows_lib = L
+    return L
+
+
+_int8_lib = None
+
+
+def int8_library_path() -> str:
+    return os.path.join(_HERE, "libbnbx_int8.so")
+
+
+def int8_lib() -> ctypes.CDLL:
+    """Load libbnbx_int8.so, the 8-bit operators (built in-tree by
+    dequant_gemm_nf4_amd.build)."""
+    global _int8_lib
+    if _int8_lib is not None:
+        return _int8_lib
+    path = int8_library_path()
+    if not os.path.exists(path):
+        raise BnbxLibraryMissing(
+            f"{path} is not built; run `python -m dequant_gemm_nf4_amd.build` (no fallback exists)")
+    try:
+        import torch  # noqa: F401  (before the library, as in lib())
+    except ImportError:  # pragma: no cover
+        pass
+    L = ctypes.CDLL(path)
+    vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+    qp = ctypes.POINTER(Int8RowsDesc)
+    L.bnbx_quantize_rows_int8.argtypes = [vp, i64, qp, vp]
+    L.bnbx_dequantize_rows_int8.argtypes = [qp, vp, i64, vp]
+    L.bnbx_gemm_int8_workspace_bytes.argtypes = [i32, i32, i32]
+    L.bnbx_gemm_int8.argtypes = [qp, qp, vp, i64, vp, sz, vp]
+    L.bnbx_linear_int8_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.bnbx_linear_int8.argtypes = [vp, i64, i32, qp, qp, vp, i64, vp, sz, vp]
+    L.bnbx_gemm_int8_dx_workspace_bytes.argtypes = [i32, i32, i32]
+    L.bnbx_gemm_int8_dx.argtypes = [vp, i64, i32, qp, vp, i64, vp, sz, vp]
+    L.bnbx_gemm_int8_dw_workspace_bytes.argtypes = [i32, i32, i32]
+    L.bnbx_gemm_int8_dw.argtypes = [vp, i64, i32, qp, vp, i64, i32, vp, sz, vp]
+    for name in INT8_EXPORTED_SYMBOLS:
+        getattr(L, name).restype = sz if name.endswith("_bytes") else i32
+    _int8_lib = L
     return L
 
 
@@ -472,3 +540,54 @@ def bnbx_gemm_nf4_adapters(x, ldx: int, packed, state: Nf4State, plan: RowGroups
                                              adapters, _ptr(y), ldy, _ptr(workspace),
                                              workspace_bytes, _stream(stream)),
            "bnbx_gemm_nf4_adapters")
+
+
+def bnbx_quantize_rows_int8(x, ldx: int, q: Int8RowsDesc, stream=None) -> None:
+    _check(int8_lib().bnbx_quantize_rows_int8(_ptr(x), ldx, q, _stream(stream)),
+           "bnbx_quantize_rows_int8")
+
+
+def bnbx_dequantize_rows_int8(q: Int8RowsDesc, out, ldo: int, stream=None) -> None:
+    _check(int8_lib().bnbx_dequantize_rows_int8(q, _ptr(out), ldo, _stream(stream)),
+           "bnbx_dequantize_rows_int8")
+
+
+def bnbx_gemm_int8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int8_lib().bnbx_gemm_int8_workspace_bytes(M, N, K)
+
+
+def bnbx_gemm_int8(x: Int8RowsDesc, w: Int8RowsDesc, y, ldy: int, workspace=None,
+                   workspace_bytes: int = 0, stream=None) -> None:
+    _check(int8_lib().bnbx_gemm_int8(x, w, _ptr(y), ldy, _ptr(workspace), workspace_bytes,
+                                     _stream(stream)), "bnbx_gemm_int8")
+
+
+def bnbx_linear_int8_workspace_bytes(M: int, N: int, K: int, saved: int = 0) -> int:
+    return int8_lib().bnbx_linear_int8_workspace_bytes(M, N, K, saved)
+
+
+def bnbx_linear_int8(x, ldx: int, M: int, w: Int8RowsDesc, saved: Int8RowsDesc | None, y,
+                     ldy: int, workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    _check(int8_lib().bnbx_linear_int8(_ptr(x), ldx, M, w, saved, _ptr(y), ldy, _ptr(workspace),
+                                       workspace_bytes, _stream(stream)), "bnbx_linear_int8")
+
+
+def bnbx_gemm_int8_dx_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int8_lib().bnbx_gemm_int8_dx_workspace_bytes(M, N, K)
+
+
+def bnbx_gemm_int8_dx(dy, lddy: int, M: int, w: Int8RowsDesc, dx, lddx: int, workspace=None,
+                      workspace_bytes: int = 0, stream=None) -> None:
+    _check(int8_lib().bnbx_gemm_int8_dx(_ptr(dy), lddy, M, w, _ptr(dx), lddx, _ptr(workspace),
+                                        workspace_bytes, _stream(stream)), "bnbx_gemm_int8_dx")
+
+
+def bnbx_gemm_int8_dw_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int8_lib().bnbx_gemm_int8_dw_workspace_bytes(M, N, K)
+
+
+def bnbx_gemm_int8_dw(dy, lddy: int, N: int, x: Int8RowsDesc, dw, lddw: int, out_dtype: int,
+                      workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    _check(int8_lib().bnbx_gemm_int8_dw(_ptr(dy), lddy, N, x, _ptr(dw), lddw, out_dtype,
+                                        _ptr(workspace), workspace_bytes, _stream(stream)),
+           "bnbx_gemm_int8_dw")

@@ -1,0 +1,50 @@
+// Internal declarations of libbnbx_int8 (include/bnbx_int8.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace bnbx {
+
+// Rows of codes (bnbx_int8_rows, checked).
+struct Int8Rows {
+  int8_t* codes;
+  float* scale;
+  int64_t ld;
+  int rows, cols;
+};
+
+hipError_t launch_quantize_rows(const uint16_t* x, int64_t ldx, const Int8Rows& q, bool f16,
+                                hipStream_t stream);
+hipError_t launch_dequantize_rows(const Int8Rows& q, uint16_t* out, int64_t ldo, bool f16,
+                                  hipStream_t stream);
+
+// Y = X . W^T over codes.
+size_t int8_gemm_workspace(int M, int N, int K);
+hipError_t launch_int8_gemm(const Int8Rows& x, const Int8Rows& w, uint16_t* y, int64_t ldy,
+                            bool f16, void* workspace, hipStream_t stream);
+
+// out[r, c] = sum_t A(r, t) v(t, c) over the values v of the codes [T, C], T and
+// C their rows and columns: A(r, t) is dy[r ldy + t], or dy[t ldy + r] (`turned`).
+enum { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2 };
+struct GradGemm {
+  const uint16_t* dy;
+  int64_t ldy;
+  int R;
+  Int8Rows v;
+  void* out;
+  int64_t ldo;
+  int out_type;
+};
+size_t int8_grad_workspace(int R, int C, int T);
+hipError_t launch_int8_grad(const GradGemm& g, bool turned, bool f16, void* workspace,
+                            hipStream_t stream);
+
+// Compute units of the current device (256 without one).
+int int8_cus();
+
+// Workspaces are cut into pieces of whole 256 bytes.
+inline size_t whole256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace bnbx

@@ -1,0 +1,342 @@
+// Y[M, N] = X . W^T over int8 codes with a scale for each row of both (the
+// 8-bit linear layer), for gfx950.
+//
+// Tiling.  A workgroup of four waves (2 x 2) owns TN rows of W by TM rows of X;
+// a wave 32 FN by 32 FM, as FN x FM tiles of v_mfma_i32_32x32x32_i8 with W as the
+// A operand: a lane then holds four consecutive n of one token.  K is walked in
+// steps of 128 bytes (whole cache lines), four substeps of 32.
+//
+// Both operands go from global memory straight into LDS (buffer_load ... lds, 16
+// bytes a lane), two buffers.  A row is 128 bytes, its eight 16-byte chunks
+// permuted by (row / 2) % 8, so that 16 lanes reading one chunk of 16 consecutive
+// rows meet all 64 banks once.  Rows past the end and chunks past K read as zeros
+// through the buffer range check.
+//
+// Pipeline of step t: substep s multiplies while the operands of substep s + 1
+// are read; before substep 3 one wait and barrier (step t+1 has landed, every
+// wave has read its last operands of step t), and under substep 3's products the
+// first operands of step t+1 are read and the copies of step t+2 begin, into the
+// buffer that step t has left.
+#include "bnbx_int8_device.hpp"
+
+namespace bnbx {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int BK = 128;
+constexpr int kXcds = 8;
+
+struct GemmArgs {
+  const int8_t* x;
+  const int8_t* w;
+  const float* sx;
+  const float* sw;
+  int64_t ldx, ldw;
+  int M, N, K;
+  uint16_t* y;
+  int64_t ldy;
+  int tiles_m, tiles_n;
+  int splits, steps_per;   // splits of K, steps of each
+  int* part;               // [splits][M][ldp] (splits > 1)
+  int64_t ldp;
+};
+
+// 16-bit results of four consecutive n.
+template <bool F16>
+__device__ __forceinline__ u32x2_t scaled4(const int* v, float sx, f32x4_t sw) {
+  float f[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = ((float)v[i] * sx) * sw[i];
+  u32x2_t r = {pack16x2<F16>(f[0], f[1]), pack16x2<F16>(f[2], f[3])};
+  return r;
+}
+
+// Eight results at y, `left` of them inside the row.
+__device__ __forceinline__ void store8(uint16_t* y, u32x4_t v, int left, bool vec) {
+  if (vec && left >= 8) {
+    *(u32x4_t*)y = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) y[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+  }
+}
+
+// Tile order: workgroup b runs on XCD b % 8; an XCD's tiles are consecutive, and
+// consecutive ones walk blocks of up to four row tiles of X, so that an XCD's L2
+// serves a few rows of both operands.
+__device__ __forceinline__ bool tile_of(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
+  constexpr int G = 4;
+  const int total = tiles_m * tiles_n, per = (total + kXcds - 1) / kXcds;
+  id = (id % kXcds) * per + id / kXcds;
+  if (id >= total || (int)(blockIdx.x / kXcds) >= per) return false;
+  const int group = id / (G * tiles_n), in = id - group * G * tiles_n;
+  const int left = tiles_m - group * G, g = left < G ? left : G;
+  tn = in / g;
+  tm = group * G + (in - tn * g);
+  return true;
+}
+
+template <int FM, int FN, bool F16, bool SPLIT>
+__global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
+  constexpr int TM = 64 * FM, TN = 64 * FN;
+  constexpr int CW = TN / 32, CX = TM / 32;   // copies a wave and step
+  __shared__ __attribute__((aligned(16))) uint8_t buf0[(TM + TN) * BK];
+  __shared__ __attribute__((aligned(16))) uint8_t buf1[(TM + TN) * BK];
+  int tm, tn;
+  if (!tile_of(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn)) return;
+  const int m0 = tm * TM, n0 = tn * TN;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, half = lane >> 5;
+  const int wn = (wave & 1) * 32 * FN, wm = (wave >> 1) * 32 * FM;   // the wave's corner
+  const int steps = (a.K + BK - 1) / BK;
+  const int t0 = SPLIT ? (int)blockIdx.y * a.steps_per : 0;
+  const int t1 = SPLIT ? (t0 + a.steps_per < steps ? t0 + a.steps_per : steps) : steps;
+  const int kp = (a.K + 15) / 16 * 16;
+
+  // Copies: instruction i of a wave fills eight rows, lane l chunk slot l % 8 of
+  // row l / 8 of them.
+  const rsrc8_t rw = rsrc8(a.w + (int64_t)n0 * a.ldw, (int64_t)kFar8);
+  const rsrc8_t rx = rsrc8(a.x + (int64_t)m0 * a.ldx, (int64_t)kFar8);
+  uint32_t off[CW + CX];
+#pragma unroll
+  for (int i = 0; i < CW + CX; ++i) {
+    const bool isw = i < CW;
+    const int r = isw ? (wave * CW + i) * 8 + (lane >> 3) : (wave * CX + i - CW) * 8 + (lane >> 3);
+    const int chunk = (lane & 7) ^ ((r >> 1) & 7);
+    const bool in = isw ? n0 + r < a.N : m0 + r < a.M;
+    off[i] = in ? (uint32_t)r * (uint32_t)(isw ? a.ldw : a.ldx) + 16u * chunk : kFar8;
+  }
+  // bytes of K left behind this lane's chunk of the even and odd instructions
+  const int c0 = (lane & 7) ^ ((lane >> 4) & 3), c1 = c0 ^ 4;
+  auto copies = [&](uint8_t* buf, int t, int i0, int i1) {
+    const int left = kp - t * BK;
+    const bool ok0 = 16 * c0 < left, ok1 = 16 * c1 < left;
+#pragma unroll
+    for (int i = i0; i < i1; ++i) {
+      const int at = i < CW ? (wave * CW + i) * 8 : TN + (wave * CX + i - CW) * 8;
+      const int r8 = i < CW ? wave * CW + i : wave * CX + i - CW;
+      const uint32_t o = ((r8 & 1) ? ok1 : ok0) ? off[i] : kFar8;
+      copy16_lds(i < CW ? rw : rx, buf + at * BK, o, (uint32_t)t * BK);
+    }
+  };
+
+  // Operand reads: lane (col, half) takes chunk 2 s + half of row col of a tile.
+  uint32_t rd[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) rd[s] = col * BK + 16 * ((2 * s + half) ^ ((col >> 1) & 7));
+  u32x4_t ow[2][FN], ox[2][FM];
+  auto reads = [&](const uint8_t* buf, int s, int set) {
+#pragma unroll
+    for (int f = 0; f < FN; ++f) ow[set][f] = *(const u32x4_t*)(buf + (wn + 32 * f) * BK + rd[s]);
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+      ox[set][f] = *(const u32x4_t*)(buf + (TN + wm + 32 * f) * BK + rd[s]);
+  };
+  i32x16_t acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+  auto products = [&](int set) {
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] = mfma_i8_32x32x32(ow[set][i], ox[set][j], acc[i][j]);
+  };
+  auto land = [&] {
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  };
+
+  constexpr int C = CW + CX, H = C / 2;
+  copies(buf0, t0, 0, C);
+  copies(buf1, t0 + 1, 0, H);
+  land();
+  reads(buf0, 0, 0);
+  auto step = [&](int t, uint8_t* cur, uint8_t* next) {
+    copies(next, t + 1, H, C);
+    reads(cur, 1, 1);
+    products(0);
+    reads(cur, 2, 0);
+    products(1);
+    reads(cur, 3, 1);
+    products(0);
+    land();
+    copies(cur, t + 2, 0, H);
+    reads(next, 0, 0);
+    products(1);
+  };
+  for (int t = t0; t < t1; t += 2) {
+    step(t, buf0, buf1);
+    if (t + 1 < t1) step(t + 1, buf1, buf0);
+  }
+
+  if constexpr (SPLIT) {
+    int* part = a.part + (int64_t)blockIdx.y * a.M * a.ldp;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const int m = m0 + wm + 32 * j + col;
+      if (m >= a.M) continue;
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int n = n0 + wn + 32 * i + 8 * g + 4 * half;
+          if (n < a.N) {
+            const i32x4_t v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                               acc[i][j][4 * g + 3]};
+            *(i32x4_t*)(part + (int64_t)m * a.ldp + n) = v;
+          }
+        }
+    }
+    return;
+  }
+
+  // Results through LDS, a wave's own quarter of the buffers: rows of 32 FN
+  // values, 16-byte chunks permuted by the row.
+  land();   // every wave has read its operands, and no copy is in flight
+  constexpr int CH = 4 * FN;
+  uint8_t* const mine = (wave < 2 ? buf0 : buf1) + (wave & 1) * 32 * FM * 64 * FN;
+  static_assert(2 * 32 * FM * 64 * FN <= (TM + TN) * BK, "results fit the buffers");
+  const rsrc8_t rs = rsrc8(a.sw, (int64_t)a.N * 4);
+  f32x4_t sw[FN][4];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      sw[i][g] = __builtin_bit_cast(
+          f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                       rs, 4u * (uint32_t)(n0 + wn + 32 * i + 8 * g + 4 * half), 0, 0));
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    const int r = 32 * j + col, m = m0 + wm + r;
+    const float sx = m < a.M ? a.sx[m] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        int v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e];
+        *(u32x2_t*)(mine + r * 64 * FN + 16 * ((4 * i + g) ^ (r & (CH - 1))) + 8 * half) =
+            scaled4<F16>(v, sx, sw[i][g]);
+      }
+  }
+  const bool vec = ((uintptr_t)a.y % 16 == 0) && a.ldy % 8 == 0;
+#pragma unroll 4
+  for (int i = 0; i < 32 * FM * CH / 64; ++i) {
+    const int r = (i * 64 + lane) / CH, ch = lane % CH;
+    const int m = m0 + wm + r, n = n0 + wn + 8 * ch;
+    const u32x4_t v = *(const u32x4_t*)(mine + r * 64 * FN + 16 * (ch ^ (r & (CH - 1))));
+    if (m < a.M && n < a.N) store8(a.y + (int64_t)m * a.ldy + n, v, a.N - n, vec);
+  }
+}
+
+// The splits of K added, scaled and rounded: a thread takes four n.
+template <bool F16>
+__global__ __launch_bounds__(kThreads) void int8_reduce_kernel(GemmArgs a) {
+  const int quads = (a.N + 3) / 4;
+  const int64_t total = (int64_t)a.M * quads;
+  for (int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x; q < total;
+       q += (int64_t)gridDim.x * kThreads) {
+    const int m = (int)(q / quads), n = 4 * (int)(q - (int64_t)m * quads);
+    const int* p = a.part + (int64_t)m * a.ldp + n;
+    i32x4_t s = *(const i32x4_t*)p;
+    for (int k = 1; k < a.splits; ++k) s += *(const i32x4_t*)(p + (int64_t)k * a.M * a.ldp);
+    const float sx = a.sx[m];
+    uint16_t* y = a.y + (int64_t)m * a.ldy + n;
+    f32x4_t sw;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sw[e] = n + e < a.N ? a.sw[n + e] : 0.0f;
+    const int v[4] = {s[0], s[1], s[2], s[3]};
+    const u32x2_t r = scaled4<F16>(v, sx, sw);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < a.N) y[e] = (uint16_t)(r[e / 2] >> (16 * (e & 1)));
+  }
+}
+
+struct Form {
+  int f;        // FM = FN
+  int splits, steps_per;
+};
+// The largest tile that fills the GPU; where even the smallest does not, K is
+// split, at least four steps each.
+Form form_of(int M, int N, int K) {
+  const int cus = int8_cus();
+  auto tiles = [&](int f) {
+    return (int64_t)((M + 64 * f - 1) / (64 * f)) * ((N + 64 * f - 1) / (64 * f));
+  };
+  const int f = tiles(4) >= cus * 3 / 4 ? 4 : tiles(2) >= cus / 2 ? 2 : 1;
+  const int steps = (K + BK - 1) / BK;
+  int splits = 1;
+  if (f == 1) {
+    const int64_t most = 2 * cus / tiles(1);
+    splits = (int)(most < steps / 4 ? most : steps / 4);
+    splits = splits < 1 ? 1 : splits;
+  }
+  const int per = (steps + splits - 1) / splits;
+  return {f, (steps + per - 1) / per, per};
+}
+
+template <bool F16, bool SPLIT>
+hipError_t launch(const GemmArgs& a, int f, hipStream_t s) {
+  const int total = a.tiles_m * a.tiles_n;
+  const dim3 grid((total + kXcds - 1) / kXcds * kXcds, a.splits);
+  if (f == 4)
+    int8_gemm_kernel<4, 4, F16, SPLIT><<<grid, kThreads, 0, s>>>(a);
+  else if (f == 2)
+    int8_gemm_kernel<2, 2, F16, SPLIT><<<grid, kThreads, 0, s>>>(a);
+  else
+    int8_gemm_kernel<1, 1, F16, SPLIT><<<grid, kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t int8_gemm_workspace(int M, int N, int K) {
+  const Form f = form_of(M, N, K);
+  return f.splits > 1 ? (size_t)f.splits * M * ((N + 3) / 4 * 4) * sizeof(int) : 0;
+}
+
+hipError_t launch_int8_gemm(const Int8Rows& x, const Int8Rows& w, uint16_t* y, int64_t ldy,
+                            bool f16, void* workspace, hipStream_t s) {
+  const Form f = form_of(x.rows, w.rows, x.cols);
+  GemmArgs a{};
+  a.x = x.codes;
+  a.w = w.codes;
+  a.sx = x.scale;
+  a.sw = w.scale;
+  a.ldx = x.ld;
+  a.ldw = w.ld;
+  a.M = x.rows;
+  a.N = w.rows;
+  a.K = x.cols;
+  a.y = y;
+  a.ldy = ldy;
+  const int64_t tm = ((int64_t)a.M + 64 * f.f - 1) / (64 * f.f),
+                tn = ((int64_t)a.N + 64 * f.f - 1) / (64 * f.f);
+  // a launch counts its threads in 32 bits
+  if (tm * tn * f.splits >= ((int64_t)1 << 32) / kThreads - kXcds) return hipErrorNotSupported;
+  a.tiles_m = (int)tm;
+  a.tiles_n = (int)tn;
+  a.splits = f.splits;
+  a.steps_per = f.steps_per;
+  a.part = (int*)workspace;
+  a.ldp = (a.N + 3) / 4 * 4;
+  if (f.splits == 1) return f16 ? launch<true, false>(a, f.f, s) : launch<false, false>(a, f.f, s);
+  const hipError_t e = f16 ? launch<true, true>(a, f.f, s) : launch<false, true>(a, f.f, s);
+  if (e != hipSuccess) return e;
+  const int64_t quads = (int64_t)a.M * ((a.N + 3) / 4), groups = (quads + kThreads - 1) / kThreads;
+  const int grid = (int)(groups < 65536 ? groups : 65536);
+  if (f16)
+    int8_reduce_kernel<true><<<grid, kThreads, 0, s>>>(a);
+  else
+    int8_reduce_kernel<false><<<grid, kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace bnbx

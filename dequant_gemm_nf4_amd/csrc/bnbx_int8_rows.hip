@@ -1,0 +1,215 @@
+// Rows of 16-bit values to int8 codes with one scale a row, and back
+// (include/bnbx_int8.h has the format).
+//
+// Both stream: 2 bytes in and 1 out an element, or 1 in and 2 out.  The
+// quantizer holds its row in registers between the maximum and the codes, so X is
+// read once: a team of T threads owns a row, thread t the 8-element pieces t, t +
+// T, ...  The smallest team that holds the row is taken where there are rows
+// enough to fill the GPU, else the largest, for the latency of a single row.
+#include "bnbx_int8_device.hpp"
+
+namespace bnbx {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Piece p of a row: 8 values as 16-bit pairs, zero behind the row's end.  VEC: the
+// row starts at 16 bytes.
+template <bool VEC>
+__device__ __forceinline__ u32x4_t load_piece(const uint16_t* row, int p, int cols) {
+  const int k = 8 * p;
+  if (VEC && k + 8 <= cols) return *(const u32x4_t*)(row + k);
+  u32x4_t v = {0, 0, 0, 0};
+  if (k < cols) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t e = k + i < cols ? row[k + i] : 0u;
+      v[i / 2] |= e << (16 * (i & 1));
+    }
+  }
+  return v;
+}
+
+typedef __attribute__((ext_vector_type(2))) uint16_t u16x2_t;
+
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t,
+                            __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
+                                                      __builtin_bit_cast(u16x2_t, b)));
+}
+// |x| as integers order like the values, infinities and NaN above them.
+__device__ __forceinline__ uint32_t max_piece(uint32_t m, u32x4_t v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max_halves(m, v[i] & 0x7fff7fffu);
+  return m;
+}
+
+template <bool F16>
+__device__ __forceinline__ u32x2_t codes_of(u32x4_t v, const RowQuant& p) {
+  uint32_t q[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    if (F16) {
+      const f16x2_t h = __builtin_bit_cast(f16x2_t, (uint32_t)v[i]);
+      lo = (float)h[0];
+      hi = (float)h[1];
+    } else {
+      lo = bf16lo_to_f32(v[i]);
+      hi = bf16hi_to_f32(v[i]);
+    }
+    q[2 * i] = code_of(lo, p);
+    q[2 * i + 1] = code_of(hi, p);
+  }
+  u32x2_t r = {pack_bytes(q[0], q[1], q[2], q[3]), pack_bytes(q[4], q[5], q[6], q[7])};
+  return r;
+}
+
+// The largest of the team's maxima, in every thread of it.
+template <int T>
+__device__ __forceinline__ uint32_t team_max(uint32_t m, uint32_t* lds) {
+  m = m > (m >> 16 | m << 16) ? m : (m >> 16 | m << 16);   // the larger half on top
+  m >>= 16;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    const uint32_t other = (uint32_t)__shfl_xor((int)m, o);
+    m = m > other ? m : other;
+  }
+  if constexpr (T > 64) {
+    constexpr int W = T / 64;
+    __syncthreads();   // the last row's maxima are read
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = lds[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) m = m > lds[w] ? m : lds[w];
+  }
+  return m;
+}
+
+// T threads a row, NP pieces a thread (0: any number, the row read twice).
+template <int T, int NP, bool F16, bool VEC>
+__global__ __launch_bounds__(T > kThreads ? T : kThreads) void quantize_rows_kernel(
+    const uint16_t* __restrict__ x, int64_t ldx, Int8Rows q) {
+  constexpr int kRows = T < kThreads ? kThreads / T : 1;   // rows a workgroup
+  __shared__ uint32_t lds[T > 64 ? T / 64 : 1];
+  const int t = threadIdx.x % T;
+  const int pieces = (q.cols + 15) / 16 * 2;
+  for (int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / T; r < q.rows;
+       r += (int64_t)gridDim.x * kRows) {
+    const uint16_t* row = x + r * ldx;
+    int8_t* out = q.codes + r * q.ld;
+    uint32_t m = 0;
+    if constexpr (NP > 0) {
+      u32x4_t v[NP];
+#pragma unroll
+      for (int i = 0; i < NP; ++i) v[i] = load_piece<VEC>(row, t + i * T, q.cols);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) m = max_piece(m, v[i]);
+      const RowQuant p = row_quant<F16>(team_max<T>(m, lds));
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        if (t + i * T < pieces) *(u32x2_t*)(out + 8 * (t + i * T)) = codes_of<F16>(v[i], p);
+      if (t == 0) q.scale[r] = p.scale;
+    } else {
+      for (int i = t; i < pieces; i += T) m = max_piece(m, load_piece<VEC>(row, i, q.cols));
+      const RowQuant p = row_quant<F16>(team_max<T>(m, lds));
+      for (int i = t; i < pieces; i += T)
+        *(u32x2_t*)(out + 8 * i) = codes_of<F16>(load_piece<VEC>(row, i, q.cols), p);
+      if (t == 0) q.scale[r] = p.scale;
+    }
+  }
+}
+
+// Values: T threads a row, 8 codes a thread and step.
+template <int T, bool F16, bool VEC>
+__global__ __launch_bounds__(kThreads) void dequantize_rows_kernel(Int8Rows q,
+                                                                   uint16_t* __restrict__ out,
+                                                                   int64_t ldo) {
+  constexpr int kRows = kThreads / T;
+  const int t = threadIdx.x % T;
+  const int pieces = (q.cols + 7) / 8;
+  for (int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / T; r < q.rows;
+       r += (int64_t)gridDim.x * kRows) {
+    const int8_t* row = q.codes + r * q.ld;
+    uint16_t* o = out + r * ldo;
+    const float s = q.scale[r];
+    for (int p = t; p < pieces; p += T) {
+      const u32x2_t c = *(const u32x2_t*)(row + 8 * p);
+      u32x4_t v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = pack16x2<F16>(code_value(c[i / 2], 2 * (i & 1), s),
+                             code_value(c[i / 2], 2 * (i & 1) + 1, s));
+      if (VEC && 8 * p + 8 <= q.cols) {
+        *(u32x4_t*)(o + 8 * p) = v;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (8 * p + i < q.cols) o[8 * p + i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+      }
+    }
+  }
+}
+
+constexpr int kMostGroups = 1 << 16;   // workgroups of a launch; they walk over the rows
+
+int groups_for(int64_t rows, int per) {
+  const int64_t n = (rows + per - 1) / per;
+  return (int)(n < kMostGroups ? n : kMostGroups);
+}
+
+template <int T, int NP, bool F16, bool VEC>
+hipError_t quantize(const uint16_t* x, int64_t ldx, const Int8Rows& q, hipStream_t s) {
+  constexpr int threads = T > kThreads ? T : kThreads;
+  quantize_rows_kernel<T, NP, F16, VEC>
+      <<<groups_for(q.rows, threads / T), threads, 0, s>>>(x, ldx, q);
+  return hipGetLastError();
+}
+
+// `few`: not enough rows for a wave on every SIMD.
+template <bool F16, bool VEC>
+hipError_t quantize(const uint16_t* x, int64_t ldx, const Int8Rows& q, bool few, hipStream_t s) {
+  const int pieces = (q.cols + 15) / 16 * 2;
+  if (pieces <= 64) return quantize<64, 1, F16, VEC>(x, ldx, q, s);
+  if (!few && pieces <= 256) return quantize<64, 4, F16, VEC>(x, ldx, q, s);
+  if (pieces <= 256) return quantize<256, 1, F16, VEC>(x, ldx, q, s);
+  if (!few && pieces <= 512) return quantize<64, 8, F16, VEC>(x, ldx, q, s);
+  if (!few && pieces <= 1024) return quantize<256, 4, F16, VEC>(x, ldx, q, s);
+  if (!few && pieces <= 2048) return quantize<256, 8, F16, VEC>(x, ldx, q, s);
+  if (pieces <= 1024) return quantize<1024, 1, F16, VEC>(x, ldx, q, s);
+  if (pieces <= 4096) return quantize<1024, 4, F16, VEC>(x, ldx, q, s);
+  return quantize<1024, 0, F16, VEC>(x, ldx, q, s);
+}
+
+template <bool F16, bool VEC>
+hipError_t dequantize(const Int8Rows& q, uint16_t* out, int64_t ldo, hipStream_t s) {
+  if (q.cols <= 512) {
+    dequantize_rows_kernel<64, F16, VEC><<<groups_for(q.rows, 4), kThreads, 0, s>>>(q, out, ldo);
+  } else {
+    dequantize_rows_kernel<256, F16, VEC><<<groups_for(q.rows, 1), kThreads, 0, s>>>(q, out, ldo);
+  }
+  return hipGetLastError();
+}
+
+bool pieces_at_16(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; }
+
+}  // namespace
+
+hipError_t launch_quantize_rows(const uint16_t* x, int64_t ldx, const Int8Rows& q, bool f16,
+                                hipStream_t s) {
+  if (q.rows == 0) return hipSuccess;
+  const bool vec = pieces_at_16(x, ldx), few = q.rows < 4 * int8_cus();
+  if (f16) return vec ? quantize<true, true>(x, ldx, q, few, s) : quantize<true, false>(x, ldx, q, few, s);
+  return vec ? quantize<false, true>(x, ldx, q, few, s) : quantize<false, false>(x, ldx, q, few, s);
+}
+
+hipError_t launch_dequantize_rows(const Int8Rows& q, uint16_t* out, int64_t ldo, bool f16,
+                                  hipStream_t s) {
+  if (q.rows == 0) return hipSuccess;
+  const bool vec = pieces_at_16(out, ldo);
+  if (f16) return vec ? dequantize<true, true>(q, out, ldo, s) : dequantize<true, false>(q, out, ldo, s);
+  return vec ? dequantize<false, true>(q, out, ldo, s) : dequantize<false, false>(q, out, ldo, s);
+}
+
+}  // namespace bnbx

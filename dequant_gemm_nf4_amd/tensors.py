@@ -10,7 +10,12 @@ import math
 
 import torch
 
-from . import (AdaptersDesc, Nf4State, RowGroupsDesc, bnbx_dequantize_nf4, bnbx_gemm_nf4_experts,
+from . import (BNBX_DTYPE_F32, AdaptersDesc, Int8RowsDesc, Nf4State, RowGroupsDesc,
+               bnbx_dequantize_nf4, bnbx_dequantize_rows_int8, bnbx_gemm_int8, bnbx_gemm_int8_dw,
+               bnbx_gemm_int8_dw_workspace_bytes, bnbx_gemm_int8_dx,
+               bnbx_gemm_int8_dx_workspace_bytes, bnbx_gemm_int8_workspace_bytes,
+               bnbx_linear_int8, bnbx_linear_int8_workspace_bytes, bnbx_quantize_rows_int8,
+               bnbx_gemm_nf4_experts,
                bnbx_gemm_nf4_adapters, bnbx_gemm_nf4_adapters_workspace_bytes,
                bnbx_gemm_nf4_experts_dx,
                bnbx_group_rows, bnbx_group_rows_workspace_bytes,
@@ -435,3 +440,217 @@ def linear_adapters(x: torch.Tensor, q: QuantizedWeight, rows: RowGroups, lora_a
 def _row(t: torch.Tensor) -> int:
     """Row stride of a stack of matrices."""
     return t.stride(1) if t.shape[1] > 1 else t.shape[2]
+
+
+# ---------------------------------------------------------------------------
+# rows of 8-bit codes
+# ---------------------------------------------------------------------------
+@dataclasses.dataclass
+class Int8Rows:
+    """Rows of int8 codes with one float32 scale a row (bnbx_int8_rows): a
+    weight [N, K], or activations [M, K].  ``codes`` is [rows, at least K
+    rounded up to 16], rows 16 bytes apart and aligned, zero behind K;
+    ``dtype`` the 16-bit type of the values they stand for."""
+
+    shape: tuple
+    codes: torch.Tensor   # int8 [rows, K rounded up to 16 or more]
+    scale: torch.Tensor   # float32 [rows]
+    dtype: torch.dtype = torch.bfloat16
+
+    def __post_init__(self):
+        # the kernels read all that the shape says
+        if len(self.shape) != 2 or self.shape[1] < 1:
+            raise ValueError(f"rows of codes are [rows, columns], not {self.shape}")
+        rows, cols = self.shape
+        if self.dtype not in DTYPES:
+            raise TypeError(f"rows of codes stand for bfloat16 or float16, not {self.dtype}")
+        if self.codes.dtype != torch.int8 or self.scale.dtype != torch.float32:
+            raise TypeError("rows of codes are int8 with float32 scales")
+        if (self.codes.dim() != 2 or self.codes.shape[0] != rows
+                or self.codes.shape[1] < -(-cols // 16) * 16
+                or (self.codes.stride(1) != 1 and self.codes.numel() > 0)):
+            raise ValueError(f"the codes must be [{rows}, {-(-cols // 16) * 16} or more], rows "
+                             f"contiguous, not {tuple(self.codes.shape)}")
+        if self.scale.shape != (rows,) or not self.scale.is_contiguous():
+            raise ValueError(f"the scales must be a contiguous vector of {rows}")
+        if self.scale.device != self.codes.device:
+            raise ValueError("codes and scales are on different devices")
+        if rows >= 2 ** 31 or cols >= 2 ** 31:
+            raise ValueError("rows and columns are numbered in 31 bits")
+
+    @property
+    def desc(self) -> Int8RowsDesc:
+        rows, cols = self.shape
+        ld = self.codes.stride(0) if rows > 1 else -(-cols // 16) * 16
+        return Int8RowsDesc(self.codes.data_ptr(), self.scale.data_ptr(), ld, rows, cols,
+                            DTYPES[self.dtype])
+
+
+def empty_int8_rows(shape, dtype: torch.dtype = torch.bfloat16, device="cuda") -> Int8Rows:
+    rows, cols = shape
+    return Int8Rows((rows, cols),
+                    torch.empty(rows, -(-cols // 16) * 16, dtype=torch.int8, device=device),
+                    torch.empty(rows, dtype=torch.float32, device=device), dtype)
+
+
+def _check_int8(name: str, q: Int8Rows, shape, dtype, device) -> None:
+    if tuple(q.shape) != tuple(shape) or q.dtype != dtype:
+        raise ValueError(f"{name} must be codes of {tuple(shape)} {dtype}, not "
+                         f"{tuple(q.shape)} {q.dtype}")
+    if q.codes.device != device:
+        raise ValueError(f"{name} is on {q.codes.device}, not on {device}")
+
+
+def _check_out(out: torch.Tensor, rows: int, cols: int, dtype, device) -> None:
+    _check_matrix("out", out, cols, dtype, device)
+    if out.shape[0] != rows:
+        raise ValueError(f"out has {out.shape[0]} rows, not {rows}")
+
+
+def _width(t: torch.Tensor) -> int:
+    """Row stride; of a matrix of one row (or none) its width."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _nbytes_of(t: torch.Tensor | None) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def quantize_rows(x: torch.Tensor, out: Int8Rows | None = None, stream=None) -> Int8Rows:
+    """bnbx_quantize_rows_int8: the codes and scales of a 16-bit matrix, row by
+    row."""
+    if x.dtype not in DTYPES:
+        raise TypeError(f"x must be bfloat16 or float16, not {x.dtype}")
+    if x.dim() != 2 or x.shape[1] < 1:
+        raise ValueError(f"x must be [rows, columns], not {tuple(x.shape)}")
+    _check_matrix("x", x, x.shape[1], x.dtype, x.device)
+    if out is not None:
+        _check_int8("out", out, x.shape, x.dtype, x.device)
+    with _on(x.device, stream):
+        q = out if out is not None else empty_int8_rows(x.shape, x.dtype, x.device)
+        bnbx_quantize_rows_int8(x, _width(x), q.desc, stream)
+    return q
+
+
+def dequantize_rows(q: Int8Rows, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """bnbx_dequantize_rows_int8: the 16-bit values of the codes."""
+    device = q.codes.device
+    if out is not None:
+        _check_out(out, *q.shape, q.dtype, device)
+    with _on(device, stream):
+        y = out if out is not None else torch.empty(q.shape, dtype=q.dtype, device=device)
+        bnbx_dequantize_rows_int8(q.desc, y, _width(y), stream)
+    return y
+
+
+def gemm_int8(x: Int8Rows, w: Int8Rows, out: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y = X . W^T from the codes of both (bnbx_gemm_int8): the int32 sums times
+    the scales of their row of X and row of W."""
+    (M, K), N, device = x.shape, w.shape[0], w.codes.device
+    _check_int8("w", w, (N, K), x.dtype, x.codes.device)
+    if out is not None:
+        _check_out(out, M, N, w.dtype, device)
+    with _on(device, stream):
+        y = out if out is not None else torch.empty(M, N, dtype=w.dtype, device=device)
+        nbytes = bnbx_gemm_int8_workspace_bytes(M, N, K)
+        ws = _scratch(workspace, nbytes, device) if nbytes else None
+        bnbx_gemm_int8(x.desc, w.desc, y, _width(y), ws, _nbytes_of(ws), stream)
+    return y
+
+
+def linear_int8(x: torch.Tensor, w: Int8Rows, out: torch.Tensor | None = None,
+                saved: Int8Rows | None = None, workspace: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """Y = X . W^T over 8-bit integers, X's rows quantized on the way
+    (bnbx_linear_int8).  ``saved`` takes X's codes, for gemm_int8_dw."""
+    N, K = w.shape
+    device = w.codes.device
+    _check_matrix("x", x, K, w.dtype, device)
+    M = x.shape[0]
+    if out is not None:
+        _check_out(out, M, N, w.dtype, device)
+    if saved is not None:
+        _check_int8("saved", saved, (M, K), w.dtype, device)
+    with _on(device, stream):
+        y = out if out is not None else torch.empty(M, N, dtype=w.dtype, device=device)
+        nbytes = bnbx_linear_int8_workspace_bytes(M, N, K, saved is not None)
+        ws = _scratch(workspace, nbytes, device) if nbytes else None
+        bnbx_linear_int8(x, _width(x), M, w.desc, saved.desc if saved is not None else None, y,
+                         _width(y), ws, _nbytes_of(ws), stream)
+    return y
+
+
+def _pieces(t: torch.Tensor, finite: bool) -> torch.Tensor:
+    """Rows as the gradients' kernels read them, in aligned pieces of eight:
+    the last piece readable, and behind the row finite where `finite`.  Rows
+    that are not so are copied, zeros behind them."""
+    rows, cols = t.shape
+    wide = -(-cols // 8) * 8
+    if cols == wide and (rows <= 1 or (t.stride(0) % 8 == 0 and t.stride(0) >= cols)) \
+            and t.data_ptr() % 16 == 0:
+        return t
+    if not finite and rows > 1 and t.stride(0) % 8 == 0 and t.stride(0) >= wide \
+            and t.data_ptr() % 16 == 0 and t.storage_offset() + (rows - 1) * t.stride(0) + wide \
+            <= t.untyped_storage().nbytes() // t.element_size():
+        return t
+    copy = t.new_zeros(rows, wide)
+    copy[:, :cols] = t
+    return copy[:, :cols]
+
+
+def _pitch(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+def gemm_int8_dx(dy: torch.Tensor, w: Int8Rows, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dX = dY . W_hat with the values of w's codes (bnbx_gemm_int8_dx, the
+    input gradient of linear_int8).  A dY whose rows are not whole aligned
+    pieces of eight values is copied first."""
+    N, K = w.shape
+    device = w.codes.device
+    _check_matrix("dy", dy, N, w.dtype, device)
+    M = dy.shape[0]
+    if out is not None:
+        _check_out(out, M, K, w.dtype, device)
+    with _on(device, stream):
+        dy = _pieces(dy, True)
+        y = out if out is not None else torch.empty(M, K, dtype=w.dtype, device=device)
+        nbytes = bnbx_gemm_int8_dx_workspace_bytes(M, N, K)
+        ws = _scratch(workspace, nbytes, device) if nbytes else None
+        bnbx_gemm_int8_dx(dy, _pitch(dy), M, w.desc, y, _width(y), ws, _nbytes_of(ws), stream)
+    return y
+
+
+def gemm_int8_dw(dy: torch.Tensor, x: Int8Rows, out: torch.Tensor | None = None,
+                 dtype: torch.dtype | None = None, workspace: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """dW = dY^T . X_hat with the values of x's codes (bnbx_gemm_int8_dw): the
+    gradient of a weight [N, K] from activations saved in 8 bits, in x's type
+    or float32 (``out``'s, else ``dtype``, else x's).  With few columns of dY it
+    is the gradient of a low-rank adapter's first factor."""
+    M, K = x.shape
+    device = x.codes.device
+    if dy.dim() != 2 or dy.shape[0] != M or dy.shape[1] < 1:
+        raise ValueError(f"dy must be [{M}, columns], not {tuple(dy.shape)}")
+    N = dy.shape[1]
+    _check_matrix("dy", dy, N, x.dtype, device)
+    if out is not None:
+        if dtype is not None and out.dtype != dtype:
+            raise TypeError(f"out is {out.dtype}, not {dtype}")
+        dtype = out.dtype
+    dtype = x.dtype if dtype is None else dtype
+    if dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"the gradient is {x.dtype} or float32, not {dtype}")
+    if out is not None:
+        _check_out(out, N, K, dtype, device)
+    with _on(device, stream):
+        dy = _pieces(dy, False)
+        y = out if out is not None else torch.empty(N, K, dtype=dtype, device=device)
+        nbytes = bnbx_gemm_int8_dw_workspace_bytes(M, N, K)
+        ws = _scratch(workspace, nbytes, device) if nbytes else None
+        bnbx_gemm_int8_dw(dy, _pitch(dy), N, x.desc, y, _width(y),
+                          BNBX_DTYPE_F32 if dtype == torch.float32 else DTYPES[dtype], ws,
+                          _nbytes_of(ws), stream)
+    return y
