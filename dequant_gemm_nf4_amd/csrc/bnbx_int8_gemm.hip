@@ -26,6 +26,10 @@ constexpr int kThreads = 256;
 constexpr int BK = 128;
 constexpr int kXcds = 8;
 
+// Scheduling-group masks (AMDGPU sched_group_barrier).
+constexpr int kSgMfma = 0x008, kSgValu = 0x002, kSgSalu = 0x004, kSgVmem = 0x010,
+              kSgDsRead = 0x100;
+
 struct GemmArgs {
   const int8_t* x;
   const int8_t* w;
@@ -151,28 +155,49 @@ __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
 
-  constexpr int C = CW + CX, H = C / 2;
+  // One substep's products with the operand reads of the next one and `nc` copies
+  // laid between them.
+  auto interleave = [&](int nc) {
+    constexpr int N = FM * FN;
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
+      if (q < FM + FN) __builtin_amdgcn_sched_group_barrier(kSgDsRead, 1, 0);
+      if (q * nc / N != (q + 1) * nc / N) {
+        __builtin_amdgcn_sched_group_barrier(kSgSalu, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kSgValu, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kSgVmem, 1, 0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  constexpr int C = CW + CX;
+  constexpr int C3 = C / 2;   // copies of a step that go out in substep 3 before it
   copies(buf0, t0, 0, C);
-  copies(buf1, t0 + 1, 0, H);
+  copies(buf1, t0 + 1, 0, C3);
   land();
   reads(buf0, 0, 0);
   auto step = [&](int t, uint8_t* cur, uint8_t* next) {
-    copies(next, t + 1, H, C);
-    reads(cur, 1, 1);
-    products(0);
-    reads(cur, 2, 0);
-    products(1);
-    reads(cur, 3, 1);
-    products(0);
-    land();
-    copies(cur, t + 2, 0, H);
-    reads(next, 0, 0);
-    products(1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (s == 0) copies(next, t + 1, C3, C);
+      if (s == 3) {
+        land();
+        copies(cur, t + 2, 0, C3);
+      }
+      reads(s == 3 ? next : cur, (s + 1) & 3, (s & 1) ^ 1);
+      products(s & 1);
+      interleave(s == 3 ? C3 : s == 0 ? C - C3 : 0);
+    }
   };
-  for (int t = t0; t < t1; t += 2) {
+  int t = t0;
+  for (; t + 1 < t1; t += 2) {
     step(t, buf0, buf1);
-    if (t + 1 < t1) step(t + 1, buf1, buf0);
+    step(t + 1, buf1, buf0);
   }
+  if (t < t1) step(t, buf0, buf1);
 
   if constexpr (SPLIT) {
     int* part = a.part + (int64_t)blockIdx.y * a.M * a.ldp;
@@ -195,25 +220,23 @@ __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
     return;
   }
 
-  // Results through LDS, a wave's own quarter of the buffers: rows of 32 FN
-  // values, 16-byte chunks permuted by the row.
+  // Results through LDS, 32 tokens at a time in a wave's own part of a buffer: rows
+  // of 32 FN values, 16-byte chunks permuted by the row, so that a row is written by
+  // neighbouring lanes.
   land();   // every wave has read its operands, and no copy is in flight
   constexpr int CH = 4 * FN;
-  uint8_t* const mine = (wave < 2 ? buf0 : buf1) + (wave & 1) * 32 * FM * 64 * FN;
-  static_assert(2 * 32 * FM * 64 * FN <= (TM + TN) * BK, "results fit the buffers");
-  const rsrc8_t rs = rsrc8(a.sw, (int64_t)a.N * 4);
-  f32x4_t sw[FN][4];
-#pragma unroll
-  for (int i = 0; i < FN; ++i)
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-      sw[i][g] = __builtin_bit_cast(
-          f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                       rs, 4u * (uint32_t)(n0 + wn + 32 * i + 8 * g + 4 * half), 0, 0));
+  static_assert(4 * 32 * CH * 16 <= (TM + TN) * BK, "results fit a buffer");
+  uint8_t* const mine = buf0 + wave * 32 * CH * 16;
+  // the tile's scales of W (64 a wave, TN of them wanted)
+  copy4_lds(rsrc8(a.sw, (int64_t)a.N * 4), buf1 + wave * 256,
+            4u * (uint32_t)(n0 + 64 * wave + lane), 0);
+  land();
+  const bool vec = ((uintptr_t)a.y % 16 == 0) && a.ldy % 8 == 0;
 #pragma unroll
   for (int j = 0; j < FM; ++j) {
-    const int r = 32 * j + col, m = m0 + wm + r;
-    const float sx = m < a.M ? a.sx[m] : 0.0f;
+    __builtin_amdgcn_sched_barrier(0);   // one tile's values in registers at a time
+    const int mj = m0 + wm + 32 * j;
+    const float sx = mj + col < a.M ? a.sx[mj + col] : 0.0f;
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -221,17 +244,16 @@ __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
         int v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e];
-        *(u32x2_t*)(mine + r * 64 * FN + 16 * ((4 * i + g) ^ (r & (CH - 1))) + 8 * half) =
-            scaled4<F16>(v, sx, sw[i][g]);
+        *(u32x2_t*)(mine + 16 * (col * CH + ((4 * i + g) ^ (col & (CH - 1)))) + 8 * half) =
+            scaled4<F16>(v, sx, *(const f32x4_t*)(buf1 + 4 * (wn + 32 * i + 8 * g + 4 * half)));
       }
-  }
-  const bool vec = ((uintptr_t)a.y % 16 == 0) && a.ldy % 8 == 0;
-#pragma unroll 4
-  for (int i = 0; i < 32 * FM * CH / 64; ++i) {
-    const int r = (i * 64 + lane) / CH, ch = lane % CH;
-    const int m = m0 + wm + r, n = n0 + wn + 8 * ch;
-    const u32x4_t v = *(const u32x4_t*)(mine + r * 64 * FN + 16 * (ch ^ (r & (CH - 1))));
-    if (m < a.M && n < a.N) store8(a.y + (int64_t)m * a.ldy + n, v, a.N - n, vec);
+#pragma unroll 2
+    for (int k = 0; k < 32 * CH / 64; ++k) {
+      const int r = (k * 64 + lane) / CH, ch = lane % CH;
+      const int m = mj + r, n = n0 + wn + 8 * ch;
+      const u32x4_t v = *(const u32x4_t*)(mine + 16 * (r * CH + (ch ^ (r & (CH - 1)))));
+      if (m < a.M && n < a.N) store8(a.y + (int64_t)m * a.ldy + n, v, a.N - n, vec);
+    }
   }
 }
 

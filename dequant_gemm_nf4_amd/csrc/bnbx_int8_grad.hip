@@ -29,6 +29,10 @@ constexpr int kThreads = 256;
 constexpr int BT = 64;
 constexpr int kXcds = 8;
 
+// Scheduling-group masks (AMDGPU sched_group_barrier).
+constexpr int kSgMfma = 0x008, kSgValu = 0x002, kSgSalu = 0x004, kSgVmem = 0x010,
+              kSgDsRead = 0x100;
+
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 typedef __attribute__((ext_vector_type(2))) int i32x2_t;
 
@@ -124,42 +128,49 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
     return FR >= 4 ? 4 * (row & 3) : FR == 2 ? 4 * ((row >> 1) & 1) : 0;
   };
   uint32_t aoff[CA];
-  int ach[CA];
 #pragma unroll
   for (int i = 0; i < CA; ++i) {
     const int row = (wave * CA + i) * AR + lane / ACH;
     const int ch = (lane % ACH) ^ turn_a(row);
-    ach[i] = 8 * ch;
     const bool in = TURNED ? r0 + 8 * ch < a.R : r0 + row < a.R;
     aoff[i] = in ? (uint32_t)row * (uint32_t)a.ldy * 2u + 16u * ch : kFar8;
   }
+  // !TURNED: the first t of this lane's chunk; instructions 4 rows pairs apart
+  // permute it by 4
+  const int ach0 = 8 * ((lane & 7) ^ ((lane >> 4) & 3));
   const rsrc8_t ra = rsrc8(a.dy + (int64_t)r0 * a.ldy, (int64_t)kFar8);
-  auto copies = [&](uint8_t* buf, int t, bool first) {
+  auto rows_left = [&](int t) {
     const int left = a.T - t * BT;
-    const int rows = left < 0 ? 0 : left < BT ? left : BT;
-    if (first) {
-      const rsrc8_t rv = rsrc8(a.codes + c0 + (int64_t)t * BT * a.ldv, rows * a.ldv);
+    return left < 0 ? 0 : left < BT ? left : BT;
+  };
+  auto copy_codes = [&](uint8_t* buf, int t) {
+    const int rows = rows_left(t);
+    const rsrc8_t rv = rsrc8(a.codes + c0 + (int64_t)t * BT * a.ldv, rows * a.ldv);
 #pragma unroll
-      for (int i = 0; i < CV; ++i)
-        copy16_lds(rv, buf + kA + (wave * CV + i) * 1024, voff[i], 0);
-      const rsrc8_t rs = rsrc8(a.scale + (int64_t)t * BT, rows * 4);
-      copy4_lds(rs, buf + kA + kV + wave * BT * 4, 4u * lane, 0);
-    } else if constexpr (TURNED) {
-      const rsrc8_t rt = rsrc8(a.dy + r0 + (int64_t)t * BT * a.ldy, rows * a.ldy * 2);
+    for (int i = 0; i < CV; ++i) copy16_lds(rv, buf + kA + (wave * CV + i) * 1024, voff[i], 0);
+    const rsrc8_t rs = rsrc8(a.scale + (int64_t)t * BT, rows * 4);
+    copy4_lds(rs, buf + kA + kV + wave * BT * 4, 4u * lane, 0);
+  };
+  auto copy_dy = [&](uint8_t* buf, int t, int i0, int i1) {
+    if constexpr (TURNED) {
+      const rsrc8_t rt = rsrc8(a.dy + r0 + (int64_t)t * BT * a.ldy, rows_left(t) * a.ldy * 2);
 #pragma unroll
-      for (int i = 0; i < CA; ++i) copy16_lds(rt, buf + (wave * CA + i) * 1024, aoff[i], 0);
+      for (int i = i0; i < i1; ++i) copy16_lds(rt, buf + (wave * CA + i) * 1024, aoff[i], 0);
     } else {
+      const int left = a.T - t * BT;
+      const bool ok0 = ach0 < left, ok1 = (ach0 ^ 32) < left;
 #pragma unroll
-      for (int i = 0; i < CA; ++i)
-        copy16_lds(ra, buf + (wave * CA + i) * 1024, ach[i] < left ? aoff[i] : kFar8,
-                   (uint32_t)t * (BT * 2));
+      for (int i = i0; i < i1; ++i)
+        copy16_lds(ra, buf + (wave * CA + i) * 1024,
+                   (((wave * CA + i) & 1) ? ok1 : ok0) ? aoff[i] : kFar8, (uint32_t)t * (BT * 2));
     }
   };
 
   // ---- operands -----------------------------------------------------------
   u32x4_t oa[2][FR];     // gradients
-  u32x2_t oc[2][FC];     // codes
-  f32x4_t os[2][2];      // scales of the lane's eight t
+  u32x4_t ov[2][FC];     // values
+  u32x2_t oc[FC];        // codes
+  f32x4_t os[2];         // scales of the lane's eight t
   const int g = lane >> 4, l16 = lane & 15;
   // Codes: 16 lanes read eight rows t of 16 columns (two lanes a row), 32 lanes
   // eight rows of 32 bytes, each row in other banks.
@@ -172,33 +183,49 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
       vrd[f] = kA + t * TC + 16 * ch + 8 * (l16 & 1);
     }
   }
+  const uint32_t srd = kA + kV + wave * BT * 4 + 32 * half;
   // Gradients: row col of a tile, chunk 2 s + half; or four rows t of 16 values in
-  // 16 lanes (four lanes a row), twice, each row in other banks.
-  uint32_t ard[4];
+  // 16 lanes (four lanes a row), twice, each row in other banks.  turn_a moves
+  // whole groups of four chunks (two with FR = 2), so tiles four apart differ by a
+  // constant.
+  constexpr int NRD = TURNED ? (FR < 4 ? FR : 4) : 4;
+  uint32_t ard[NRD];
+  if constexpr (TURNED) {
+    const int t = 8 * (g >> 1) + (l16 >> 2);   // + 16 s + 4 j, the same turn_a for FR >= 4
 #pragma unroll
-  for (int s = 0; s < 4; ++s) ard[s] = col * BT * 2 + 16 * ((2 * s + half) ^ turn_a(col));
-  auto turned_at = [&](int s, int f, int j) {
-    const int t = 16 * s + 8 * (g >> 1) + 4 * j + (l16 >> 2);
-    const int ch = (4 * f + 2 * (g & 1) + ((l16 & 3) >> 1)) ^ turn_a(t);
-    return (uint32_t)(t * TR * 2 + 16 * ch + 8 * (l16 & 1));
+    for (int f = 0; f < NRD; ++f)
+      ard[f] = t * TR * 2 + 16 * ((4 * f + 2 * (g & 1) + ((l16 & 3) >> 1)) ^ turn_a(t)) +
+               8 * (l16 & 1);
+  } else {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) ard[s] = col * BT * 2 + 16 * ((2 * s + half) ^ turn_a(col));
+  }
+  auto read_codes = [&](const uint8_t* buf, int s) {
+#pragma unroll
+    for (int f = 0; f < FC; ++f) oc[f] = read_tr8(buf + vrd[f] + 16 * s * TC);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) os[j] = *(const f32x4_t*)(buf + srd + 64 * s + 16 * j);
   };
-  auto reads = [&](const uint8_t* buf, int s, int set) {
-#pragma unroll
-    for (int f = 0; f < FC; ++f) oc[set][f] = read_tr8(buf + vrd[f] + 16 * s * TC);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      os[set][j] =
-          *(const f32x4_t*)(buf + kA + kV + wave * BT * 4 + 4 * (16 * s + 8 * half + 4 * j));
+  auto read_dy = [&](const uint8_t* buf, int s, int set) {
 #pragma unroll
     for (int f = 0; f < FR; ++f) {
       if constexpr (TURNED) {
-        const u32x2_t lo = read_tr16(buf + turned_at(s, f, 0));
-        const u32x2_t hi = read_tr16(buf + turned_at(s, f, 1));
+        const uint8_t* p = buf + ard[f % NRD] + 16 * s * TR * 2 + f / NRD * 256;
+        const u32x2_t lo = read_tr16(p), hi = read_tr16(p + 4 * TR * 2);
         oa[set][f] = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
       } else {
         oa[set][f] = *(const u32x4_t*)(buf + 32 * f * BT * 2 + ard[s]);
       }
     }
+  };
+  auto convert = [&](int set) {
+#pragma unroll
+    for (int i = 0; i < FC; ++i)
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        ov[set][i][p] =
+            pack16x2<F16>(code_value(oc[i][p / 2], 2 * (p & 1), os[p / 2][2 * (p & 1)]),
+                          code_value(oc[i][p / 2], 2 * (p & 1) + 1, os[p / 2][2 * (p & 1) + 1]));
   };
   f32x16_t acc[FC][FR];
 #pragma unroll
@@ -209,63 +236,100 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
   auto products = [&](int set) {
 #pragma unroll
-    for (int i = 0; i < FC; ++i) {
-      u32x4_t v;
+    for (int j = 0; j < FR; ++j)
 #pragma unroll
-      for (int p = 0; p < 4; ++p)
-        v[p] = pack16x2<F16>(
-            code_value(oc[set][i][p / 2], 2 * (p & 1), os[set][p / 2][2 * (p & 1)]),
-            code_value(oc[set][i][p / 2], 2 * (p & 1) + 1, os[set][p / 2][2 * (p & 1) + 1]));
+      for (int i = 0; i < FC; ++i)
+        acc[i][j] = mfma_32x32x16<F16>(ov[set][i], oa[set][j], acc[i][j]);
+  };
+  // One substep's products with the reads and the conversion of the next one laid
+  // between them, and `nc` copies.
+  auto interleave = [&](int nc) {
+    constexpr int N = FC * FR;
+    __builtin_amdgcn_sched_group_barrier(kSgDsRead, FC + 2, 0);
 #pragma unroll
-      for (int j = 0; j < FR; ++j) acc[i][j] = mfma_32x32x16<F16>(v, oa[set][j], acc[i][j]);
+    for (int q = 0; q < N; ++q) {
+      __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
+      if (q < N / 2) {
+        __builtin_amdgcn_sched_group_barrier(kSgDsRead, (TURNED ? 4 : 2) / FC, 0);
+        __builtin_amdgcn_sched_group_barrier(kSgValu, 2, 0);
+      } else {
+        __builtin_amdgcn_sched_group_barrier(kSgValu, 44 / FR, 0);
+      }
+      if (q * nc / N != (q + 1) * nc / N) {
+        __builtin_amdgcn_sched_group_barrier(kSgSalu, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(kSgVmem, 1, 0);
+      }
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
   auto land = [&] {
     __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
 
-  copies(buf0, t0, true);
-  copies(buf0, t0, false);
-  copies(buf1, t0 + 1, true);
+  copy_codes(buf0, t0);
+  copy_dy(buf0, t0, 0, CA);
+  copy_codes(buf1, t0 + 1);
   land();
-  reads(buf0, 0, 0);
+  read_codes(buf0, 0);
+  read_dy(buf0, 0, 0);
+  convert(0);
   auto step = [&](int t, uint8_t* cur, uint8_t* next) {
-    copies(next, t + 1, false);
-    reads(cur, 1, 1);
-    products(0);
-    reads(cur, 2, 0);
-    products(1);
-    reads(cur, 3, 1);
-    products(0);
-    land();
-    copies(cur, t + 2, true);
-    reads(next, 0, 0);
-    products(1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int set = s & 1;
+      if (s == 3) {
+        land();
+        copy_codes(cur, t + 2);
+      }
+      if (s == 0) copy_dy(next, t + 1, 0, (CA + 1) / 2);
+      if (s == 1) copy_dy(next, t + 1, (CA + 1) / 2, CA);
+      const uint8_t* from = s == 3 ? next : cur;
+      read_codes(from, (s + 1) & 3);
+      read_dy(from, (s + 1) & 3, set ^ 1);
+      products(set);
+      convert(set ^ 1);
+      interleave(s == 3 ? CV + 1 : s == 0 ? (CA + 1) / 2 : s == 1 ? CA / 2 : 0);
+    }
   };
-  for (int t = t0; t < t1; t += 2) {
+  int t = t0;
+  for (; t + 1 < t1; t += 2) {
     step(t, buf0, buf1);
-    if (t + 1 < t1) step(t + 1, buf1, buf0);
+    step(t + 1, buf1, buf0);
   }
+  if (t < t1) step(t, buf0, buf1);
 
-  // ---- results: value 4 g + e of a tile is row col, column 8 g + 4 half + e ----
+  // ---- results: value 4 q + e of a tile is row col, column 8 q + 4 half + e ----
+  // Through LDS, 32 rows at a time in a wave's own part of a buffer (16-byte chunks
+  // permuted by the row), so that a row is written by neighbouring lanes.
   void* const out = SPLIT ? (void*)(a.part + (int64_t)blockIdx.y * a.R * a.ldp) : a.out;
   constexpr int KIND = SPLIT ? (int)kOutF32 : OUT;
+  constexpr int OCH = 8 * FC, OR = 64 / OCH;   // chunks a row, rows an instruction
+  static_assert(4 * 32 * OCH * 16 <= kBuf, "results fit a buffer");
   const int64_t ldo = SPLIT ? a.ldp : a.ldo;
+  const int cend = SPLIT ? (int)a.ldp : a.C;
   const bool vec = SPLIT || whole4<KIND>(out, ldo);
+  auto turn_o = [](int row) { return FC == 2 ? row & 15 : (row >> 1) & 7; };
+  land();   // every wave has read its operands, and no copy is in flight
+  uint8_t* const mine = buf0 + wave * 32 * OCH * 16;
 #pragma unroll
   for (int j = 0; j < FR; ++j) {
-    const int r = r0 + 32 * j + col;
-    if (r >= a.R) continue;
 #pragma unroll
     for (int i = 0; i < FC; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int c = c0 + 32 * (wave * FC + i) + 8 * q + 4 * half;
         const f32x4_t v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
                            acc[i][j][4 * q + 3]};
-        if (c < a.C) store4<KIND>(out, (int64_t)r * ldo + c, v, SPLIT ? 4 : a.C - c, vec);
+        *(f32x4_t*)(mine + 16 * (col * OCH + ((8 * i + 2 * q + half) ^ turn_o(col)))) = v;
       }
+#pragma unroll 2
+    for (int k = 0; k < 32 / OR; ++k) {
+      const int row = k * OR + lane / OCH, ch = lane % OCH;
+      const f32x4_t v = *(const f32x4_t*)(mine + 16 * (row * OCH + (ch ^ turn_o(row))));
+      const int r = r0 + 32 * j + row, c = c0 + 32 * FC * wave + 4 * ch;
+      if (r < a.R && c < cend) store4<KIND>(out, (int64_t)r * ldo + c, v, cend - c, vec);
+    }
   }
 }
 
