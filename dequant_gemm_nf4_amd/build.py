@@ -25,7 +25,7 @@ ROWS_SOURCES = ["bnbx_rows_api.hip", "bnbx_tables.hip", "bnbx_rows_group.hip",
                 "bnbx_rows_lora.hip", "bnbx_rows_gemm.hip", "bnbx_rows_gemm_lora.hip",
                 "bnbx_rows_dx_stream.hip"]
 INT8_SOURCES = ["bnbx_int8_api.hip", "bnbx_int8_rows.hip", "bnbx_int8_gemm.hip",
-                "bnbx_int8_grad.hip"]
+                "bnbx_int8_few.hip", "bnbx_int8_rows16.hip", "bnbx_int8_grad.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -25,6 +25,17 @@ size_t int8_gemm_workspace(int M, int N, int K);
 hipError_t launch_int8_gemm(const Int8Rows& x, const Int8Rows& w, uint16_t* y, int64_t ldy,
                             bool f16, void* workspace, hipStream_t stream);
 
+// The same for few rows of X, in one launch: x null, the codes q; else X's 16-bit
+// rows, whose codes are written to q where it has any.
+bool int8_few_takes(int M, int K);
+hipError_t launch_int8_few(const uint16_t* x, int64_t ldx, const Int8Rows& q, const Int8Rows& w,
+                           uint16_t* y, int64_t ldy, bool f16, hipStream_t stream);
+
+// The same for up to 64 rows of X, without a workspace.
+bool int8_rows16_takes(int M);
+hipError_t launch_int8_rows16(const Int8Rows& x, const Int8Rows& w, uint16_t* y, int64_t ldy,
+                              bool f16, hipStream_t stream);
+
 // out[r, c] = sum_t A(r, t) v(t, c) over the values v of the codes [T, C], T and
 // C their rows and columns: A(r, t) is dy[r ldy + t], or dy[t ldy + r] (`turned`).
 enum { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2 };

@@ -95,7 +95,7 @@ int bnbx_dequantize_rows_int8(const bnbx_int8_rows* q, uint16_t* out, int64_t ld
 }
 
 size_t bnbx_gemm_int8_workspace_bytes(int M, int N, int K) {
-  if (M < 1 || N < 1 || K < 1 || K > BNBX_INT8_MAX_COLS) return 0;
+  if (M < 1 || N < 1 || K < 1 || K > BNBX_INT8_MAX_COLS || int8_few_takes(M, K)) return 0;
   return int8_gemm_workspace(M, N, K);
 }
 
@@ -110,14 +110,18 @@ int bnbx_gemm_int8(const bnbx_int8_rows* x, const bnbx_int8_rows* w, uint16_t* y
   if (s != BNBX_OK) return s;
   if (x->cols > BNBX_INT8_MAX_COLS) return BNBX_E_UNSUPPORTED;
   if (x->rows == 0) return BNBX_OK;
+  const bool f16 = x->dtype == BNBX_DTYPE_F16;
+  if (int8_few_takes(x->rows, x->cols))
+    return status8(launch_int8_few(nullptr, 0, rows8(x), rows8(w), y, ldy, f16,
+                                   (hipStream_t)stream));
   s = check_workspace8(workspace, workspace_bytes, int8_gemm_workspace(x->rows, w->rows, x->cols));
   if (s != BNBX_OK) return s;
-  return status8(launch_int8_gemm(rows8(x), rows8(w), y, ldy, x->dtype == BNBX_DTYPE_F16,
+  return status8(launch_int8_gemm(rows8(x), rows8(w), y, ldy, f16,
                                   workspace, (hipStream_t)stream));
 }
 
 size_t bnbx_linear_int8_workspace_bytes(int M, int N, int K, int saved) {
-  if (M < 1 || N < 1 || K < 1 || K > BNBX_INT8_MAX_COLS) return 0;
+  if (M < 1 || N < 1 || K < 1 || K > BNBX_INT8_MAX_COLS || int8_few_takes(M, K)) return 0;
   return (saved ? 0 : codes_bytes(M, K)) + int8_gemm_workspace(M, N, K);
 }
 
@@ -143,8 +147,12 @@ int bnbx_linear_int8(const uint16_t* x, int64_t ldx, int M, const bnbx_int8_rows
                        bnbx_linear_int8_workspace_bytes(M, N, K, saved != nullptr));
   if (s != BNBX_OK) return s;
   const bool f16 = w->dtype == BNBX_DTYPE_F16;
+  Int8Rows q{nullptr, nullptr, 0, M, K};
+  if (int8_few_takes(M, K)) {
+    if (saved != nullptr) q = rows8(saved);
+    return status8(launch_int8_few(x, ldx, q, rows8(w), y, ldy, f16, (hipStream_t)stream));
+  }
   uint8_t* ws = (uint8_t*)workspace;
-  Int8Rows q;
   if (saved != nullptr) {
     q = rows8(saved);
   } else {

@@ -17,6 +17,8 @@
 // wave has read its last operands of step t), and under substep 3's products the
 // first operands of step t+1 are read and the copies of step t+2 begin, into the
 // buffer that step t has left.
+#include <type_traits>
+
 #include "bnbx_int8_device.hpp"
 
 namespace bnbx {
@@ -81,12 +83,16 @@ __device__ __forceinline__ bool tile_of(int id, int tiles_m, int tiles_n, int& t
   return true;
 }
 
-template <int FM, int FN, bool F16, bool SPLIT>
+// ND: buffers, 2 or 4.
+template <int FM, int FN, int ND, bool F16, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
   constexpr int TM = 64 * FM, TN = 64 * FN;
   constexpr int CW = TN / 32, CX = TM / 32;   // copies a wave and step
-  __shared__ __attribute__((aligned(16))) uint8_t buf0[(TM + TN) * BK];
-  __shared__ __attribute__((aligned(16))) uint8_t buf1[(TM + TN) * BK];
+  constexpr int kBuf = (TM + TN) * BK;
+  __shared__ __attribute__((aligned(16))) uint8_t buf0[kBuf];
+  __shared__ __attribute__((aligned(16))) uint8_t buf1[kBuf];
+  __shared__ __attribute__((aligned(16))) uint8_t buf2[ND > 2 ? kBuf : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t buf3[ND > 2 ? kBuf : 16];
   int tm, tn;
   if (!tile_of(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn)) return;
   const int m0 = tm * TM, n0 = tn * TN;
@@ -150,10 +156,13 @@ __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
 #pragma unroll
       for (int j = 0; j < FM; ++j) acc[i][j] = mfma_i8_32x32x32(ow[set][i], ox[set][j], acc[i][j]);
   };
-  auto land = [&] {
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+  // all but the last `out` of this wave's copies have landed, and every wave is here
+  auto land = [&](auto out) {
+    constexpr int n = decltype(out)::value;
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | (n >> 4) << 14);   // vmcnt(n)
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
+  using All = std::integral_constant<int, 0>;
 
   // One substep's products with the operand reads of the next one and `nc` copies
   // laid between them.
@@ -173,19 +182,24 @@ __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
   };
 
   constexpr int C = CW + CX;
-  constexpr int C3 = C / 2;   // copies of a step that go out in substep 3 before it
+  constexpr int C3 = C / 2;   // copies of a step that go out in substep 3, as its buffer is left
+  using Ahead = std::integral_constant<int, (ND - 2) * C>;   // copies of later steps
   copies(buf0, t0, 0, C);
-  copies(buf1, t0 + 1, 0, C3);
-  land();
+  if constexpr (ND > 2) {
+    copies(buf1, t0 + 1, 0, C);
+    copies(buf2, t0 + 2, 0, C);
+  }
+  copies(ND > 2 ? buf3 : buf1, t0 + ND - 1, 0, C3);
+  land(std::integral_constant<int, (ND - 2) * C + C3>{});
   reads(buf0, 0, 0);
-  auto step = [&](int t, uint8_t* cur, uint8_t* next) {
+  auto step = [&](int t, uint8_t* last, uint8_t* cur, uint8_t* next) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      if (s == 0) copies(next, t + 1, C3, C);
+      if (s == 0) copies(last, t + ND - 1, C3, C);
       if (s == 3) {
-        land();
-        copies(cur, t + 2, 0, C3);
+        land(Ahead{});
+        copies(cur, t + ND, 0, C3);
       }
       reads(s == 3 ? next : cur, (s + 1) & 3, (s & 1) ^ 1);
       products(s & 1);
@@ -193,11 +207,23 @@ __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
     }
   };
   int t = t0;
-  for (; t + 1 < t1; t += 2) {
-    step(t, buf0, buf1);
-    step(t + 1, buf1, buf0);
+  if constexpr (ND == 2) {
+    for (; t + 1 < t1; t += 2) {
+      step(t, buf1, buf0, buf1);
+      step(t + 1, buf0, buf1, buf0);
+    }
+    if (t < t1) step(t, buf1, buf0, buf1);
+  } else {
+    for (; t + 3 < t1; t += 4) {
+      step(t, buf3, buf0, buf1);
+      step(t + 1, buf0, buf1, buf2);
+      step(t + 2, buf1, buf2, buf3);
+      step(t + 3, buf2, buf3, buf0);
+    }
+    if (t < t1) step(t, buf3, buf0, buf1);
+    if (t + 1 < t1) step(t + 1, buf0, buf1, buf2);
+    if (t + 2 < t1) step(t + 2, buf1, buf2, buf3);
   }
-  if (t < t1) step(t, buf0, buf1);
 
   if constexpr (SPLIT) {
     int* part = a.part + (int64_t)blockIdx.y * a.M * a.ldp;
@@ -223,14 +249,14 @@ __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
   // Results through LDS, 32 tokens at a time in a wave's own part of a buffer: rows
   // of 32 FN values, 16-byte chunks permuted by the row, so that a row is written by
   // neighbouring lanes.
-  land();   // every wave has read its operands, and no copy is in flight
+  land(All{});   // every wave has read its operands, and no copy is in flight
   constexpr int CH = 4 * FN;
   static_assert(4 * 32 * CH * 16 <= (TM + TN) * BK, "results fit a buffer");
   uint8_t* const mine = buf0 + wave * 32 * CH * 16;
   // the tile's scales of W (64 a wave, TN of them wanted)
   copy4_lds(rsrc8(a.sw, (int64_t)a.N * 4), buf1 + wave * 256,
             4u * (uint32_t)(n0 + 64 * wave + lane), 0);
-  land();
+  land(All{});
   const bool vec = ((uintptr_t)a.y % 16 == 0) && a.ldy % 8 == 0;
 #pragma unroll
   for (int j = 0; j < FM; ++j) {
@@ -309,23 +335,25 @@ hipError_t launch(const GemmArgs& a, int f, hipStream_t s) {
   const int total = a.tiles_m * a.tiles_n;
   const dim3 grid((total + kXcds - 1) / kXcds * kXcds, a.splits);
   if (f == 4)
-    int8_gemm_kernel<4, 4, F16, SPLIT><<<grid, kThreads, 0, s>>>(a);
+    int8_gemm_kernel<4, 4, 2, F16, SPLIT><<<grid, kThreads, 0, s>>>(a);
   else if (f == 2)
-    int8_gemm_kernel<2, 2, F16, SPLIT><<<grid, kThreads, 0, s>>>(a);
+    int8_gemm_kernel<2, 2, 4, F16, SPLIT><<<grid, kThreads, 0, s>>>(a);
   else
-    int8_gemm_kernel<1, 1, F16, SPLIT><<<grid, kThreads, 0, s>>>(a);
+    int8_gemm_kernel<1, 1, 4, F16, SPLIT><<<grid, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t int8_gemm_workspace(int M, int N, int K) {
+  if (int8_rows16_takes(M)) return 0;
   const Form f = form_of(M, N, K);
   return f.splits > 1 ? (size_t)f.splits * M * ((N + 3) / 4 * 4) * sizeof(int) : 0;
 }
 
 hipError_t launch_int8_gemm(const Int8Rows& x, const Int8Rows& w, uint16_t* y, int64_t ldy,
                             bool f16, void* workspace, hipStream_t s) {
+  if (int8_rows16_takes(x.rows)) return launch_int8_rows16(x, w, y, ldy, f16, s);
   const Form f = form_of(x.rows, w.rows, x.cols);
   GemmArgs a{};
   a.x = x.codes;

@@ -20,6 +20,8 @@
 // codes, scales and gradients.  The pipeline is that of the forward product: the
 // operands of a substep are read during the products of the one before, with one
 // wait and barrier a step before the last substep.
+#include <type_traits>
+
 #include "bnbx_int8_device.hpp"
 
 namespace bnbx {
@@ -89,14 +91,17 @@ __device__ __forceinline__ bool whole4(const void* out, int64_t ldo) {
   return (uintptr_t)out % (OUT == kOutF32 ? 16 : 8) == 0 && ldo % 4 == 0;
 }
 
-// OUT: kOutBf16 / kOutF16 / kOutF32; SPLIT: fp32 partial sums instead.
-template <int FR, int FC, bool TURNED, bool F16, int OUT, bool SPLIT>
+// ND: buffers, 2 or 4.  OUT: kOutBf16 / kOutF16 / kOutF32; SPLIT: fp32 partial sums
+// instead.
+template <int FR, int FC, int ND, bool TURNED, bool F16, int OUT, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
   constexpr int TR = 32 * FR, TC = 128 * FC;
   constexpr int kA = TR * BT * 2, kV = BT * TC, kBuf = kA + kV + 4 * BT * 4;
   constexpr int CA = FR, CV = 2 * FC;   // copies a wave and step
   __shared__ __attribute__((aligned(16))) uint8_t buf0[kBuf];
   __shared__ __attribute__((aligned(16))) uint8_t buf1[kBuf];
+  __shared__ __attribute__((aligned(16))) uint8_t buf2[ND > 2 ? kBuf : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t buf3[ND > 2 ? kBuf : 16];
   // consecutive tiles (one band of rows r) on one XCD
   const int total = a.tiles_r * a.tiles_c, per = (total + kXcds - 1) / kXcds;
   const int id = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
@@ -262,29 +267,40 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto land = [&] {
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+  // all but the last `out` of this wave's copies have landed, and every wave is here
+  auto land = [&](auto out) {
+    constexpr int n = decltype(out)::value;
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | (n >> 4) << 14);   // vmcnt(n)
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
+  using All = std::integral_constant<int, 0>;
+  using Ahead = std::integral_constant<int, (ND - 2) * (CA + CV + 1)>;   // of later steps
 
-  copy_codes(buf0, t0);
-  copy_dy(buf0, t0, 0, CA);
-  copy_codes(buf1, t0 + 1);
-  land();
+  auto copy_step = [&](uint8_t* buf, int t) {
+    copy_codes(buf, t);
+    copy_dy(buf, t, 0, CA);
+  };
+  copy_step(buf0, t0);
+  if constexpr (ND > 2) {
+    copy_step(buf1, t0 + 1);
+    copy_step(buf2, t0 + 2);
+  }
+  copy_codes(ND > 2 ? buf3 : buf1, t0 + ND - 1);
+  land(std::integral_constant<int, Ahead::value + CV + 1>{});
   read_codes(buf0, 0);
   read_dy(buf0, 0, 0);
   convert(0);
-  auto step = [&](int t, uint8_t* cur, uint8_t* next) {
+  auto step = [&](int t, uint8_t* last, uint8_t* cur, uint8_t* next) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int set = s & 1;
       if (s == 3) {
-        land();
-        copy_codes(cur, t + 2);
+        land(Ahead{});
+        copy_codes(cur, t + ND);
       }
-      if (s == 0) copy_dy(next, t + 1, 0, (CA + 1) / 2);
-      if (s == 1) copy_dy(next, t + 1, (CA + 1) / 2, CA);
+      if (s == 0) copy_dy(last, t + ND - 1, 0, (CA + 1) / 2);
+      if (s == 1) copy_dy(last, t + ND - 1, (CA + 1) / 2, CA);
       const uint8_t* from = s == 3 ? next : cur;
       read_codes(from, (s + 1) & 3);
       read_dy(from, (s + 1) & 3, set ^ 1);
@@ -294,11 +310,23 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
     }
   };
   int t = t0;
-  for (; t + 1 < t1; t += 2) {
-    step(t, buf0, buf1);
-    step(t + 1, buf1, buf0);
+  if constexpr (ND == 2) {
+    for (; t + 1 < t1; t += 2) {
+      step(t, buf1, buf0, buf1);
+      step(t + 1, buf0, buf1, buf0);
+    }
+    if (t < t1) step(t, buf1, buf0, buf1);
+  } else {
+    for (; t + 3 < t1; t += 4) {
+      step(t, buf3, buf0, buf1);
+      step(t + 1, buf0, buf1, buf2);
+      step(t + 2, buf1, buf2, buf3);
+      step(t + 3, buf2, buf3, buf0);
+    }
+    if (t < t1) step(t, buf3, buf0, buf1);
+    if (t + 1 < t1) step(t + 1, buf0, buf1, buf2);
+    if (t + 2 < t1) step(t + 2, buf1, buf2, buf3);
   }
-  if (t < t1) step(t, buf0, buf1);
 
   // ---- results: value 4 q + e of a tile is row col, column 8 q + 4 half + e ----
   // Through LDS, 32 rows at a time in a wave's own part of a buffer (16-byte chunks
@@ -311,7 +339,7 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
   const int cend = SPLIT ? (int)a.ldp : a.C;
   const bool vec = SPLIT || whole4<KIND>(out, ldo);
   auto turn_o = [](int row) { return FC == 2 ? row & 15 : (row >> 1) & 7; };
-  land();   // every wave has read its operands, and no copy is in flight
+  land(All{});   // every wave has read its operands, and no copy is in flight
   uint8_t* const mine = buf0 + wave * 32 * OCH * 16;
 #pragma unroll
   for (int j = 0; j < FR; ++j) {
@@ -377,9 +405,9 @@ template <bool TURNED, bool F16, int OUT, bool SPLIT>
 hipError_t launch(const GradArgs& a, const Form& f, hipStream_t s) {
   const dim3 grid((a.tiles_r * a.tiles_c + kXcds - 1) / kXcds * kXcds, a.splits);
   if (f.fr == 8)
-    int8_grad_kernel<8, 2, TURNED, F16, OUT, SPLIT><<<grid, kThreads, 0, s>>>(a);
+    int8_grad_kernel<8, 2, 2, TURNED, F16, OUT, SPLIT><<<grid, kThreads, 0, s>>>(a);
   else
-    int8_grad_kernel<2, 1, TURNED, F16, OUT, SPLIT><<<grid, kThreads, 0, s>>>(a);
+    int8_grad_kernel<2, 1, 4, TURNED, F16, OUT, SPLIT><<<grid, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 

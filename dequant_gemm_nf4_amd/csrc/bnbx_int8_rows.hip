@@ -30,51 +30,10 @@ __device__ __forceinline__ u32x4_t load_piece(const uint16_t* row, int p, int co
   return v;
 }
 
-typedef __attribute__((ext_vector_type(2))) uint16_t u16x2_t;
-
-__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(uint32_t,
-                            __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
-                                                      __builtin_bit_cast(u16x2_t, b)));
-}
-// |x| as integers order like the values, infinities and NaN above them.
-__device__ __forceinline__ uint32_t max_piece(uint32_t m, u32x4_t v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = max_halves(m, v[i] & 0x7fff7fffu);
-  return m;
-}
-
-template <bool F16>
-__device__ __forceinline__ u32x2_t codes_of(u32x4_t v, const RowQuant& p) {
-  uint32_t q[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float lo, hi;
-    if (F16) {
-      const f16x2_t h = __builtin_bit_cast(f16x2_t, (uint32_t)v[i]);
-      lo = (float)h[0];
-      hi = (float)h[1];
-    } else {
-      lo = bf16lo_to_f32(v[i]);
-      hi = bf16hi_to_f32(v[i]);
-    }
-    q[2 * i] = code_of(lo, p);
-    q[2 * i + 1] = code_of(hi, p);
-  }
-  u32x2_t r = {pack_bytes(q[0], q[1], q[2], q[3]), pack_bytes(q[4], q[5], q[6], q[7])};
-  return r;
-}
-
 // The largest of the team's maxima, in every thread of it.
 template <int T>
 __device__ __forceinline__ uint32_t team_max(uint32_t m, uint32_t* lds) {
-  m = m > (m >> 16 | m << 16) ? m : (m >> 16 | m << 16);   // the larger half on top
-  m >>= 16;
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    const uint32_t other = (uint32_t)__shfl_xor((int)m, o);
-    m = m > other ? m : other;
-  }
+  m = wave_top(m);
   if constexpr (T > 64) {
     constexpr int W = T / 64;
     __syncthreads();   // the last row's maxima are read
