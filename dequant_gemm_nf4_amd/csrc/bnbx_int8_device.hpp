@@ -19,6 +19,12 @@ __device__ __forceinline__ rsrc8_t rsrc8(const void* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)n, 0x00020000);
 }
 
+// The same over fewer than 2^31 bytes.
+__device__ __forceinline__ rsrc8_t rsrc8_near(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes,
+                                           0x00020000);
+}
+
 // 16 bytes a lane from global memory into LDS at `lds` + 16 lane.
 __device__ __forceinline__ void copy16_lds(rsrc8_t r, void* lds, uint32_t voff, uint32_t soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (void __attribute__((address_space(3)))*)lds, 16,
@@ -36,6 +42,22 @@ __device__ __forceinline__ i32x16_t mfma_i8_32x32x32(u32x4_t a, u32x4_t b, i32x1
 __device__ __forceinline__ i32x4_t mfma_i8_16x16x64(u32x4_t a, u32x4_t b, i32x4_t c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a),
                                                __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
+}
+
+// Tile order: workgroup b runs on XCD b % 8; an XCD's tiles are consecutive, and
+// consecutive ones walk blocks of up to four row tiles by all column tiles, so that
+// the workgroups of an XCD share both operands in its L2.
+constexpr int kXcds = 8;
+__device__ __forceinline__ bool tile_of(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
+  constexpr int G = 4;
+  const int total = tiles_m * tiles_n, per = (total + kXcds - 1) / kXcds;
+  id = (id % kXcds) * per + id / kXcds;
+  if (id >= total || (int)(blockIdx.x / kXcds) >= per) return false;
+  const int group = id / (G * tiles_n), in = id - group * G * tiles_n;
+  const int left = tiles_m - group * G, g = left < G ? left : G;
+  tn = in / g;
+  tm = group * G + (in - tn * g);
+  return true;
 }
 
 // Codes of a row.  With a = max |x| the code is 127 x / a, exact quotient,

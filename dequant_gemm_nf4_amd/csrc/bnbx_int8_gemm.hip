@@ -26,7 +26,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int BK = 128;
-constexpr int kXcds = 8;
 
 // Scheduling-group masks (AMDGPU sched_group_barrier).
 constexpr int kSgMfma = 0x008, kSgValu = 0x002, kSgSalu = 0x004, kSgVmem = 0x010,
@@ -68,22 +67,7 @@ __device__ __forceinline__ void store8(uint16_t* y, u32x4_t v, int left, bool ve
   }
 }
 
-// Tile order: workgroup b runs on XCD b % 8; an XCD's tiles are consecutive, and
-// consecutive ones walk blocks of up to four row tiles of X, so that an XCD's L2
-// serves a few rows of both operands.
-__device__ __forceinline__ bool tile_of(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
-  constexpr int G = 4;
-  const int total = tiles_m * tiles_n, per = (total + kXcds - 1) / kXcds;
-  id = (id % kXcds) * per + id / kXcds;
-  if (id >= total || (int)(blockIdx.x / kXcds) >= per) return false;
-  const int group = id / (G * tiles_n), in = id - group * G * tiles_n;
-  const int left = tiles_m - group * G, g = left < G ? left : G;
-  tn = in / g;
-  tm = group * G + (in - tn * g);
-  return true;
-}
-
-// ND: buffers, 2 or 4.
+// ND: buffers, 2 to 4.
 template <int FM, int FN, int ND, bool F16, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
   constexpr int TM = 64 * FM, TN = 64 * FN;
@@ -92,7 +76,7 @@ __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t buf0[kBuf];
   __shared__ __attribute__((aligned(16))) uint8_t buf1[kBuf];
   __shared__ __attribute__((aligned(16))) uint8_t buf2[ND > 2 ? kBuf : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t buf3[ND > 2 ? kBuf : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t buf3[ND > 3 ? kBuf : 16];
   int tm, tn;
   if (!tile_of(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn)) return;
   const int m0 = tm * TM, n0 = tn * TN;
@@ -184,12 +168,11 @@ __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
   constexpr int C = CW + CX;
   constexpr int C3 = C / 2;   // copies of a step that go out in substep 3, as its buffer is left
   using Ahead = std::integral_constant<int, (ND - 2) * C>;   // copies of later steps
-  copies(buf0, t0, 0, C);
-  if constexpr (ND > 2) {
-    copies(buf1, t0 + 1, 0, C);
-    copies(buf2, t0 + 2, 0, C);
+  {
+    uint8_t* const bufs[4] = {buf0, buf1, buf2, buf3};
+#pragma unroll
+    for (int k = 0; k < ND; ++k) copies(bufs[k], t0 + k, 0, k + 1 < ND ? C : C3);
   }
-  copies(ND > 2 ? buf3 : buf1, t0 + ND - 1, 0, C3);
   land(std::integral_constant<int, (ND - 2) * C + C3>{});
   reads(buf0, 0, 0);
   auto step = [&](int t, uint8_t* last, uint8_t* cur, uint8_t* next) {
@@ -213,6 +196,14 @@ __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
       step(t + 1, buf0, buf1, buf0);
     }
     if (t < t1) step(t, buf1, buf0, buf1);
+  } else if constexpr (ND == 3) {
+    for (; t + 2 < t1; t += 3) {
+      step(t, buf2, buf0, buf1);
+      step(t + 1, buf0, buf1, buf2);
+      step(t + 2, buf1, buf2, buf0);
+    }
+    if (t < t1) step(t, buf2, buf0, buf1);
+    if (t + 1 < t1) step(t + 1, buf0, buf1, buf2);
   } else {
     for (; t + 3 < t1; t += 4) {
       step(t, buf3, buf0, buf1);
@@ -307,39 +298,60 @@ __global__ __launch_bounds__(kThreads) void int8_reduce_kernel(GemmArgs a) {
   }
 }
 
-struct Form {
-  int f;        // FM = FN
-  int splits, steps_per;
+// The forms: FM, FN, ND, and the time of a step of K with a workgroup on every CU
+// (us; 2048 x 8192 x 8192 and the sizes below, timed one form after the other).
+struct Shape {
+  int fm, fn;
+  double step;
 };
-// The largest tile that fills the GPU; where even the smallest does not, K is
-// split, at least four steps each.
+constexpr Shape kShapes[] = {{4, 4, 1.77}, {4, 2, 1.13}, {2, 2, 0.60}, {2, 1, 0.38}, {1, 1, 0.23}};
+struct Form {
+  int shape;
+  int splits, steps_per;   // of K
+};
+// The form and the split of K that take the least by this count: rounds of
+// workgroups over the CUs (a last round that is not full is a little faster),
+// their steps, 4 us for a launch's first copies and its results, and for a split 3 us
+// for the second launch and the partial sums written and read at 6.5 TB/s.
+// Counted and measured (us), 301 x 4096 x 11008: 2 x 1 tiles whole 34 / 31, 2 x 2 in
+// two splits 34 / 34, 1 x 1 whole 44 / 44; 1000 x 4096 x 11008: 2 x 2 whole 56 / 59,
+// 4 x 2 in two 66 / 66; 2048 x 4096 x 4096: 4 x 2 whole 40 / 40, 4 x 4 whole 52 / 52.
 Form form_of(int M, int N, int K) {
   const int cus = int8_cus();
-  auto tiles = [&](int f) {
-    return (int64_t)((M + 64 * f - 1) / (64 * f)) * ((N + 64 * f - 1) / (64 * f));
-  };
-  const int f = tiles(4) >= cus * 3 / 4 ? 4 : tiles(2) >= cus / 2 ? 2 : 1;
   const int steps = (K + BK - 1) / BK;
-  int splits = 1;
-  if (f == 1) {
-    const int64_t most = 2 * cus / tiles(1);
-    splits = (int)(most < steps / 4 ? most : steps / 4);
-    splits = splits < 1 ? 1 : splits;
+  Form best{0, 1, steps};
+  double least = 1e30;
+  for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
+    const Shape& f = kShapes[i];
+    const int64_t tiles = (((int64_t)M + 64 * f.fm - 1) / (64 * f.fm)) *
+                          (((int64_t)N + 64 * f.fn - 1) / (64 * f.fn));
+    for (int splits = 1; splits <= 16 && (splits == 1 || steps / splits >= 4); ++splits) {
+      const int per = (steps + splits - 1) / splits, n = (steps + per - 1) / per;
+      if (n > 1 && tiles * n > 2 * (int64_t)cus) break;
+      const double fill = (double)(tiles * n) / cus;
+      const double rounds = fill <= 1.0 ? 0.7 + 0.3 * fill : (double)((tiles * n + cus - 1) / cus);
+      const double us = rounds * per * f.step + 4.0 +
+                        (n > 1 ? 3.0 + 8.0 * n * (double)M * (double)N / 6.5e6 : 0.0);
+      if (us < least) {
+        least = us;
+        best = {i, n, per};
+      }
+    }
   }
-  const int per = (steps + splits - 1) / splits;
-  return {f, (steps + per - 1) / per, per};
+  return best;
 }
 
 template <bool F16, bool SPLIT>
-hipError_t launch(const GemmArgs& a, int f, hipStream_t s) {
+hipError_t launch(const GemmArgs& a, int shape, hipStream_t s) {
   const int total = a.tiles_m * a.tiles_n;
   const dim3 grid((total + kXcds - 1) / kXcds * kXcds, a.splits);
-  if (f == 4)
-    int8_gemm_kernel<4, 4, 2, F16, SPLIT><<<grid, kThreads, 0, s>>>(a);
-  else if (f == 2)
-    int8_gemm_kernel<2, 2, 4, F16, SPLIT><<<grid, kThreads, 0, s>>>(a);
-  else
-    int8_gemm_kernel<1, 1, 4, F16, SPLIT><<<grid, kThreads, 0, s>>>(a);
+  switch (shape) {
+    case 0: int8_gemm_kernel<4, 4, 2, F16, SPLIT><<<grid, kThreads, 0, s>>>(a); break;
+    case 1: int8_gemm_kernel<4, 2, 3, F16, SPLIT><<<grid, kThreads, 0, s>>>(a); break;
+    case 2: int8_gemm_kernel<2, 2, 4, F16, SPLIT><<<grid, kThreads, 0, s>>>(a); break;
+    case 3: int8_gemm_kernel<2, 1, 4, F16, SPLIT><<<grid, kThreads, 0, s>>>(a); break;
+    default: int8_gemm_kernel<1, 1, 4, F16, SPLIT><<<grid, kThreads, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
@@ -367,8 +379,9 @@ hipError_t launch_int8_gemm(const Int8Rows& x, const Int8Rows& w, uint16_t* y, i
   a.K = x.cols;
   a.y = y;
   a.ldy = ldy;
-  const int64_t tm = ((int64_t)a.M + 64 * f.f - 1) / (64 * f.f),
-                tn = ((int64_t)a.N + 64 * f.f - 1) / (64 * f.f);
+  const int wide_m = 64 * kShapes[f.shape].fm, wide_n = 64 * kShapes[f.shape].fn;
+  const int64_t tm = ((int64_t)a.M + wide_m - 1) / wide_m,
+                tn = ((int64_t)a.N + wide_n - 1) / wide_n;
   // a launch counts its threads in 32 bits
   if (tm * tn * f.splits >= ((int64_t)1 << 32) / kThreads - kXcds) return hipErrorNotSupported;
   a.tiles_m = (int)tm;
@@ -377,8 +390,8 @@ hipError_t launch_int8_gemm(const Int8Rows& x, const Int8Rows& w, uint16_t* y, i
   a.steps_per = f.steps_per;
   a.part = (int*)workspace;
   a.ldp = (a.N + 3) / 4 * 4;
-  if (f.splits == 1) return f16 ? launch<true, false>(a, f.f, s) : launch<false, false>(a, f.f, s);
-  const hipError_t e = f16 ? launch<true, true>(a, f.f, s) : launch<false, true>(a, f.f, s);
+  if (f.splits == 1) return f16 ? launch<true, false>(a, f.shape, s) : launch<false, false>(a, f.shape, s);
+  const hipError_t e = f16 ? launch<true, true>(a, f.shape, s) : launch<false, true>(a, f.shape, s);
   if (e != hipSuccess) return e;
   const int64_t quads = (int64_t)a.M * ((a.N + 3) / 4), groups = (quads + kThreads - 1) / kThreads;
   const int grid = (int)(groups < 65536 ? groups : 65536);

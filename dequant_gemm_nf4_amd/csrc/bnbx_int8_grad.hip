@@ -27,14 +27,8 @@
 namespace bnbx {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;   // of the reduction
 constexpr int BT = 64;
-constexpr int kXcds = 8;
-
-// Scheduling-group masks (AMDGPU sched_group_barrier).
-constexpr int kSgMfma = 0x008, kSgValu = 0x002, kSgSalu = 0x004, kSgVmem = 0x010,
-              kSgDsRead = 0x100;
-
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 typedef __attribute__((ext_vector_type(2))) int i32x2_t;
 
@@ -91,30 +85,32 @@ __device__ __forceinline__ bool whole4(const void* out, int64_t ldo) {
   return (uintptr_t)out % (OUT == kOutF32 ? 16 : 8) == 0 && ldo % 4 == 0;
 }
 
-// ND: buffers, 2 or 4.  OUT: kOutBf16 / kOutF16 / kOutF32; SPLIT: fp32 partial sums
-// instead.
-template <int FR, int FC, int ND, bool TURNED, bool F16, int OUT, bool SPLIT>
-__global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
-  constexpr int TR = 32 * FR, TC = 128 * FC;
-  constexpr int kA = TR * BT * 2, kV = BT * TC, kBuf = kA + kV + 4 * BT * 4;
-  constexpr int CA = FR, CV = 2 * FC;   // copies a wave and step
+// ND: buffers, 2 to 4.  KW: groups of four waves; with two, each takes half of
+// every step's substeps and half of the rows at the end, so that two waves a SIMD
+// cover each other's waits.  OUT: kOutBf16 / kOutF16 / kOutF32; SPLIT: fp32 partial
+// sums instead.
+template <int FR, int FC, int ND, int KW, bool TURNED, bool F16, int OUT, bool SPLIT>
+__global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
+  constexpr int TR = 32 * FR, TC = 128 * FC, WV = 4 * KW;
+  constexpr int kA = TR * BT * 2, kV = BT * TC, kBuf = kA + kV + WV * BT * 4;
+  constexpr int CA = FR / KW, CV = 2 * FC / KW;   // copies a wave and step
+  static_assert(CA * KW == FR && CV * KW == 2 * FC, "whole copies a wave");
   __shared__ __attribute__((aligned(16))) uint8_t buf0[kBuf];
   __shared__ __attribute__((aligned(16))) uint8_t buf1[kBuf];
   __shared__ __attribute__((aligned(16))) uint8_t buf2[ND > 2 ? kBuf : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t buf3[ND > 2 ? kBuf : 16];
-  // consecutive tiles (one band of rows r) on one XCD
-  const int total = a.tiles_r * a.tiles_c, per = (total + kXcds - 1) / kXcds;
-  const int id = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
-  if ((int)(blockIdx.x / kXcds) >= per || id >= total) return;
-  const int r0 = id / a.tiles_c * TR, c0 = id % a.tiles_c * TC;
+  __shared__ __attribute__((aligned(16))) uint8_t buf3[ND > 3 ? kBuf : 16];
+  int tr, tc;
+  if (!tile_of(blockIdx.x, a.tiles_r, a.tiles_c, tr, tc)) return;
+  const int r0 = tr * TR, c0 = tc * TC;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wc = wave & 3, kg = wave >> 2;   // the wave's columns, its substeps
   const int col = lane & 31, half = lane >> 5;
   const int steps = (a.T + BT - 1) / BT;
   const int t0 = SPLIT ? (int)blockIdx.y * a.steps_per : 0;
   const int t1 = SPLIT ? (t0 + a.steps_per < steps ? t0 + a.steps_per : steps) : steps;
 
   // ---- copies -------------------------------------------------------------
-  // Codes: rows t of TC bytes, chunk permuted by kTurnV.
+  // Codes: rows t of TC bytes, chunk permuted by turn_v.
   constexpr int VCH = TC / 16, VR = 64 / VCH;   // chunks a row, rows an instruction
   auto turn_v = [](int t) { return FC == 2 ? 2 * (t & 7) : 2 * ((t >> 1) & 3); };
   const int cp = (a.C + 15) / 16 * 16;
@@ -140,34 +136,41 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
     const bool in = TURNED ? r0 + 8 * ch < a.R : r0 + row < a.R;
     aoff[i] = in ? (uint32_t)row * (uint32_t)a.ldy * 2u + 16u * ch : kFar8;
   }
-  // !TURNED: the first t of this lane's chunk; instructions 4 rows pairs apart
-  // permute it by 4
+  // !TURNED: the first t of this lane's chunk; odd instructions permute by 4 more
   const int ach0 = 8 * ((lane & 7) ^ ((lane >> 4) & 3));
   const rsrc8_t ra = rsrc8(a.dy + (int64_t)r0 * a.ldy, (int64_t)kFar8);
-  auto rows_left = [&](int t) {
-    const int left = a.T - t * BT;
-    return left < 0 ? 0 : left < BT ? left : BT;
+  const uint32_t ldv = (uint32_t)a.ldv, ldy2 = (uint32_t)a.ldy * 2u;
+  // A step's source: rows t past the end are past the resources.
+  struct Source {
+    rsrc8_t v, s, y;
+    uint32_t soff;
+    bool ok0, ok1;
   };
-  auto copy_codes = [&](uint8_t* buf, int t) {
-    const int rows = rows_left(t);
-    const rsrc8_t rv = rsrc8(a.codes + c0 + (int64_t)t * BT * a.ldv, rows * a.ldv);
-#pragma unroll
-    for (int i = 0; i < CV; ++i) copy16_lds(rv, buf + kA + (wave * CV + i) * 1024, voff[i], 0);
-    const rsrc8_t rs = rsrc8(a.scale + (int64_t)t * BT, rows * 4);
-    copy4_lds(rs, buf + kA + kV + wave * BT * 4, 4u * lane, 0);
+  auto source = [&](int t) {
+    int rows = a.T - t * BT;
+    Source f;
+    f.soff = (uint32_t)t * (BT * 2);
+    f.ok0 = ach0 < rows;
+    f.ok1 = (ach0 ^ 32) < rows;
+    rows = rows < 0 ? 0 : rows < BT ? rows : BT;
+    f.v = rsrc8_near(a.codes + c0 + (int64_t)t * BT * a.ldv, rows * ldv);
+    f.s = rsrc8_near(a.scale + (int64_t)t * BT, rows * 4u);
+    f.y = TURNED ? rsrc8_near(a.dy + r0 + (int64_t)t * BT * a.ldy, rows * ldy2) : ra;
+    return f;
   };
-  auto copy_dy = [&](uint8_t* buf, int t, int i0, int i1) {
-    if constexpr (TURNED) {
-      const rsrc8_t rt = rsrc8(a.dy + r0 + (int64_t)t * BT * a.ldy, rows_left(t) * a.ldy * 2);
-#pragma unroll
-      for (int i = i0; i < i1; ++i) copy16_lds(rt, buf + (wave * CA + i) * 1024, aoff[i], 0);
+  constexpr int C = CV + 1 + CA;
+  auto copy = [&](uint8_t* buf, const Source& f, int i) {
+    if (i < CV) {
+      copy16_lds(f.v, buf + kA + (wave * CV + i) * 1024, voff[i], 0);
+    } else if (i == CV) {
+      copy4_lds(f.s, buf + kA + kV + wave * BT * 4, 4u * lane, 0);
     } else {
-      const int left = a.T - t * BT;
-      const bool ok0 = ach0 < left, ok1 = (ach0 ^ 32) < left;
-#pragma unroll
-      for (int i = i0; i < i1; ++i)
-        copy16_lds(ra, buf + (wave * CA + i) * 1024,
-                   (((wave * CA + i) & 1) ? ok1 : ok0) ? aoff[i] : kFar8, (uint32_t)t * (BT * 2));
+      i -= CV + 1;
+      uint8_t* const to = buf + (wave * CA + i) * 1024;
+      if constexpr (TURNED)
+        copy16_lds(f.y, to, aoff[i], 0);
+      else
+        copy16_lds(f.y, to, (((wave * CA + i) & 1) ? f.ok1 : f.ok0) ? aoff[i] : kFar8, f.soff);
     }
   };
 
@@ -184,7 +187,7 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
     const int t = 8 * (g >> 1) + (l16 >> 1);   // + 16 s, which leaves turn_v alone
 #pragma unroll
     for (int f = 0; f < FC; ++f) {
-      const int ch = ((wave * FC + f) * 2 + (g & 1)) ^ turn_v(t);
+      const int ch = ((wc * FC + f) * 2 + (g & 1)) ^ turn_v(t);
       vrd[f] = kA + t * TC + 16 * ch + 8 * (l16 & 1);
     }
   }
@@ -193,7 +196,8 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
   // 16 lanes (four lanes a row), twice, each row in other banks.  turn_a moves
   // whole groups of four chunks (two with FR = 2), so tiles four apart differ by a
   // constant.
-  constexpr int NRD = TURNED ? (FR < 4 ? FR : 4) : 4;
+  constexpr int SUB = 4 / KW;   // substeps of a wave
+  constexpr int NRD = TURNED ? (FR < 4 ? FR : 4) : SUB;
   uint32_t ard[NRD];
   if constexpr (TURNED) {
     const int t = 8 * (g >> 1) + (l16 >> 2);   // + 16 s + 4 j, the same turn_a for FR >= 4
@@ -203,19 +207,21 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
                8 * (l16 & 1);
   } else {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) ard[s] = col * BT * 2 + 16 * ((2 * s + half) ^ turn_a(col));
+    for (int s = 0; s < SUB; ++s)
+      ard[s] = col * BT * 2 + 16 * ((2 * (s + SUB * kg) + half) ^ turn_a(col));
   }
-  auto read_codes = [&](const uint8_t* buf, int s) {
-#pragma unroll
-    for (int f = 0; f < FC; ++f) oc[f] = read_tr8(buf + vrd[f] + 16 * s * TC);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) os[j] = *(const f32x4_t*)(buf + srd + 64 * s + 16 * j);
-  };
-  auto read_dy = [&](const uint8_t* buf, int s, int set) {
-#pragma unroll
-    for (int f = 0; f < FR; ++f) {
+  const uint32_t sub0 = 16 * SUB * kg;   // the wave's first t of a step
+  // Read i of substep s: the codes, the scales, then the gradients.
+  constexpr int NR = FC + 2 + FR;
+  auto read = [&](const uint8_t* buf, int s, int set, int i) {
+    if (i < FC) {
+      oc[i] = read_tr8(buf + vrd[i] + (16 * s + sub0) * TC);
+    } else if (i < FC + 2) {
+      os[i - FC] = *(const f32x4_t*)(buf + srd + 4 * (16 * s + sub0) + 16 * (i - FC));
+    } else {
+      const int f = i - FC - 2;
       if constexpr (TURNED) {
-        const uint8_t* p = buf + ard[f % NRD] + 16 * s * TR * 2 + f / NRD * 256;
+        const uint8_t* p = buf + ard[f % NRD] + (16 * s + sub0) * TR * 2 + f / NRD * 256;
         const u32x2_t lo = read_tr16(p), hi = read_tr16(p + 4 * TR * 2);
         oa[set][f] = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
       } else {
@@ -223,14 +229,13 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
       }
     }
   };
-  auto convert = [&](int set) {
-#pragma unroll
-    for (int i = 0; i < FC; ++i)
-#pragma unroll
-      for (int p = 0; p < 4; ++p)
-        ov[set][i][p] =
-            pack16x2<F16>(code_value(oc[i][p / 2], 2 * (p & 1), os[p / 2][2 * (p & 1)]),
-                          code_value(oc[i][p / 2], 2 * (p & 1) + 1, os[p / 2][2 * (p & 1) + 1]));
+  // Pair i of the values.
+  constexpr int NP = 4 * FC;
+  auto convert = [&](int set, int i) {
+    const int f = i / 4, p = i % 4;
+    ov[set][f][p] =
+        pack16x2<F16>(code_value(oc[f][p / 2], 2 * (p & 1), os[p / 2][2 * (p & 1)]),
+                      code_value(oc[f][p / 2], 2 * (p & 1) + 1, os[p / 2][2 * (p & 1) + 1]));
   };
   f32x16_t acc[FC][FR];
 #pragma unroll
@@ -239,34 +244,6 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
     for (int j = 0; j < FR; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-  auto products = [&](int set) {
-#pragma unroll
-    for (int j = 0; j < FR; ++j)
-#pragma unroll
-      for (int i = 0; i < FC; ++i)
-        acc[i][j] = mfma_32x32x16<F16>(ov[set][i], oa[set][j], acc[i][j]);
-  };
-  // One substep's products with the reads and the conversion of the next one laid
-  // between them, and `nc` copies.
-  auto interleave = [&](int nc) {
-    constexpr int N = FC * FR;
-    __builtin_amdgcn_sched_group_barrier(kSgDsRead, FC + 2, 0);
-#pragma unroll
-    for (int q = 0; q < N; ++q) {
-      __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
-      if (q < N / 2) {
-        __builtin_amdgcn_sched_group_barrier(kSgDsRead, (TURNED ? 4 : 2) / FC, 0);
-        __builtin_amdgcn_sched_group_barrier(kSgValu, 2, 0);
-      } else {
-        __builtin_amdgcn_sched_group_barrier(kSgValu, 44 / FR, 0);
-      }
-      if (q * nc / N != (q + 1) * nc / N) {
-        __builtin_amdgcn_sched_group_barrier(kSgSalu, 2, 0);
-        __builtin_amdgcn_sched_group_barrier(kSgVmem, 1, 0);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  };
   // all but the last `out` of this wave's copies have landed, and every wave is here
   auto land = [&](auto out) {
     constexpr int n = decltype(out)::value;
@@ -274,39 +251,59 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
   using All = std::integral_constant<int, 0>;
-  using Ahead = std::integral_constant<int, (ND - 2) * (CA + CV + 1)>;   // of later steps
 
-  auto copy_step = [&](uint8_t* buf, int t) {
-    copy_codes(buf, t);
-    copy_dy(buf, t, 0, CA);
-  };
-  copy_step(buf0, t0);
-  if constexpr (ND > 2) {
-    copy_step(buf1, t0 + 1);
-    copy_step(buf2, t0 + 2);
-  }
-  copy_codes(ND > 2 ? buf3 : buf1, t0 + ND - 1);
-  land(std::integral_constant<int, Ahead::value + CV + 1>{});
-  read_codes(buf0, 0);
-  read_dy(buf0, 0, 0);
-  convert(0);
-  auto step = [&](int t, uint8_t* last, uint8_t* cur, uint8_t* next) {
-    __builtin_amdgcn_sched_barrier(0);
+  // The copies of a step go out as its buffer is left: the first CL of them in the
+  // last substep, the rest in the substeps after it.
+  constexpr int CL = SUB == 2 ? (C + 1) / 2 : (C + 2) / 3;
+  constexpr int C0 = SUB == 2 ? C : CL + (C - CL + 1) / 2;   // up to substep 0; then all
+  using Ahead = std::integral_constant<int, (ND - 2) * C>;   // of later steps
+  {
+    uint8_t* const bufs[4] = {buf0, buf1, buf2, buf3};
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int k = 0; k < ND; ++k) {
+      const Source f = source(t0 + k);
+#pragma unroll
+      for (int i = 0; i < (k + 1 < ND ? C : CL); ++i) copy(bufs[k], f, i);
+    }
+  }
+  land(std::integral_constant<int, Ahead::value + CL>{});
+#pragma unroll
+  for (int i = 0; i < NR; ++i) read(buf0, 0, 0, i);
+#pragma unroll
+  for (int i = 0; i < NP; ++i) convert(0, i);
+
+  auto step = [&](int t, uint8_t* last, uint8_t* cur, uint8_t* next) {
+    Source f = source(t + ND - 1);
+#pragma unroll
+    for (int s = 0; s < SUB; ++s) {
       const int set = s & 1;
-      if (s == 3) {
+      const bool end = s == SUB - 1;
+      __builtin_amdgcn_sched_barrier(0);
+      if (end) {
         land(Ahead{});
-        copy_codes(cur, t + ND);
+        f = source(t + ND);
       }
-      if (s == 0) copy_dy(last, t + ND - 1, 0, (CA + 1) / 2);
-      if (s == 1) copy_dy(last, t + ND - 1, (CA + 1) / 2, CA);
-      const uint8_t* from = s == 3 ? next : cur;
-      read_codes(from, (s + 1) & 3);
-      read_dy(from, (s + 1) & 3, set ^ 1);
-      products(set);
-      convert(set ^ 1);
-      interleave(s == 3 ? CV + 1 : s == 0 ? (CA + 1) / 2 : s == 1 ? CA / 2 : 0);
+      uint8_t* const to = end ? cur : last;
+      const int i0 = end ? 0 : s == 0 ? CL : s == 1 ? C0 : C;
+      const int i1 = end ? CL : s == 0 ? C0 : C;
+      // One product a slot, and between the products what the next substep needs:
+      // its reads in the first half, the conversion in the second, and the copies.
+      constexpr int N = FC * FR, H = N / 2;
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        const int j = q / FC, i = q % FC;
+        acc[i][j] = mfma_32x32x16<F16>(ov[set][i], oa[set][j], acc[i][j]);
+#pragma unroll
+        for (int k = 0; k < NR; ++k)
+          if (k * H / NR == q) read(end ? next : cur, end ? 0 : s + 1, set ^ 1, k);
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+          if (H + k * (N - H) / NP == q) convert(set ^ 1, k);
+#pragma unroll
+        for (int k = i0; k < i1; ++k)
+          if ((k - i0) * N / (i1 - i0) == q) copy(to, f, k);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   };
   int t = t0;
@@ -316,6 +313,14 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
       step(t + 1, buf0, buf1, buf0);
     }
     if (t < t1) step(t, buf1, buf0, buf1);
+  } else if constexpr (ND == 3) {
+    for (; t + 2 < t1; t += 3) {
+      step(t, buf2, buf0, buf1);
+      step(t + 1, buf0, buf1, buf2);
+      step(t + 2, buf1, buf2, buf0);
+    }
+    if (t < t1) step(t, buf2, buf0, buf1);
+    if (t + 1 < t1) step(t + 1, buf0, buf1, buf2);
   } else {
     for (; t + 3 < t1; t += 4) {
       step(t, buf3, buf0, buf1);
@@ -327,6 +332,42 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
     if (t + 1 < t1) step(t + 1, buf0, buf1, buf2);
     if (t + 2 < t1) step(t + 2, buf1, buf2, buf3);
   }
+  land(All{});   // every wave has read its operands, and no copy is in flight
+
+  // With two groups: each hands the other the sums of half the rows.
+  constexpr int FE = FR / KW;   // tiles of rows a wave finishes
+  if constexpr (KW == 2) {
+    constexpr int kHand = FC * FE * 4096;   // bytes a wave hands over
+    static_assert(ND > 3 && 2 * kHand <= kBuf, "two waves' sums fit a buffer");
+    uint8_t* const mine = (wc == 0 ? buf0 : wc == 1 ? buf1 : wc == 2 ? buf2 : buf3);
+#pragma unroll
+    for (int j = 0; j < FE; ++j)
+#pragma unroll
+      for (int i = 0; i < FC; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f32x4_t v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = kg == 0 ? acc[i][FE + j][4 * q + e] : acc[i][j][4 * q + e];
+          *(f32x4_t*)(mine + kg * kHand + 16 * (((j * FC + i) * 4 + q) * 64 + lane)) = v;
+        }
+    land(All{});
+#pragma unroll
+    for (int j = 0; j < FE; ++j)
+#pragma unroll
+      for (int i = 0; i < FC; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4_t v = *(const f32x4_t*)(mine + (kg ^ 1) * kHand +
+                                              16 * (((j * FC + i) * 4 + q) * 64 + lane));
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[i][j][4 * q + e] =
+                kg == 0 ? acc[i][j][4 * q + e] + v[e] : v[e] + acc[i][FE + j][4 * q + e];
+        }
+    land(All{});
+  }
 
   // ---- results: value 4 q + e of a tile is row col, column 8 q + 4 half + e ----
   // Through LDS, 32 rows at a time in a wave's own part of a buffer (16-byte chunks
@@ -334,15 +375,17 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
   void* const out = SPLIT ? (void*)(a.part + (int64_t)blockIdx.y * a.R * a.ldp) : a.out;
   constexpr int KIND = SPLIT ? (int)kOutF32 : OUT;
   constexpr int OCH = 8 * FC, OR = 64 / OCH;   // chunks a row, rows an instruction
-  static_assert(4 * 32 * OCH * 16 <= kBuf, "results fit a buffer");
+  static_assert(2 * 32 * OCH * 16 <= kBuf, "results of two waves fit a buffer");
   const int64_t ldo = SPLIT ? a.ldp : a.ldo;
   const int cend = SPLIT ? (int)a.ldp : a.C;
   const bool vec = SPLIT || whole4<KIND>(out, ldo);
   auto turn_o = [](int row) { return FC == 2 ? row & 15 : (row >> 1) & 7; };
-  land(All{});   // every wave has read its operands, and no copy is in flight
-  uint8_t* const mine = buf0 + wave * 32 * OCH * 16;
+  uint8_t* const mine =
+      (KW == 2 ? (wc == 0 ? buf0 : wc == 1 ? buf1 : wc == 2 ? buf2 : buf3) + kg * 32 * OCH * 16
+               : (wave < 2 ? buf0 : buf1) + (wave & 1) * 32 * OCH * 16);
+  const int re = r0 + 32 * FE * kg;
 #pragma unroll
-  for (int j = 0; j < FR; ++j) {
+  for (int j = 0; j < FE; ++j) {
 #pragma unroll
     for (int i = 0; i < FC; ++i)
 #pragma unroll
@@ -355,7 +398,7 @@ __global__ __launch_bounds__(kThreads) void int8_grad_kernel(GradArgs a) {
     for (int k = 0; k < 32 / OR; ++k) {
       const int row = k * OR + lane / OCH, ch = lane % OCH;
       const f32x4_t v = *(const f32x4_t*)(mine + 16 * (row * OCH + (ch ^ turn_o(row))));
-      const int r = r0 + 32 * j + row, c = c0 + 32 * FC * wave + 4 * ch;
+      const int r = re + 32 * j + row, c = c0 + 32 * FC * wc + 4 * ch;
       if (r < a.R && c < cend) store4<KIND>(out, (int64_t)r * ldo + c, v, cend - c, vec);
     }
   }
@@ -378,43 +421,63 @@ __global__ __launch_bounds__(kThreads) void int8_grad_reduce_kernel(GradArgs a) 
   }
 }
 
-struct Form {
+// The forms: FR, FC, and the time of a step of t with a workgroup on every CU (us;
+// 4096 x 11008 x 4096 and the sizes below, timed one form after the other).
+struct Shape {
   int fr, fc;
-  int splits, steps_per;
+  double step;
 };
+constexpr Shape kShapes[] = {{8, 2, 1.72}, {4, 2, 1.03}, {4, 1, 0.61}, {2, 1, 0.42}};
+struct Form {
+  int shape;
+  int splits, steps_per;   // of t
+};
+// As the forward product's: rounds of workgroups, steps, 4 us a launch, and for a
+// split of t 3 us and the partial sums at 6.5 TB/s.  Counted and measured (us), R x
+// T x C = 200 x 4096 x 4096: 4 x 1 in four 21 / 22, 2 x 1 in two 22 / 23, 4 x 2 in eight
+// 23 / 26; 1000 x 4096 x 4096: 4 x 1 whole 43 / 45, 4 x 2 in two 49 / 53; 1001 x 777 x
+// 4100: 4 x 2 whole 17 / 21, 2 x 1 whole 20 / 24.
 Form form_of(int R, int C, int T) {
   const int cus = int8_cus();
-  auto tiles = [&](int fr, int fc) {
-    return (int64_t)((R + 32 * fr - 1) / (32 * fr)) * ((C + 128 * fc - 1) / (128 * fc));
-  };
-  Form f{2, 1, 1, 1};
-  if (tiles(8, 2) >= cus * 3 / 4) f = Form{8, 2, 1, 1};
   const int steps = (T + BT - 1) / BT;
-  if (f.fr == 2) {
-    const int64_t most = 2 * cus / tiles(2, 1);
-    f.splits = (int)(most < steps / 4 ? most : steps / 4);
-    f.splits = f.splits < 1 ? 1 : f.splits;
+  Form best{0, 1, steps};
+  double least = 1e30;
+  for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
+    const Shape& f = kShapes[i];
+    const int64_t tiles = (((int64_t)R + 32 * f.fr - 1) / (32 * f.fr)) *
+                          (((int64_t)C + 128 * f.fc - 1) / (128 * f.fc));
+    for (int splits = 1; splits <= 32 && (splits == 1 || steps / splits >= 4); ++splits) {
+      const int per = (steps + splits - 1) / splits, n = per > 0 ? (steps + per - 1) / per : 1;
+      if (n > 1 && tiles * n > 2 * (int64_t)cus) break;
+      const double fill = (double)(tiles * n) / cus;
+      const double rounds = fill <= 1.0 ? 0.7 + 0.3 * fill : (double)((tiles * n + cus - 1) / cus);
+      const double us = rounds * per * f.step + 4.0 +
+                        (n > 1 ? 3.0 + 8.0 * n * (double)R * (double)C / 6.5e6 : 0.0);
+      if (us < least) {
+        least = us;
+        best = {i, n, per};
+      }
+    }
   }
-  f.steps_per = (steps + f.splits - 1) / f.splits;
-  if (f.steps_per < 1) f.steps_per = 1;
-  f.splits = steps > 0 ? (steps + f.steps_per - 1) / f.steps_per : 1;
-  return f;
+  return best;
 }
 
 template <bool TURNED, bool F16, int OUT, bool SPLIT>
-hipError_t launch(const GradArgs& a, const Form& f, hipStream_t s) {
+hipError_t launch(const GradArgs& a, int shape, hipStream_t s) {
   const dim3 grid((a.tiles_r * a.tiles_c + kXcds - 1) / kXcds * kXcds, a.splits);
-  if (f.fr == 8)
-    int8_grad_kernel<8, 2, 2, TURNED, F16, OUT, SPLIT><<<grid, kThreads, 0, s>>>(a);
-  else
-    int8_grad_kernel<2, 1, 4, TURNED, F16, OUT, SPLIT><<<grid, kThreads, 0, s>>>(a);
+  switch (shape) {
+    case 0: int8_grad_kernel<8, 2, 3, 1, TURNED, F16, OUT, SPLIT><<<grid, 256, 0, s>>>(a); break;
+    case 1: int8_grad_kernel<4, 2, 4, 2, TURNED, F16, OUT, SPLIT><<<grid, 512, 0, s>>>(a); break;
+    case 2: int8_grad_kernel<4, 1, 4, 2, TURNED, F16, OUT, SPLIT><<<grid, 512, 0, s>>>(a); break;
+    default: int8_grad_kernel<2, 1, 4, 2, TURNED, F16, OUT, SPLIT><<<grid, 512, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
 template <bool TURNED, bool F16, int OUT>
 hipError_t launch(const GradArgs& a, const Form& f, hipStream_t s) {
-  if (f.splits == 1) return launch<TURNED, F16, OUT, false>(a, f, s);
-  const hipError_t e = launch<TURNED, F16, kOutF32, true>(a, f, s);
+  if (f.splits == 1) return launch<TURNED, F16, OUT, false>(a, f.shape, s);
+  const hipError_t e = launch<TURNED, F16, kOutF32, true>(a, f.shape, s);
   if (e != hipSuccess) return e;
   const int64_t groups = ((int64_t)a.R * ((a.C + 3) / 4) + kThreads - 1) / kThreads;
   int8_grad_reduce_kernel<OUT>
@@ -450,8 +513,9 @@ hipError_t launch_int8_grad(const GradGemm& g, bool turned, bool f16, void* work
   a.T = g.v.rows;
   a.out = g.out;
   a.ldo = g.ldo;
-  const int64_t tr = ((int64_t)a.R + 32 * f.fr - 1) / (32 * f.fr),
-                tc = ((int64_t)a.C + 128 * f.fc - 1) / (128 * f.fc);
+  const int wide_r = 32 * kShapes[f.shape].fr, wide_c = 128 * kShapes[f.shape].fc;
+  const int64_t tr = ((int64_t)a.R + wide_r - 1) / wide_r,
+                tc = ((int64_t)a.C + wide_c - 1) / wide_c;
   // a launch counts its threads in 32 bits
   if (tr * tc * f.splits >= ((int64_t)1 << 32) / kThreads - kXcds) return hipErrorNotSupported;
   a.tiles_r = (int)tr;
