@@ -5,7 +5,10 @@ weight on load; the same layer with a LoRA adapter as
 rows belong to groups: ``torch.ops.bnbx.group_rows`` (the plan),
 ``torch.ops.bnbx.experts4bit`` with ``Experts4bit`` (one 4-bit weight an expert)
 and ``torch.ops.bnbx.linear4bit_adapters`` with ``Linear4bitAdapters`` (one 4-bit
-weight, one adapter a request).
+weight, one adapter a request).  Beside them the 8-bit layer:
+``torch.ops.bnbx.linear8bit`` with ``Linear8bit`` (a frozen weight) and
+``torch.ops.bnbx.linear8bit_train`` with ``Linear8bitTrain`` (a 16-bit weight that is
+trained, its input kept in 8 bits for the backward pass).
 
 The pomoai.com overview (module list) has ``Linear4bit`` replacing
 ``torch.nn.Linear`` and the mlqm.cn article (section 4) loads a model in
@@ -499,3 +502,245 @@ class Linear4bitAdapters(Linear4bit):
 
     def extra_repr(self) -> str:
         return super().extra_repr() + f", adapters={self.adapters}, rank={self.rank}"
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit layer
+# ---------------------------------------------------------------------------
+def _rows8(name: str, codes: torch.Tensor, scale: torch.Tensor, cols: int, dtype) -> T.Int8Rows:
+    if dtype not in _DTYPES:
+        raise TypeError(f"{name}: bfloat16 or float16, not {dtype}")
+    return T.Int8Rows((codes.shape[0], cols), codes, scale, dtype)
+
+
+def _matrix(t: torch.Tensor) -> torch.Tensor:
+    """Any batch of rows as a matrix of its own rows."""
+    t = t.reshape(-1, t.shape[-1])
+    if t.stride(-1) != 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        # (contiguous() leaves the stride of a single column as it is)
+        t = torch.empty(t.shape, dtype=t.dtype, device=t.device).copy_(t)
+    return t
+
+
+def _pitch16(cols: int) -> int:
+    return -(-cols // 16) * 16
+
+
+@torch.library.custom_op("bnbx::quantize_rows8", mutates_args=())
+def quantize_rows8(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """int8 codes [rows, columns rounded up to 16] and float32 scales [rows] of
+    16-bit rows (leading dimensions flattened): scale = max |x| / 127."""
+    q = T.quantize_rows(_matrix(x))
+    return q.codes, q.scale
+
+
+@quantize_rows8.register_fake
+def _(x):
+    rows = x.numel() // x.shape[-1]
+    return (x.new_empty(rows, _pitch16(x.shape[-1]), dtype=torch.int8),
+            x.new_empty(rows, dtype=torch.float32))
+
+
+@torch.library.custom_op("bnbx::linear8bit", mutates_args=())
+def linear8bit(x: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor) -> torch.Tensor:
+    """Y[..., N] = X[..., K] . W^T over 8-bit integers: X's rows are quantized on
+    the way, W is given as codes [N, K rounded up to 16] and scales [N]; Y in
+    X's dtype (bf16 or fp16).  Its backward is linear8bit_dx; the weight is
+    frozen and gets none."""
+    w = _rows8("linear8bit", codes, scale, x.shape[-1], x.dtype)
+    y = T.linear_int8(_matrix(x), w)
+    return y.reshape(*x.shape[:-1], codes.shape[0])
+
+
+@linear8bit.register_fake
+def _(x, codes, scale):
+    return x.new_empty(*x.shape[:-1], codes.shape[0])
+
+
+@torch.library.custom_op("bnbx::linear8bit_dx", mutates_args=())
+def linear8bit_dx(dy: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor,
+                  in_features: int) -> torch.Tensor:
+    """dX[..., K] = dY[..., N] . W_hat in dY's dtype, W_hat the values of the codes."""
+    w = _rows8("linear8bit_dx", codes, scale, in_features, dy.dtype)
+    dx = T.gemm_int8_dx(_matrix(dy), w)
+    return dx.reshape(*dy.shape[:-1], in_features)
+
+
+@linear8bit_dx.register_fake
+def _(dy, codes, scale, in_features):
+    return dy.new_empty(*dy.shape[:-1], in_features)
+
+
+@torch.library.custom_op("bnbx::linear8bit_dw", mutates_args=())
+def linear8bit_dw(dy: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor,
+                  in_features: int, dtype: torch.dtype) -> torch.Tensor:
+    """dW[N, K] = dY^T . X_hat from activations saved as codes [rows, K rounded up
+    to 16] and scales [rows] (quantize_rows8), in dY's dtype or float32."""
+    x = _rows8("linear8bit_dw", codes, scale, in_features, dy.dtype)
+    return T.gemm_int8_dw(_matrix(dy), x, dtype=dtype)
+
+
+@linear8bit_dw.register_fake
+def _(dy, codes, scale, in_features, dtype):
+    return dy.new_empty(dy.shape[-1], in_features, dtype=dtype)
+
+
+def _linear8bit_setup(ctx, inputs, output):
+    x, codes, scale = inputs
+    ctx.save_for_backward(codes, scale)
+    ctx.in_features = x.shape[-1]
+
+
+def _linear8bit_backward(ctx, grad):
+    dx = None
+    if ctx.needs_input_grad[0]:
+        dx = torch.ops.bnbx.linear8bit_dx(grad, *ctx.saved_tensors, ctx.in_features)
+    return dx, None, None
+
+
+linear8bit.register_autograd(_linear8bit_backward, setup_context=_linear8bit_setup)
+
+
+@torch.library.custom_op("bnbx::linear8bit_train", mutates_args=())
+def linear8bit_train(x: torch.Tensor, weight: torch.Tensor) -> tuple[
+        torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(Y, X's codes, X's scales, W's codes, W's scales) of Y[..., N] = X[..., K] .
+    W^T over 8-bit integers, both quantized within the call.  The backward pass
+    of Y needs the codes only: dX = dY . W_hat, dW = dY^T . X_hat, so X itself is
+    not kept (one byte a value instead of two)."""
+    if weight.dim() != 2 or weight.shape[1] != x.shape[-1] or weight.dtype != x.dtype:
+        raise ValueError(f"linear8bit_train: weight must be [N, {x.shape[-1]}] {x.dtype}, not "
+                         f"{tuple(weight.shape)} {weight.dtype}")
+    w = T.quantize_rows(_matrix(weight))
+    x2 = _matrix(x)
+    saved = T.empty_int8_rows(tuple(x2.shape), x.dtype, x.device)
+    y = T.linear_int8(x2, w, saved=saved)
+    return (y.reshape(*x.shape[:-1], weight.shape[0]), saved.codes, saved.scale, w.codes, w.scale)
+
+
+@linear8bit_train.register_fake
+def _(x, weight):
+    rows, wide = x.numel() // x.shape[-1], _pitch16(x.shape[-1])
+    n = weight.shape[0]
+    return (x.new_empty(*x.shape[:-1], n), x.new_empty(rows, wide, dtype=torch.int8),
+            x.new_empty(rows, dtype=torch.float32), x.new_empty(n, wide, dtype=torch.int8),
+            x.new_empty(n, dtype=torch.float32))
+
+
+def _linear8bit_train_setup(ctx, inputs, output):
+    x, weight = inputs
+    _, xq, xs, wq, ws = output
+    ctx.mark_non_differentiable(xq, xs, wq, ws)
+    ctx.save_for_backward(xq, xs, wq, ws)
+    ctx.in_features = x.shape[-1]
+
+
+def _linear8bit_train_backward(ctx, grad, *_):
+    xq, xs, wq, ws = ctx.saved_tensors
+    dx = dw = None
+    if ctx.needs_input_grad[0]:
+        dx = torch.ops.bnbx.linear8bit_dx(grad, wq, ws, ctx.in_features)
+    if ctx.needs_input_grad[1]:
+        dw = torch.ops.bnbx.linear8bit_dw(grad, xq, xs, ctx.in_features, grad.dtype)
+    return dx, dw
+
+
+linear8bit_train.register_autograd(_linear8bit_train_backward,
+                                   setup_context=_linear8bit_train_setup)
+
+
+class Linear8bit(torch.nn.Module):
+    """A bias-free ``nn.Linear(in_features, out_features)`` whose weight is held as
+    int8 codes with one scale for each output feature, frozen; the forward
+    (``torch.ops.bnbx.linear8bit``) quantizes its input for each row and multiplies
+    8-bit integers.  ``load_weight`` quantizes a [out, in] weight on the device."""
+
+    def __init__(self, in_features: int, out_features: int,
+                 compute_dtype: torch.dtype = torch.bfloat16, device="cuda"):
+        super().__init__()
+        if compute_dtype not in _DTYPES:
+            raise ValueError("compute_dtype must be torch.bfloat16 or torch.float16")
+        if in_features < 1 or out_features < 1:
+            raise ValueError("in_features and out_features must be positive")
+        self.in_features, self.out_features = in_features, out_features
+        self.compute_dtype = compute_dtype
+        self.register_buffer("codes", torch.zeros(out_features, _pitch16(in_features),
+                                                  dtype=torch.int8, device=device))
+        self.register_buffer("scale", torch.zeros(out_features, dtype=torch.float32,
+                                                  device=device))
+
+    def quantized(self) -> T.Int8Rows:
+        return T.Int8Rows((self.out_features, self.in_features), self.codes, self.scale,
+                          self.compute_dtype)
+
+    @torch.no_grad()
+    def load_weight(self, w: torch.Tensor) -> "Linear8bit":
+        """Quantize-on-load of a weight [out_features, in_features], rounded to the
+        compute dtype first."""
+        if tuple(w.shape) != (self.out_features, self.in_features):
+            raise ValueError(f"weight shape {tuple(w.shape)} != "
+                             f"{(self.out_features, self.in_features)}")
+        w = w.to(device=self.codes.device, dtype=self.compute_dtype)
+        T.quantize_rows(_matrix(w), out=self.quantized())
+        return self
+
+    @classmethod
+    def from_linear(cls, linear: torch.nn.Linear, **kw) -> "Linear8bit":
+        if linear.bias is not None:
+            raise ValueError("Linear8bit has no bias")
+        m = cls(linear.in_features, linear.out_features, device=linear.weight.device, **kw)
+        return m.load_weight(linear.weight)
+
+    def dequantize(self) -> torch.Tensor:
+        return T.dequantize_rows(self.quantized())
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if x.dtype != self.compute_dtype:
+            raise TypeError(f"input dtype {x.dtype} != compute dtype {self.compute_dtype}")
+        return torch.ops.bnbx.linear8bit(x, self.codes, self.scale)
+
+    def extra_repr(self) -> str:
+        return (f"in_features={self.in_features}, out_features={self.out_features}, "
+                f"compute_dtype={self.compute_dtype}")
+
+
+class Linear8bitTrain(torch.nn.Module):
+    """A bias-free linear layer that trains a 16-bit weight through 8-bit products:
+    every forward quantizes the weight for each output feature and the input for
+    each row (``torch.ops.bnbx.linear8bit_train``), and what the backward pass keeps
+    of the input are its codes.  The gradients pass the rounding to codes
+    unchanged: dX = dY . W_hat, dW = dY^T . X_hat."""
+
+    def __init__(self, in_features: int, out_features: int, dtype: torch.dtype = torch.bfloat16,
+                 device="cuda"):
+        super().__init__()
+        if dtype not in _DTYPES:
+            raise ValueError("dtype must be torch.bfloat16 or torch.float16")
+        self.in_features, self.out_features = in_features, out_features
+        self.weight = torch.nn.Parameter(torch.empty(out_features, in_features, dtype=dtype,
+                                                     device=device))
+        torch.nn.init.kaiming_uniform_(self.weight, a=5 ** 0.5)
+
+    @classmethod
+    def from_linear(cls, linear: torch.nn.Linear) -> "Linear8bitTrain":
+        if linear.bias is not None:
+            raise ValueError("Linear8bitTrain has no bias")
+        m = cls(linear.in_features, linear.out_features, linear.weight.dtype,
+                linear.weight.device)
+        with torch.no_grad():
+            m.weight.copy_(linear.weight)
+        return m
+
+    def freeze(self) -> Linear8bit:
+        """The layer with this weight's codes, for inference."""
+        m = Linear8bit(self.in_features, self.out_features, self.weight.dtype,
+                       self.weight.device)
+        return m.load_weight(self.weight)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if x.dtype != self.weight.dtype:
+            raise TypeError(f"input dtype {x.dtype} != weight dtype {self.weight.dtype}")
+        return torch.ops.bnbx.linear8bit_train(x, self.weight)[0]
+
+    def extra_repr(self) -> str:
+        return f"in_features={self.in_features}, out_features={self.out_features}"

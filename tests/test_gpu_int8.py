@@ -181,8 +181,13 @@ def test_linear_is_the_product_of_the_codes(M, N, K, dtype):
     assert torch.equal(T.gemm_int8(saved, wq), y)
 
 
-@pytest.mark.parametrize("M,N,K,dtype", [(2048, 6100, 512, "bf16"), (1000, 8192, 272, "f16"),
-                                         (4097, 4096, 96, "bf16")])
+@pytest.mark.parametrize("M,N,K,dtype", [
+    (2048, 6100, 512, "bf16"), (1000, 8192, 272, "f16"), (4097, 4096, 96, "bf16"),
+    (2000, 8100, 2000, "bf16"), (2047, 4090, 1040, "f16"), (1000, 4090, 1500, "bf16"),
+    (290, 4090, 1300, "f16"), (130, 4096, 4096, "bf16"), (70, 300, 20000, "f16"),
+    (300, 2000, 16000, "bf16"), (600, 1000, 12000, "f16"), (1, 40, 65536, "bf16"),
+    (2, 300, 32768, "f16"), (3, 100, 21824, "bf16"), (4, 50, 16384, "f16"),
+    (4, 50, 16400, "bf16"), (64, 130, 131071, "f16")])
 def test_linear_large_tiles(M, N, K, dtype):
     x, w = activations(M, K, 5, dtype), rand((N, K), 6, 0.02, dtype)
     product_check(T.linear_int8(x, held(w)), x, w, (M, N, K))
@@ -278,6 +283,19 @@ def test_gradients_large_tiles(dtype):
     M, N, K = 200, 3500, 4100
     dy, x = rand((M, N), 3, 0.05, dtype), activations(M, K, 4, dtype)
     v = values_of(*codes_in_64(x), DT[dtype])
+    gradient_check(T.gemm_int8_dw(dy, held(x)), dy.t(), v, "dw")
+    gradient_check(T.gemm_int8_dw(dy, held(x), dtype=torch.float32), dy.t(), v, "dw f32")
+
+
+@pytest.mark.parametrize("R,C,T_", [(200, 4096, 4096), (1000, 4100, 1000), (1001, 4100, 777),
+                                    (64, 4090, 4096), (2048, 6100, 320), (40, 130, 9000),
+                                    (2000, 2000, 130), (700, 700, 5000)])
+def test_gradients_of_every_form(R, C, T_):
+    dy, w = rand((R, T_ // 8 * 8), 1, 0.05), rand((T_ // 8 * 8, C), 2, 0.02)
+    gradient_check(T.gemm_int8_dx(dy, held(w)), dy, values_of(*codes_in_64(w), torch.bfloat16),
+                   "dx")
+    dy, x = rand((T_, R), 3, 0.05, "f16"), activations(T_, C, 4, "f16")
+    v = values_of(*codes_in_64(x), torch.float16)
     gradient_check(T.gemm_int8_dw(dy, held(x)), dy.t(), v, "dw")
     gradient_check(T.gemm_int8_dw(dy, held(x), dtype=torch.float32), dy.t(), v, "dw f32")
 
