@@ -4,8 +4,7 @@
 // Both stream: 2 bytes in and 1 out an element, or 1 in and 2 out.  The
 // quantizer holds its row in registers between the maximum and the codes, so X is
 // read once: a team of T threads owns a row, thread t the 8-element pieces t, t +
-// T, ...  The smallest team that holds the row is taken where there are rows
-// enough to fill the GPU, else the largest, for the latency of a single row.
+// T, ...
 #include "bnbx_int8_device.hpp"
 
 namespace bnbx {
@@ -126,17 +125,19 @@ hipError_t quantize(const uint16_t* x, int64_t ldx, const Int8Rows& q, hipStream
   return hipGetLastError();
 }
 
-// `few`: not enough rows for a wave on every SIMD.
+// The team that holds a row with few idle pieces and enough loads a thread.
+// Measured (us), (T, NP): 301 x 11008 (512, 3) 4.8, (256, 8) 5.4, (1024, 2) 5.4; 16 x
+// 4096 (256, 2) 2.9, (1024, 1) 3.1; 2048 x 8192 (256, 4) 10.3, (1024, 1) 13.4; 8192 x
+// 4096 (256, 2) 18.2, (64, 8) 19.3; 8192 x 14336 (512, 4) 64.0, (256, 8) 64.9.
 template <bool F16, bool VEC>
-hipError_t quantize(const uint16_t* x, int64_t ldx, const Int8Rows& q, bool few, hipStream_t s) {
+hipError_t quantize(const uint16_t* x, int64_t ldx, const Int8Rows& q, hipStream_t s) {
   const int pieces = (q.cols + 15) / 16 * 2;
   if (pieces <= 64) return quantize<64, 1, F16, VEC>(x, ldx, q, s);
-  if (!few && pieces <= 256) return quantize<64, 4, F16, VEC>(x, ldx, q, s);
-  if (pieces <= 256) return quantize<256, 1, F16, VEC>(x, ldx, q, s);
-  if (!few && pieces <= 512) return quantize<64, 8, F16, VEC>(x, ldx, q, s);
-  if (!few && pieces <= 1024) return quantize<256, 4, F16, VEC>(x, ldx, q, s);
-  if (!few && pieces <= 2048) return quantize<256, 8, F16, VEC>(x, ldx, q, s);
-  if (pieces <= 1024) return quantize<1024, 1, F16, VEC>(x, ldx, q, s);
+  if (pieces <= 256) return quantize<64, 4, F16, VEC>(x, ldx, q, s);
+  if (pieces <= 512) return quantize<256, 2, F16, VEC>(x, ldx, q, s);
+  if (pieces <= 1024) return quantize<256, 4, F16, VEC>(x, ldx, q, s);
+  if (pieces <= 1536) return quantize<512, 3, F16, VEC>(x, ldx, q, s);
+  if (pieces <= 2048) return quantize<512, 4, F16, VEC>(x, ldx, q, s);
   if (pieces <= 4096) return quantize<1024, 4, F16, VEC>(x, ldx, q, s);
   return quantize<1024, 0, F16, VEC>(x, ldx, q, s);
 }
@@ -158,9 +159,9 @@ bool pieces_at_16(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && 
 hipError_t launch_quantize_rows(const uint16_t* x, int64_t ldx, const Int8Rows& q, bool f16,
                                 hipStream_t s) {
   if (q.rows == 0) return hipSuccess;
-  const bool vec = pieces_at_16(x, ldx), few = q.rows < 4 * int8_cus();
-  if (f16) return vec ? quantize<true, true>(x, ldx, q, few, s) : quantize<true, false>(x, ldx, q, few, s);
-  return vec ? quantize<false, true>(x, ldx, q, few, s) : quantize<false, false>(x, ldx, q, few, s);
+  const bool vec = pieces_at_16(x, ldx);
+  if (f16) return vec ? quantize<true, true>(x, ldx, q, s) : quantize<true, false>(x, ldx, q, s);
+  return vec ? quantize<false, true>(x, ldx, q, s) : quantize<false, false>(x, ldx, q, s);
 }
 
 hipError_t launch_dequantize_rows(const Int8Rows& q, uint16_t* out, int64_t ldo, bool f16,

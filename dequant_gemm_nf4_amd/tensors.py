@@ -10,11 +10,8 @@ import math
 
 import torch
 
-from . import (BNBX_DTYPE_F32, AdaptersDesc, Int8RowsDesc, Nf4State, RowGroupsDesc,
-               bnbx_dequantize_nf4, bnbx_dequantize_rows_int8, bnbx_gemm_int8, bnbx_gemm_int8_dw,
-               bnbx_gemm_int8_dw_workspace_bytes, bnbx_gemm_int8_dx,
-               bnbx_gemm_int8_dx_workspace_bytes, bnbx_gemm_int8_workspace_bytes,
-               bnbx_linear_int8, bnbx_linear_int8_workspace_bytes, bnbx_quantize_rows_int8,
+from . import (BNBX_DTYPE_F32, AdaptersDesc, BnbxError, Int8RowsDesc, Nf4State, RowGroupsDesc,
+               bnbx_dequantize_nf4, current_stream, int8_lib,
                bnbx_gemm_nf4_experts,
                bnbx_gemm_nf4_adapters, bnbx_gemm_nf4_adapters_workspace_bytes,
                bnbx_gemm_nf4_experts_dx,
@@ -493,53 +490,84 @@ def empty_int8_rows(shape, dtype: torch.dtype = torch.bfloat16, device="cuda") -
                     torch.empty(rows, dtype=torch.float32, device=device), dtype)
 
 
-def _check_int8(name: str, q: Int8Rows, shape, dtype, device) -> None:
-    if tuple(q.shape) != tuple(shape) or q.dtype != dtype:
-        raise ValueError(f"{name} must be codes of {tuple(shape)} {dtype}, not "
+def _check_int8(name: str, q: Int8Rows, rows: int, cols: int, dtype, device) -> None:
+    if q.shape[0] != rows or q.shape[1] != cols or q.dtype != dtype:
+        raise ValueError(f"{name} must be codes of {(rows, cols)} {dtype}, not "
                          f"{tuple(q.shape)} {q.dtype}")
     if q.codes.device != device:
         raise ValueError(f"{name} is on {q.codes.device}, not on {device}")
 
 
-def _check_out(out: torch.Tensor, rows: int, cols: int, dtype, device) -> None:
-    _check_matrix("out", out, cols, dtype, device)
-    if out.shape[0] != rows:
-        raise ValueError(f"out has {out.shape[0]} rows, not {rows}")
+def _rows_ld(name: str, t: torch.Tensor, cols: int, dtype, device) -> tuple[int, int]:
+    """Rows and row stride (of one row or none its width) of a matrix, checked
+    as _check_matrix does; the usual case in few lookups (a call's own work takes
+    less time than its checks)."""
+    if t.dim() == 2 and t.dtype == dtype and t.device == device:
+        rows, width = t.shape
+        ld, step = t.stride()
+        if width == cols and step == 1 and rows < 2 ** 31:
+            return rows, ld if rows > 1 else cols
+    _check_matrix(name, t, cols, dtype, device)
+    return t.shape[0], t.stride(0) if t.shape[0] > 1 else cols
 
 
-def _width(t: torch.Tensor) -> int:
-    """Row stride; of a matrix of one row (or none) its width."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _out_ld(out: torch.Tensor, rows: int, cols: int, dtype, device) -> int:
+    have, ld = _rows_ld("out", out, cols, dtype, device)
+    if have != rows:
+        raise ValueError(f"out has {have} rows, not {rows}")
+    return ld
 
 
-def _nbytes_of(t: torch.Tensor | None) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
+def _int8_stream(stream, device) -> int | None:
+    if stream is None:
+        return current_stream(device.index)
+    return stream if isinstance(stream, int) else int(stream.cuda_stream)
+
+
+def _int8_call(name: str, *args) -> None:
+    status = getattr(int8_lib(), name)(*args)
+    if status != 0:
+        raise BnbxError(status, name)
+
+
+def _int8_scratch(name: str, args, workspace, device):
+    """The workspace a call needs (the given one, or one allocated here, which
+    the caller holds until the launch), its address and bytes."""
+    nbytes = getattr(int8_lib(), name + "_workspace_bytes")(*args)
+    if nbytes == 0:
+        return None, None, 0
+    held = _scratch(workspace, nbytes, device)
+    return held, held.data_ptr(), held.numel() * held.element_size()
 
 
 def quantize_rows(x: torch.Tensor, out: Int8Rows | None = None, stream=None) -> Int8Rows:
     """bnbx_quantize_rows_int8: the codes and scales of a 16-bit matrix, row by
     row."""
-    if x.dtype not in DTYPES:
-        raise TypeError(f"x must be bfloat16 or float16, not {x.dtype}")
+    dtype, device = x.dtype, x.device
+    if dtype not in DTYPES:
+        raise TypeError(f"x must be bfloat16 or float16, not {dtype}")
     if x.dim() != 2 or x.shape[1] < 1:
         raise ValueError(f"x must be [rows, columns], not {tuple(x.shape)}")
-    _check_matrix("x", x, x.shape[1], x.dtype, x.device)
+    cols = x.shape[1]
+    rows, ld = _rows_ld("x", x, cols, dtype, device)
     if out is not None:
-        _check_int8("out", out, x.shape, x.dtype, x.device)
-    with _on(x.device, stream):
-        q = out if out is not None else empty_int8_rows(x.shape, x.dtype, x.device)
-        bnbx_quantize_rows_int8(x, _width(x), q.desc, stream)
+        _check_int8("out", out, rows, cols, dtype, device)
+    with _on(device, stream):
+        q = out if out is not None else empty_int8_rows((rows, cols), dtype, device)
+        _int8_call("bnbx_quantize_rows_int8", x.data_ptr(), ld, q.desc,
+                   _int8_stream(stream, device))
     return q
 
 
 def dequantize_rows(q: Int8Rows, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """bnbx_dequantize_rows_int8: the 16-bit values of the codes."""
     device = q.codes.device
-    if out is not None:
-        _check_out(out, *q.shape, q.dtype, device)
+    rows, cols = q.shape
+    ld = _out_ld(out, rows, cols, q.dtype, device) if out is not None else cols
     with _on(device, stream):
-        y = out if out is not None else torch.empty(q.shape, dtype=q.dtype, device=device)
-        bnbx_dequantize_rows_int8(q.desc, y, _width(y), stream)
+        y = out if out is not None else torch.empty(rows, cols, dtype=q.dtype, device=device)
+        _int8_call("bnbx_dequantize_rows_int8", q.desc, y.data_ptr(), ld,
+                   _int8_stream(stream, device))
     return y
 
 
@@ -548,14 +576,14 @@ def gemm_int8(x: Int8Rows, w: Int8Rows, out: torch.Tensor | None = None,
     """Y = X . W^T from the codes of both (bnbx_gemm_int8): the int32 sums times
     the scales of their row of X and row of W."""
     (M, K), N, device = x.shape, w.shape[0], w.codes.device
-    _check_int8("w", w, (N, K), x.dtype, x.codes.device)
-    if out is not None:
-        _check_out(out, M, N, w.dtype, device)
+    _check_int8("w", w, N, K, x.dtype, x.codes.device)
+    ld = _out_ld(out, M, N, w.dtype, device) if out is not None else N
     with _on(device, stream):
         y = out if out is not None else torch.empty(M, N, dtype=w.dtype, device=device)
-        nbytes = bnbx_gemm_int8_workspace_bytes(M, N, K)
-        ws = _scratch(workspace, nbytes, device) if nbytes else None
-        bnbx_gemm_int8(x.desc, w.desc, y, _width(y), ws, _nbytes_of(ws), stream)
+        held, ws, nbytes = _int8_scratch("bnbx_gemm_int8", (M, N, K), workspace, device)
+        _int8_call("bnbx_gemm_int8", x.desc, w.desc, y.data_ptr(), ld, ws, nbytes,
+                   _int8_stream(stream, device))
+        del held
     return y
 
 
@@ -566,18 +594,18 @@ def linear_int8(x: torch.Tensor, w: Int8Rows, out: torch.Tensor | None = None,
     (bnbx_linear_int8).  ``saved`` takes X's codes, for gemm_int8_dw."""
     N, K = w.shape
     device = w.codes.device
-    _check_matrix("x", x, K, w.dtype, device)
-    M = x.shape[0]
-    if out is not None:
-        _check_out(out, M, N, w.dtype, device)
+    M, ldx = _rows_ld("x", x, K, w.dtype, device)
+    ld = _out_ld(out, M, N, w.dtype, device) if out is not None else N
     if saved is not None:
-        _check_int8("saved", saved, (M, K), w.dtype, device)
+        _check_int8("saved", saved, M, K, w.dtype, device)
     with _on(device, stream):
         y = out if out is not None else torch.empty(M, N, dtype=w.dtype, device=device)
-        nbytes = bnbx_linear_int8_workspace_bytes(M, N, K, saved is not None)
-        ws = _scratch(workspace, nbytes, device) if nbytes else None
-        bnbx_linear_int8(x, _width(x), M, w.desc, saved.desc if saved is not None else None, y,
-                         _width(y), ws, _nbytes_of(ws), stream)
+        held, ws, nbytes = _int8_scratch("bnbx_linear_int8", (M, N, K, saved is not None),
+                                         workspace, device)
+        _int8_call("bnbx_linear_int8", x.data_ptr(), ldx, M, w.desc,
+                   saved.desc if saved is not None else None, y.data_ptr(), ld, ws, nbytes,
+                   _int8_stream(stream, device))
+        del held
     return y
 
 
@@ -587,13 +615,13 @@ def _pieces(t: torch.Tensor, finite: bool) -> torch.Tensor:
     that are not so are copied, zeros behind them."""
     rows, cols = t.shape
     wide = -(-cols // 8) * 8
-    if cols == wide and (rows <= 1 or (t.stride(0) % 8 == 0 and t.stride(0) >= cols)) \
-            and t.data_ptr() % 16 == 0:
-        return t
-    if not finite and rows > 1 and t.stride(0) % 8 == 0 and t.stride(0) >= wide \
-            and t.data_ptr() % 16 == 0 and t.storage_offset() + (rows - 1) * t.stride(0) + wide \
-            <= t.untyped_storage().nbytes() // t.element_size():
-        return t
+    whole = rows <= 1 or (t.stride(0) % 8 == 0 and t.stride(0) >= cols)
+    if whole and t.data_ptr() % 16 == 0:
+        if cols == wide:
+            return t
+        if not finite and rows > 1 and t.stride(0) >= wide and t.storage_offset() + \
+                (rows - 1) * t.stride(0) + wide <= t.untyped_storage().nbytes() // t.element_size():
+            return t
     copy = t.new_zeros(rows, wide)
     copy[:, :cols] = t
     return copy[:, :cols]
@@ -610,16 +638,15 @@ def gemm_int8_dx(dy: torch.Tensor, w: Int8Rows, out: torch.Tensor | None = None,
     pieces of eight values is copied first."""
     N, K = w.shape
     device = w.codes.device
-    _check_matrix("dy", dy, N, w.dtype, device)
-    M = dy.shape[0]
-    if out is not None:
-        _check_out(out, M, K, w.dtype, device)
+    M, _ = _rows_ld("dy", dy, N, w.dtype, device)
+    ld = _out_ld(out, M, K, w.dtype, device) if out is not None else K
     with _on(device, stream):
         dy = _pieces(dy, True)
         y = out if out is not None else torch.empty(M, K, dtype=w.dtype, device=device)
-        nbytes = bnbx_gemm_int8_dx_workspace_bytes(M, N, K)
-        ws = _scratch(workspace, nbytes, device) if nbytes else None
-        bnbx_gemm_int8_dx(dy, _pitch(dy), M, w.desc, y, _width(y), ws, _nbytes_of(ws), stream)
+        held, ws, nbytes = _int8_scratch("bnbx_gemm_int8_dx", (M, N, K), workspace, device)
+        _int8_call("bnbx_gemm_int8_dx", dy.data_ptr(), _pitch(dy), M, w.desc, y.data_ptr(), ld, ws,
+                   nbytes, _int8_stream(stream, device))
+        del held
     return y
 
 
@@ -635,7 +662,7 @@ def gemm_int8_dw(dy: torch.Tensor, x: Int8Rows, out: torch.Tensor | None = None,
     if dy.dim() != 2 or dy.shape[0] != M or dy.shape[1] < 1:
         raise ValueError(f"dy must be [{M}, columns], not {tuple(dy.shape)}")
     N = dy.shape[1]
-    _check_matrix("dy", dy, N, x.dtype, device)
+    _rows_ld("dy", dy, N, x.dtype, device)
     if out is not None:
         if dtype is not None and out.dtype != dtype:
             raise TypeError(f"out is {out.dtype}, not {dtype}")
@@ -643,14 +670,13 @@ def gemm_int8_dw(dy: torch.Tensor, x: Int8Rows, out: torch.Tensor | None = None,
     dtype = x.dtype if dtype is None else dtype
     if dtype not in (x.dtype, torch.float32):
         raise TypeError(f"the gradient is {x.dtype} or float32, not {dtype}")
-    if out is not None:
-        _check_out(out, N, K, dtype, device)
+    ld = _out_ld(out, N, K, dtype, device) if out is not None else K
     with _on(device, stream):
         dy = _pieces(dy, False)
         y = out if out is not None else torch.empty(N, K, dtype=dtype, device=device)
-        nbytes = bnbx_gemm_int8_dw_workspace_bytes(M, N, K)
-        ws = _scratch(workspace, nbytes, device) if nbytes else None
-        bnbx_gemm_int8_dw(dy, _pitch(dy), N, x.desc, y, _width(y),
-                          BNBX_DTYPE_F32 if dtype == torch.float32 else DTYPES[dtype], ws,
-                          _nbytes_of(ws), stream)
+        held, ws, nbytes = _int8_scratch("bnbx_gemm_int8_dw", (M, N, K), workspace, device)
+        _int8_call("bnbx_gemm_int8_dw", dy.data_ptr(), _pitch(dy), N, x.desc, y.data_ptr(), ld,
+                   BNBX_DTYPE_F32 if dtype == torch.float32 else DTYPES[dtype], ws, nbytes,
+                   _int8_stream(stream, device))
+        del held
     return y
