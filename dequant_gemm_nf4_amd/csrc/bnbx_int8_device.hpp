@@ -1,6 +1,8 @@
 // Device helpers of the 8-bit operators.
 #pragma once
 
+#include <type_traits>
+
 #include "bnbx_device.hpp"
 #include "bnbx_int8.hpp"
 
@@ -58,6 +60,15 @@ __device__ __forceinline__ bool tile_of(int id, int tiles_m, int tiles_n, int& t
   tn = in / g;
   tm = group * G + (in - tn * g);
   return true;
+}
+
+// f(0), f(1), .. f(N - 1) with the numbers as types (unrolled buffers).
+template <int N, int K = 0, typename F>
+__device__ __forceinline__ void in_turn(F&& f) {
+  if constexpr (K < N) {
+    f(std::integral_constant<int, K>{});
+    in_turn<N, K + 1>(f);
+  }
 }
 
 // Codes of a row.  With a = max |x| the code is 127 x / a, exact quotient,

@@ -1,8 +1,8 @@
 // Y[M, N] = X . W^T over int8 codes with a scale for each row of both (the
 // 8-bit linear layer), for gfx950.
 //
-// Tiling.  A workgroup of four waves (2 x 2) owns TN rows of W by TM rows of X;
-// a wave 32 FN by 32 FM, as FN x FM tiles of v_mfma_i32_32x32x32_i8 with W as the
+// Tiling.  A workgroup of WN x WM waves owns TN rows of W by TM rows of X; a wave
+// 32 FN by 32 FM, as FN x FM tiles of v_mfma_i32_32x32x32_i8 with W as the
 // A operand: a lane then holds four consecutive n of one token.  K is walked in
 // steps of 128 bytes (whole cache lines), four substeps of 32.
 //
@@ -24,7 +24,7 @@
 namespace bnbx {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;   // of the reduction
 constexpr int BK = 128;
 
 // Scheduling-group masks (AMDGPU sched_group_barrier).
@@ -68,57 +68,60 @@ __device__ __forceinline__ void store8(uint16_t* y, u32x4_t v, int left, bool ve
 }
 
 // ND: buffers, 2 to 4.
-template <int FM, int FN, int ND, bool F16, bool SPLIT>
-__global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
-  constexpr int TM = 64 * FM, TN = 64 * FN;
-  constexpr int CW = TN / 32, CX = TM / 32;   // copies a wave and step
+template <int FM, int FN, int WM, int WN, int ND, bool F16, bool SPLIT>
+__global__ __launch_bounds__(64 * WM * WN) void int8_gemm_kernel(GemmArgs a) {
+  constexpr int TM = 32 * FM * WM, TN = 32 * FN * WN, WV = WM * WN;
+  constexpr int SUB = BK / 32, RCH = BK / 16, RI = 64 / RCH;   // RI: rows an instruction copies
+  constexpr int CW = TN / RI / WV, CX = TM / RI / WV;          // copies a wave and step
+  static_assert(CW * RI * WV == TN && CX * RI * WV == TM, "whole copies a wave");
   constexpr int kBuf = (TM + TN) * BK;
   __shared__ __attribute__((aligned(16))) uint8_t buf0[kBuf];
   __shared__ __attribute__((aligned(16))) uint8_t buf1[kBuf];
   __shared__ __attribute__((aligned(16))) uint8_t buf2[ND > 2 ? kBuf : 16];
   __shared__ __attribute__((aligned(16))) uint8_t buf3[ND > 3 ? kBuf : 16];
+  uint8_t* const bufs[4] = {buf0, buf1, buf2, buf3};
   int tm, tn;
   if (!tile_of(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn)) return;
   const int m0 = tm * TM, n0 = tn * TN;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
-  const int wn = (wave & 1) * 32 * FN, wm = (wave >> 1) * 32 * FM;   // the wave's corner
+  const int wn = wave % WN * 32 * FN, wm = wave / WN * 32 * FM;   // the wave's corner
   const int steps = (a.K + BK - 1) / BK;
   const int t0 = SPLIT ? (int)blockIdx.y * a.steps_per : 0;
   const int t1 = SPLIT ? (t0 + a.steps_per < steps ? t0 + a.steps_per : steps) : steps;
   const int kp = (a.K + 15) / 16 * 16;
 
-  // Copies: instruction i of a wave fills eight rows, lane l chunk slot l % 8 of
-  // row l / 8 of them.
+  // Copies: instruction i of a wave fills RI rows, lane l chunk slot l % RCH of row
+  // l / RCH of them.  A row's chunks are permuted by turn(row).
+  auto turn = [](int row) { return (row >> 1) & 7; };
   const rsrc8_t rw = rsrc8(a.w + (int64_t)n0 * a.ldw, (int64_t)kFar8);
   const rsrc8_t rx = rsrc8(a.x + (int64_t)m0 * a.ldx, (int64_t)kFar8);
   uint32_t off[CW + CX];
 #pragma unroll
   for (int i = 0; i < CW + CX; ++i) {
     const bool isw = i < CW;
-    const int r = isw ? (wave * CW + i) * 8 + (lane >> 3) : (wave * CX + i - CW) * 8 + (lane >> 3);
-    const int chunk = (lane & 7) ^ ((r >> 1) & 7);
+    const int r = (isw ? wave * CW + i : wave * CX + i - CW) * RI + lane / RCH;
+    const int chunk = (lane % RCH) ^ turn(r);
     const bool in = isw ? n0 + r < a.N : m0 + r < a.M;
     off[i] = in ? (uint32_t)r * (uint32_t)(isw ? a.ldw : a.ldx) + 16u * chunk : kFar8;
   }
-  // bytes of K left behind this lane's chunk of the even and odd instructions
-  const int c0 = (lane & 7) ^ ((lane >> 4) & 3), c1 = c0 ^ 4;
+  // this lane's chunk in the even instructions, and in the odd ones (eight rows on)
+  const int c0 = (lane % RCH) ^ turn(lane / RCH), c1 = c0 ^ 4;
   auto copies = [&](uint8_t* buf, int t, int i0, int i1) {
     const int left = kp - t * BK;
     const bool ok0 = 16 * c0 < left, ok1 = 16 * c1 < left;
 #pragma unroll
     for (int i = i0; i < i1; ++i) {
-      const int at = i < CW ? (wave * CW + i) * 8 : TN + (wave * CX + i - CW) * 8;
-      const int r8 = i < CW ? wave * CW + i : wave * CX + i - CW;
-      const uint32_t o = ((r8 & 1) ? ok1 : ok0) ? off[i] : kFar8;
-      copy16_lds(i < CW ? rw : rx, buf + at * BK, o, (uint32_t)t * BK);
+      const int ri = i < CW ? wave * CW + i : wave * CX + i - CW;
+      const uint32_t o = ((ri & 1) ? ok1 : ok0) ? off[i] : kFar8;
+      copy16_lds(i < CW ? rw : rx, buf + ((i < CW ? 0 : TN) + ri * RI) * BK, o, (uint32_t)t * BK);
     }
   };
 
   // Operand reads: lane (col, half) takes chunk 2 s + half of row col of a tile.
-  uint32_t rd[4];
+  uint32_t rd[SUB];
 #pragma unroll
-  for (int s = 0; s < 4; ++s) rd[s] = col * BK + 16 * ((2 * s + half) ^ ((col >> 1) & 7));
+  for (int s = 0; s < SUB; ++s) rd[s] = col * BK + 16 * ((2 * s + half) ^ turn(col));
   u32x4_t ow[2][FN], ox[2][FM];
   auto reads = [&](const uint8_t* buf, int s, int set) {
 #pragma unroll
@@ -143,6 +146,7 @@ __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
   // all but the last `out` of this wave's copies have landed, and every wave is here
   auto land = [&](auto out) {
     constexpr int n = decltype(out)::value;
+    static_assert(n < 64, "the memory counter");
     __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | (n >> 4) << 14);   // vmcnt(n)
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
@@ -166,55 +170,38 @@ __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
   };
 
   constexpr int C = CW + CX;
-  constexpr int C3 = C / 2;   // copies of a step that go out in substep 3, as its buffer is left
+  constexpr int CL = C / 2;   // copies of a step that go out in the last substep, as its
+                              // buffer is left; the others in the next substep
   using Ahead = std::integral_constant<int, (ND - 2) * C>;   // copies of later steps
-  {
-    uint8_t* const bufs[4] = {buf0, buf1, buf2, buf3};
 #pragma unroll
-    for (int k = 0; k < ND; ++k) copies(bufs[k], t0 + k, 0, k + 1 < ND ? C : C3);
-  }
-  land(std::integral_constant<int, (ND - 2) * C + C3>{});
+  for (int k = 0; k < ND; ++k) copies(bufs[k], t0 + k, 0, k + 1 < ND ? C : CL);
+  land(std::integral_constant<int, (ND - 2) * C + CL>{});
   reads(buf0, 0, 0);
-  auto step = [&](int t, uint8_t* last, uint8_t* cur, uint8_t* next) {
+  // step t, in buffer k of ND
+  auto step = [&](int t, auto at) {
+    constexpr int k = decltype(at)::value;
+    uint8_t* const last = bufs[(k + ND - 1) % ND];
+    uint8_t* const cur = bufs[k];
+    uint8_t* const next = bufs[(k + 1) % ND];
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      if (s == 0) copies(last, t + ND - 1, C3, C);
-      if (s == 3) {
+    for (int s = 0; s < SUB; ++s) {
+      const bool end = s == SUB - 1;
+      if (s == 0) copies(last, t + ND - 1, CL, C);
+      if (end) {
         land(Ahead{});
-        copies(cur, t + ND, 0, C3);
+        copies(cur, t + ND, 0, CL);
       }
-      reads(s == 3 ? next : cur, (s + 1) & 3, (s & 1) ^ 1);
+      reads(end ? next : cur, end ? 0 : s + 1, (s & 1) ^ 1);
       products(s & 1);
-      interleave(s == 3 ? C3 : s == 0 ? C - C3 : 0);
+      interleave(end ? CL : s == 0 ? C - CL : 0);
     }
   };
   int t = t0;
-  if constexpr (ND == 2) {
-    for (; t + 1 < t1; t += 2) {
-      step(t, buf1, buf0, buf1);
-      step(t + 1, buf0, buf1, buf0);
-    }
-    if (t < t1) step(t, buf1, buf0, buf1);
-  } else if constexpr (ND == 3) {
-    for (; t + 2 < t1; t += 3) {
-      step(t, buf2, buf0, buf1);
-      step(t + 1, buf0, buf1, buf2);
-      step(t + 2, buf1, buf2, buf0);
-    }
-    if (t < t1) step(t, buf2, buf0, buf1);
-    if (t + 1 < t1) step(t + 1, buf0, buf1, buf2);
-  } else {
-    for (; t + 3 < t1; t += 4) {
-      step(t, buf3, buf0, buf1);
-      step(t + 1, buf0, buf1, buf2);
-      step(t + 2, buf1, buf2, buf3);
-      step(t + 3, buf2, buf3, buf0);
-    }
-    if (t < t1) step(t, buf3, buf0, buf1);
-    if (t + 1 < t1) step(t + 1, buf0, buf1, buf2);
-    if (t + 2 < t1) step(t + 2, buf1, buf2, buf3);
-  }
+  for (; t + ND <= t1; t += ND) in_turn<ND>([&](auto k) { step(t + k, k); });
+  in_turn<ND - 1>([&](auto k) {
+    if (t + k < t1) step(t + k, k);
+  });
 
   if constexpr (SPLIT) {
     int* part = a.part + (int64_t)blockIdx.y * a.M * a.ldp;
@@ -242,8 +229,10 @@ __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
   // neighbouring lanes.
   land(All{});   // every wave has read its operands, and no copy is in flight
   constexpr int CH = 4 * FN;
-  static_assert(4 * 32 * CH * 16 <= (TM + TN) * BK, "results fit a buffer");
-  uint8_t* const mine = buf0 + wave * 32 * CH * 16;
+  constexpr int PER = ND > 2 ? (WV + 1) / 2 : WV;   // waves a buffer serves
+  static_assert(PER * 32 * CH * 16 <= kBuf && WV * 256 <= kBuf && TN <= 64 * WV,
+                "results and scales fit a buffer");
+  uint8_t* const mine = (wave < PER ? buf0 : buf2) + wave % PER * 32 * CH * 16;
   // the tile's scales of W (64 a wave, TN of them wanted)
   copy4_lds(rsrc8(a.sw, (int64_t)a.N * 4), buf1 + wave * 256,
             4u * (uint32_t)(n0 + 64 * wave + lane), 0);
@@ -274,7 +263,9 @@ __global__ __launch_bounds__(kThreads) void int8_gemm_kernel(GemmArgs a) {
   }
 }
 
-// The splits of K added, scaled and rounded: a thread takes four n.
+// The splits of K added, scaled and rounded: a thread takes four n, eight splits'
+// loads under way at a time.
+constexpr int kAtOnce = 8;
 template <bool F16>
 __global__ __launch_bounds__(kThreads) void int8_reduce_kernel(GemmArgs a) {
   const int quads = (a.N + 3) / 4;
@@ -283,8 +274,16 @@ __global__ __launch_bounds__(kThreads) void int8_reduce_kernel(GemmArgs a) {
        q += (int64_t)gridDim.x * kThreads) {
     const int m = (int)(q / quads), n = 4 * (int)(q - (int64_t)m * quads);
     const int* p = a.part + (int64_t)m * a.ldp + n;
-    i32x4_t s = *(const i32x4_t*)p;
-    for (int k = 1; k < a.splits; ++k) s += *(const i32x4_t*)(p + (int64_t)k * a.M * a.ldp);
+    const int64_t pitch = (int64_t)a.M * a.ldp;
+    i32x4_t s = {0, 0, 0, 0};
+    for (int k = 0; k < a.splits; k += kAtOnce) {
+      i32x4_t v[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        v[i] = k + i < a.splits ? *(const i32x4_t*)(p + (k + i) * pitch) : i32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) s += v[i];
+    }
     const float sx = a.sx[m];
     uint16_t* y = a.y + (int64_t)m * a.ldy + n;
     f32x4_t sw;
@@ -298,13 +297,14 @@ __global__ __launch_bounds__(kThreads) void int8_reduce_kernel(GemmArgs a) {
   }
 }
 
-// The forms: FM, FN, ND, and the time of a step of K with a workgroup on every CU
+// The forms: rows of X and of W a workgroup, and the time of a step of K with a workgroup on every CU
 // (us; 2048 x 8192 x 8192 and the sizes below, timed one form after the other).
 struct Shape {
-  int fm, fn;
+  int tm, tn;
   double step;
 };
-constexpr Shape kShapes[] = {{4, 4, 1.77}, {4, 2, 1.13}, {2, 2, 0.60}, {2, 1, 0.38}, {1, 1, 0.23}};
+constexpr Shape kShapes[] = {
+    {256, 256, 1.72}, {256, 128, 1.05}, {128, 128, 0.60}, {128, 64, 0.38}, {64, 64, 0.23}};
 struct Form {
   int shape;
   int splits, steps_per;   // of K
@@ -313,9 +313,10 @@ struct Form {
 // workgroups over the CUs (a last round that is not full is a little faster),
 // their steps, 4 us for a launch's first copies and its results, and for a split 3 us
 // for the second launch and the partial sums written and read at 6.5 TB/s.
-// Counted and measured (us), 301 x 4096 x 11008: 2 x 1 tiles whole 34 / 31, 2 x 2 in
-// two splits 34 / 34, 1 x 1 whole 44 / 44; 1000 x 4096 x 11008: 2 x 2 whole 56 / 59,
-// 4 x 2 in two 66 / 66; 2048 x 4096 x 4096: 4 x 2 whole 40 / 40, 4 x 4 whole 52 / 52.
+// Counted and measured (us), 301 x 4096 x 11008: 128 x 64 whole 34 / 31, 128 x 128 in
+// two splits 34 / 34, 64 x 64 whole 44 / 44; 1000 x 4096 x 11008: 128 x 128 whole 56 /
+// 58, 256 x 128 in two 61 / 64; 2048 x 4096 x 4096: 256 x 128 whole 38 / 38, 256 x 256
+// whole 51 / 48.
 Form form_of(int M, int N, int K) {
   const int cus = int8_cus();
   const int steps = (K + BK - 1) / BK;
@@ -323,8 +324,7 @@ Form form_of(int M, int N, int K) {
   double least = 1e30;
   for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
     const Shape& f = kShapes[i];
-    const int64_t tiles = (((int64_t)M + 64 * f.fm - 1) / (64 * f.fm)) *
-                          (((int64_t)N + 64 * f.fn - 1) / (64 * f.fn));
+    const int64_t tiles = (((int64_t)M + f.tm - 1) / f.tm) * (((int64_t)N + f.tn - 1) / f.tn);
     for (int splits = 1; splits <= 16 && (splits == 1 || steps / splits >= 4); ++splits) {
       const int per = (steps + splits - 1) / splits, n = (steps + per - 1) / per;
       if (n > 1 && tiles * n > 2 * (int64_t)cus) break;
@@ -346,11 +346,11 @@ hipError_t launch(const GemmArgs& a, int shape, hipStream_t s) {
   const int total = a.tiles_m * a.tiles_n;
   const dim3 grid((total + kXcds - 1) / kXcds * kXcds, a.splits);
   switch (shape) {
-    case 0: int8_gemm_kernel<4, 4, 2, F16, SPLIT><<<grid, kThreads, 0, s>>>(a); break;
-    case 1: int8_gemm_kernel<4, 2, 3, F16, SPLIT><<<grid, kThreads, 0, s>>>(a); break;
-    case 2: int8_gemm_kernel<2, 2, 4, F16, SPLIT><<<grid, kThreads, 0, s>>>(a); break;
-    case 3: int8_gemm_kernel<2, 1, 4, F16, SPLIT><<<grid, kThreads, 0, s>>>(a); break;
-    default: int8_gemm_kernel<1, 1, 4, F16, SPLIT><<<grid, kThreads, 0, s>>>(a);
+    case 0: int8_gemm_kernel<4, 2, 2, 4, 2, F16, SPLIT><<<grid, 512, 0, s>>>(a); break;
+    case 1: int8_gemm_kernel<2, 2, 4, 2, 3, F16, SPLIT><<<grid, 512, 0, s>>>(a); break;
+    case 2: int8_gemm_kernel<2, 1, 2, 4, 4, F16, SPLIT><<<grid, 512, 0, s>>>(a); break;
+    case 3: int8_gemm_kernel<2, 1, 2, 2, 4, F16, SPLIT><<<grid, 256, 0, s>>>(a); break;
+    default: int8_gemm_kernel<1, 1, 2, 2, 4, F16, SPLIT><<<grid, 256, 0, s>>>(a);
   }
   return hipGetLastError();
 }
@@ -379,9 +379,8 @@ hipError_t launch_int8_gemm(const Int8Rows& x, const Int8Rows& w, uint16_t* y, i
   a.K = x.cols;
   a.y = y;
   a.ldy = ldy;
-  const int wide_m = 64 * kShapes[f.shape].fm, wide_n = 64 * kShapes[f.shape].fn;
-  const int64_t tm = ((int64_t)a.M + wide_m - 1) / wide_m,
-                tn = ((int64_t)a.N + wide_n - 1) / wide_n;
+  const Shape& tile = kShapes[f.shape];
+  const int64_t tm = ((int64_t)a.M + tile.tm - 1) / tile.tm, tn = ((int64_t)a.N + tile.tn - 1) / tile.tn;
   // a launch counts its threads in 32 bits
   if (tm * tn * f.splits >= ((int64_t)1 << 32) / kThreads - kXcds) return hipErrorNotSupported;
   a.tiles_m = (int)tm;

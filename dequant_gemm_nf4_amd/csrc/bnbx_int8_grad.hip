@@ -404,7 +404,9 @@ __global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
   }
 }
 
-// The splits of t added in order and rounded: a thread takes four columns.
+// The splits of t added in order and rounded: a thread takes four columns, eight
+// splits' loads under way at a time.
+constexpr int kAtOnce = 8;
 template <int OUT>
 __global__ __launch_bounds__(kThreads) void int8_grad_reduce_kernel(GradArgs a) {
   const int quads = (a.C + 3) / 4;
@@ -415,8 +417,16 @@ __global__ __launch_bounds__(kThreads) void int8_grad_reduce_kernel(GradArgs a) 
     const int64_t r = q / quads;
     const int c = 4 * (int)(q - r * quads);
     const float* p = a.part + r * a.ldp + c;
-    f32x4_t s = *(const f32x4_t*)p;
-    for (int k = 1; k < a.splits; ++k) s += *(const f32x4_t*)(p + (int64_t)k * a.R * a.ldp);
+    const int64_t pitch = (int64_t)a.R * a.ldp;
+    f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k = 0; k < a.splits; k += kAtOnce) {
+      f32x4_t v[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        v[i] = k + i < a.splits ? *(const f32x4_t*)(p + (k + i) * pitch) : f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) s += v[i];
+    }
     store4<OUT>(a.out, r * a.ldo + c, s, a.C - c, vec);
   }
 }
