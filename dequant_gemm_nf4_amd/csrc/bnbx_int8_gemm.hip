@@ -79,7 +79,14 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_gemm_kernel(GemmArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t buf1[kBuf];
   __shared__ __attribute__((aligned(16))) uint8_t buf2[ND > 2 ? kBuf : 16];
   __shared__ __attribute__((aligned(16))) uint8_t buf3[ND > 3 ? kBuf : 16];
-  uint8_t* const bufs[4] = {buf0, buf1, buf2, buf3};
+  // buffer k mod ND, known at compile time
+  auto buf = [&](auto k) -> uint8_t* {
+    constexpr int i = decltype(k)::value % ND;
+    if constexpr (i == 0) return buf0;
+    if constexpr (i == 1) return buf1;
+    if constexpr (i == 2) return buf2;
+    return buf3;
+  };
   int tm, tn;
   if (!tile_of(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn)) return;
   const int m0 = tm * TM, n0 = tn * TN;
@@ -173,16 +180,17 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_gemm_kernel(GemmArgs a) {
   constexpr int CL = C / 2;   // copies of a step that go out in the last substep, as its
                               // buffer is left; the others in the next substep
   using Ahead = std::integral_constant<int, (ND - 2) * C>;   // copies of later steps
-#pragma unroll
-  for (int k = 0; k < ND; ++k) copies(bufs[k], t0 + k, 0, k + 1 < ND ? C : CL);
+  in_turn<ND>([&](auto k) {
+    copies(buf(k), t0 + k, 0, decltype(k)::value + 1 < ND ? C : CL);
+  });
   land(std::integral_constant<int, (ND - 2) * C + CL>{});
   reads(buf0, 0, 0);
   // step t, in buffer k of ND
   auto step = [&](int t, auto at) {
     constexpr int k = decltype(at)::value;
-    uint8_t* const last = bufs[(k + ND - 1) % ND];
-    uint8_t* const cur = bufs[k];
-    uint8_t* const next = bufs[(k + 1) % ND];
+    uint8_t* const last = buf(std::integral_constant<int, k + ND - 1>{});
+    uint8_t* const cur = buf(at);
+    uint8_t* const next = buf(std::integral_constant<int, k + 1>{});
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < SUB; ++s) {

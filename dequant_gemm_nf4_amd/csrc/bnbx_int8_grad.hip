@@ -14,12 +14,16 @@
 // then holds four consecutive columns of one row.  t is walked in steps of 64,
 // four substeps of 16.
 //
-// All operands go from global memory straight into LDS, two buffers; 16-byte
-// chunks are permuted by their row so that the reads below meet every bank evenly
-// (which rows a read meets is said at each).  Rows t past the end read as zero
+// All operands go from global memory straight into LDS, three or four buffers;
+// 16-byte chunks are permuted by their row so that the reads below meet every bank
+// evenly (which rows a read meets is said at each).  Rows t past the end read as zero
 // codes, scales and gradients.  The pipeline is that of the forward product: the
-// operands of a substep are read during the products of the one before, with one
-// wait and barrier a step before the last substep.
+// operands of a substep are read and the codes converted during the products of the
+// one before, with one wait and barrier a step before the last substep.
+//
+// What bounds it (4096 x 11008 x 4096, timed in copies with a part taken out): the
+// products with their reads 230 us, the copies 200, the conversion 30, which overlap
+// to 295 us or 1.25 PFLOP/s; a large bf16 library product of that shape runs at 0.92.
 #include <type_traits>
 
 #include "bnbx_int8_device.hpp"
@@ -85,16 +89,16 @@ __device__ __forceinline__ bool whole4(const void* out, int64_t ldo) {
   return (uintptr_t)out % (OUT == kOutF32 ? 16 : 8) == 0 && ldo % 4 == 0;
 }
 
-// ND: buffers, 2 to 4.  KW: groups of four waves; with two, each takes half of
-// every step's substeps and half of the rows at the end, so that two waves a SIMD
-// cover each other's waits.  OUT: kOutBf16 / kOutF16 / kOutF32; SPLIT: fp32 partial
-// sums instead.
-template <int FR, int FC, int ND, int KW, bool TURNED, bool F16, int OUT, bool SPLIT>
-__global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
-  constexpr int TR = 32 * FR, TC = 128 * FC, WV = 4 * KW;
-  constexpr int kA = TR * BT * 2, kV = BT * TC, kBuf = kA + kV + WV * BT * 4;
-  constexpr int CA = FR / KW, CV = 2 * FC / KW;   // copies a wave and step
-  static_assert(CA * KW == FR && CV * KW == 2 * FC, "whole copies a wave");
+// ND: buffers, 3 or 4.  LOAD: four more waves make all the copies, so that a wave
+// that multiplies never waits to hand one over (with the largest tile a wave's
+// registers leave no room for them).  OUT: kOutBf16 / kOutF16 / kOutF32; SPLIT: fp32
+// partial sums instead.
+template <int FR, int FC, int ND, bool LOAD, bool TURNED, bool F16, int OUT, bool SPLIT>
+__global__ __launch_bounds__(LOAD ? 512 : 256) void int8_grad_kernel(GradArgs a) {
+  constexpr int TR = 32 * FR, TC = 128 * FC;
+  constexpr int CW = 4;   // waves that copy: those that multiply, or the four behind them
+  constexpr int kA = TR * BT * 2, kV = BT * TC, kBuf = kA + kV + CW * BT * 4;
+  constexpr int CA = FR, CV = 2 * FC;   // copies of such a wave and step
   __shared__ __attribute__((aligned(16))) uint8_t buf0[kBuf];
   __shared__ __attribute__((aligned(16))) uint8_t buf1[kBuf];
   __shared__ __attribute__((aligned(16))) uint8_t buf2[ND > 2 ? kBuf : 16];
@@ -103,7 +107,7 @@ __global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
   if (!tile_of(blockIdx.x, a.tiles_r, a.tiles_c, tr, tc)) return;
   const int r0 = tr * TR, c0 = tc * TC;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wc = wave & 3, kg = wave >> 2;   // the wave's columns, its substeps
+  const int cw = wave & 3;   // its number among those that multiply, or copy
   const int col = lane & 31, half = lane >> 5;
   const int steps = (a.T + BT - 1) / BT;
   const int t0 = SPLIT ? (int)blockIdx.y * a.steps_per : 0;
@@ -117,7 +121,7 @@ __global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
   uint32_t voff[CV];
 #pragma unroll
   for (int i = 0; i < CV; ++i) {
-    const int t = (wave * CV + i) * VR + lane / VCH;
+    const int t = (cw * CV + i) * VR + lane / VCH;
     const int ch = (lane % VCH) ^ turn_v(t);
     voff[i] = c0 + 16 * ch < cp ? (uint32_t)t * (uint32_t)a.ldv + 16u * ch : kFar8;
   }
@@ -131,7 +135,7 @@ __global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
   uint32_t aoff[CA];
 #pragma unroll
   for (int i = 0; i < CA; ++i) {
-    const int row = (wave * CA + i) * AR + lane / ACH;
+    const int row = (cw * CA + i) * AR + lane / ACH;
     const int ch = (lane % ACH) ^ turn_a(row);
     const bool in = TURNED ? r0 + 8 * ch < a.R : r0 + row < a.R;
     aoff[i] = in ? (uint32_t)row * (uint32_t)a.ldy * 2u + 16u * ch : kFar8;
@@ -159,18 +163,18 @@ __global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
     return f;
   };
   constexpr int C = CV + 1 + CA;
-  auto copy = [&](uint8_t* buf, const Source& f, int i) {
+  auto copy = [&](uint8_t* to_buf, const Source& f, int i) {
     if (i < CV) {
-      copy16_lds(f.v, buf + kA + (wave * CV + i) * 1024, voff[i], 0);
+      copy16_lds(f.v, to_buf + kA + (cw * CV + i) * 1024, voff[i], 0);
     } else if (i == CV) {
-      copy4_lds(f.s, buf + kA + kV + wave * BT * 4, 4u * lane, 0);
+      copy4_lds(f.s, to_buf + kA + kV + cw * BT * 4, 4u * lane, 0);
     } else {
       i -= CV + 1;
-      uint8_t* const to = buf + (wave * CA + i) * 1024;
+      uint8_t* const to = to_buf + (cw * CA + i) * 1024;
       if constexpr (TURNED)
         copy16_lds(f.y, to, aoff[i], 0);
       else
-        copy16_lds(f.y, to, (((wave * CA + i) & 1) ? f.ok1 : f.ok0) ? aoff[i] : kFar8, f.soff);
+        copy16_lds(f.y, to, (((cw * CA + i) & 1) ? f.ok1 : f.ok0) ? aoff[i] : kFar8, f.soff);
     }
   };
 
@@ -187,16 +191,16 @@ __global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
     const int t = 8 * (g >> 1) + (l16 >> 1);   // + 16 s, which leaves turn_v alone
 #pragma unroll
     for (int f = 0; f < FC; ++f) {
-      const int ch = ((wc * FC + f) * 2 + (g & 1)) ^ turn_v(t);
+      const int ch = ((cw * FC + f) * 2 + (g & 1)) ^ turn_v(t);
       vrd[f] = kA + t * TC + 16 * ch + 8 * (l16 & 1);
     }
   }
-  const uint32_t srd = kA + kV + wave * BT * 4 + 32 * half;
+  const uint32_t srd = kA + kV + cw * BT * 4 + 32 * half;
   // Gradients: row col of a tile, chunk 2 s + half; or four rows t of 16 values in
   // 16 lanes (four lanes a row), twice, each row in other banks.  turn_a moves
   // whole groups of four chunks (two with FR = 2), so tiles four apart differ by a
   // constant.
-  constexpr int SUB = 4 / KW;   // substeps of a wave
+  constexpr int SUB = 4;   // substeps of a step
   constexpr int NRD = TURNED ? (FR < 4 ? FR : 4) : SUB;
   uint32_t ard[NRD];
   if constexpr (TURNED) {
@@ -208,20 +212,19 @@ __global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
   } else {
 #pragma unroll
     for (int s = 0; s < SUB; ++s)
-      ard[s] = col * BT * 2 + 16 * ((2 * (s + SUB * kg) + half) ^ turn_a(col));
+      ard[s] = col * BT * 2 + 16 * ((2 * s + half) ^ turn_a(col));
   }
-  const uint32_t sub0 = 16 * SUB * kg;   // the wave's first t of a step
   // Read i of substep s: the codes, the scales, then the gradients.
   constexpr int NR = FC + 2 + FR;
   auto read = [&](const uint8_t* buf, int s, int set, int i) {
     if (i < FC) {
-      oc[i] = read_tr8(buf + vrd[i] + (16 * s + sub0) * TC);
+      oc[i] = read_tr8(buf + vrd[i] + 16 * s * TC);
     } else if (i < FC + 2) {
-      os[i - FC] = *(const f32x4_t*)(buf + srd + 4 * (16 * s + sub0) + 16 * (i - FC));
+      os[i - FC] = *(const f32x4_t*)(buf + srd + 64 * s + 16 * (i - FC));
     } else {
       const int f = i - FC - 2;
       if constexpr (TURNED) {
-        const uint8_t* p = buf + ard[f % NRD] + (16 * s + sub0) * TR * 2 + f / NRD * 256;
+        const uint8_t* p = buf + ard[f % NRD] + 16 * s * TR * 2 + f / NRD * 256;
         const u32x2_t lo = read_tr16(p), hi = read_tr16(p + 4 * TR * 2);
         oa[set][f] = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
       } else {
@@ -254,26 +257,57 @@ __global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
 
   // The copies of a step go out as its buffer is left: the first CL of them in the
   // last substep, the rest in the substeps after it.
-  constexpr int CL = SUB == 2 ? (C + 1) / 2 : (C + 2) / 3;
-  constexpr int C0 = SUB == 2 ? C : CL + (C - CL + 1) / 2;   // up to substep 0; then all
-  using Ahead = std::integral_constant<int, (ND - 2) * C>;   // of later steps
-  {
-    uint8_t* const bufs[4] = {buf0, buf1, buf2, buf3};
+  constexpr int CL = (C + 2) / 3, C0 = CL + (C - CL + 1) / 2;   // up to substep 0; then all
+  using Ahead = std::integral_constant<int, LOAD ? 0 : (ND - 2) * C>;   // of later steps
+  if constexpr (LOAD) {
+    if (wave >= 4) {
+      static_assert(ND == 4, "four buffers");
+      auto step_of = [&](uint8_t* to, int t) {
+        const Source f = source(t);
 #pragma unroll
-    for (int k = 0; k < ND; ++k) {
-      const Source f = source(t0 + k);
-#pragma unroll
-      for (int i = 0; i < (k + 1 < ND ? C : CL); ++i) copy(bufs[k], f, i);
+        for (int i = 0; i < C; ++i) copy(to, f, i);
+      };
+      step_of(buf0, t0);
+      step_of(buf1, t0 + 1);
+      step_of(buf2, t0 + 2);
+      step_of(buf3, t0 + 3);
+      land(std::integral_constant<int, 3 * C>{});
+      auto turn = [&](int t, uint8_t* cur) {
+        land(std::integral_constant<int, 2 * C>{});
+        step_of(cur, t + 4);
+      };
+      int t = t0;
+      for (; t + 3 < t1; t += 4) {
+        turn(t, buf0);
+        turn(t + 1, buf1);
+        turn(t + 2, buf2);
+        turn(t + 3, buf3);
+      }
+      if (t < t1) turn(t, buf0);
+      if (t + 1 < t1) turn(t + 1, buf1);
+      if (t + 2 < t1) turn(t + 2, buf2);
+      land(All{});   // nothing is in flight
+      return;
     }
+  } else {
+    static_assert(ND == 3, "three buffers");
+    const Source f0 = source(t0), f1 = source(t0 + 1), f2 = source(t0 + 2);
+#pragma unroll
+    for (int i = 0; i < C; ++i) copy(buf0, f0, i);
+#pragma unroll
+    for (int i = 0; i < C; ++i) copy(buf1, f1, i);
+#pragma unroll
+    for (int i = 0; i < CL; ++i) copy(buf2, f2, i);
   }
-  land(std::integral_constant<int, Ahead::value + CL>{});
+  land(std::integral_constant<int, LOAD ? 0 : Ahead::value + CL>{});
 #pragma unroll
   for (int i = 0; i < NR; ++i) read(buf0, 0, 0, i);
 #pragma unroll
   for (int i = 0; i < NP; ++i) convert(0, i);
 
   auto step = [&](int t, uint8_t* last, uint8_t* cur, uint8_t* next) {
-    Source f = source(t + ND - 1);
+    Source f{};
+    if constexpr (!LOAD) f = source(t + ND - 1);
 #pragma unroll
     for (int s = 0; s < SUB; ++s) {
       const int set = s & 1;
@@ -281,7 +315,7 @@ __global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
       __builtin_amdgcn_sched_barrier(0);
       if (end) {
         land(Ahead{});
-        f = source(t + ND);
+        if constexpr (!LOAD) f = source(t + ND);
       }
       uint8_t* const to = end ? cur : last;
       const int i0 = end ? 0 : s == 0 ? CL : s == 1 ? C0 : C;
@@ -301,19 +335,13 @@ __global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
           if (H + k * (N - H) / NP == q) convert(set ^ 1, k);
 #pragma unroll
         for (int k = i0; k < i1; ++k)
-          if ((k - i0) * N / (i1 - i0) == q) copy(to, f, k);
+          if (!LOAD && (k - i0) * N / (i1 - i0) == q) copy(to, f, k);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
   int t = t0;
-  if constexpr (ND == 2) {
-    for (; t + 1 < t1; t += 2) {
-      step(t, buf1, buf0, buf1);
-      step(t + 1, buf0, buf1, buf0);
-    }
-    if (t < t1) step(t, buf1, buf0, buf1);
-  } else if constexpr (ND == 3) {
+  if constexpr (ND == 3) {
     for (; t + 2 < t1; t += 3) {
       step(t, buf2, buf0, buf1);
       step(t + 1, buf0, buf1, buf2);
@@ -334,41 +362,6 @@ __global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
   }
   land(All{});   // every wave has read its operands, and no copy is in flight
 
-  // With two groups: each hands the other the sums of half the rows.
-  constexpr int FE = FR / KW;   // tiles of rows a wave finishes
-  if constexpr (KW == 2) {
-    constexpr int kHand = FC * FE * 4096;   // bytes a wave hands over
-    static_assert(ND > 3 && 2 * kHand <= kBuf, "two waves' sums fit a buffer");
-    uint8_t* const mine = (wc == 0 ? buf0 : wc == 1 ? buf1 : wc == 2 ? buf2 : buf3);
-#pragma unroll
-    for (int j = 0; j < FE; ++j)
-#pragma unroll
-      for (int i = 0; i < FC; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          f32x4_t v;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = kg == 0 ? acc[i][FE + j][4 * q + e] : acc[i][j][4 * q + e];
-          *(f32x4_t*)(mine + kg * kHand + 16 * (((j * FC + i) * 4 + q) * 64 + lane)) = v;
-        }
-    land(All{});
-#pragma unroll
-    for (int j = 0; j < FE; ++j)
-#pragma unroll
-      for (int i = 0; i < FC; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x4_t v = *(const f32x4_t*)(mine + (kg ^ 1) * kHand +
-                                              16 * (((j * FC + i) * 4 + q) * 64 + lane));
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[i][j][4 * q + e] =
-                kg == 0 ? acc[i][j][4 * q + e] + v[e] : v[e] + acc[i][FE + j][4 * q + e];
-        }
-    land(All{});
-  }
-
   // ---- results: value 4 q + e of a tile is row col, column 8 q + 4 half + e ----
   // Through LDS, 32 rows at a time in a wave's own part of a buffer (16-byte chunks
   // permuted by the row), so that a row is written by neighbouring lanes.
@@ -380,12 +373,9 @@ __global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
   const int cend = SPLIT ? (int)a.ldp : a.C;
   const bool vec = SPLIT || whole4<KIND>(out, ldo);
   auto turn_o = [](int row) { return FC == 2 ? row & 15 : (row >> 1) & 7; };
-  uint8_t* const mine =
-      (KW == 2 ? (wc == 0 ? buf0 : wc == 1 ? buf1 : wc == 2 ? buf2 : buf3) + kg * 32 * OCH * 16
-               : (wave < 2 ? buf0 : buf1) + (wave & 1) * 32 * OCH * 16);
-  const int re = r0 + 32 * FE * kg;
+  uint8_t* const mine = (wave < 2 ? buf0 : buf1) + (wave & 1) * 32 * OCH * 16;
 #pragma unroll
-  for (int j = 0; j < FE; ++j) {
+  for (int j = 0; j < FR; ++j) {
 #pragma unroll
     for (int i = 0; i < FC; ++i)
 #pragma unroll
@@ -398,7 +388,7 @@ __global__ __launch_bounds__(256 * KW) void int8_grad_kernel(GradArgs a) {
     for (int k = 0; k < 32 / OR; ++k) {
       const int row = k * OR + lane / OCH, ch = lane % OCH;
       const f32x4_t v = *(const f32x4_t*)(mine + 16 * (row * OCH + (ch ^ turn_o(row))));
-      const int r = re + 32 * j + row, c = c0 + 32 * FC * wc + 4 * ch;
+      const int r = r0 + 32 * j + row, c = c0 + 32 * FC * cw + 4 * ch;
       if (r < a.R && c < cend) store4<KIND>(out, (int64_t)r * ldo + c, v, cend - c, vec);
     }
   }
@@ -437,16 +427,17 @@ struct Shape {
   int fr, fc;
   double step;
 };
-constexpr Shape kShapes[] = {{8, 2, 1.72}, {4, 2, 1.03}, {4, 1, 0.61}, {2, 1, 0.42}};
+constexpr Shape kShapes[] = {
+    {8, 2, 1.72}, {4, 2, 0.92}, {4, 1, 0.57}, {2, 1, 0.36}, {1, 1, 0.31}};
 struct Form {
   int shape;
   int splits, steps_per;   // of t
 };
 // As the forward product's: rounds of workgroups, steps, 4 us a launch, and for a
 // split of t 3 us and the partial sums at 6.5 TB/s.  Counted and measured (us), R x
-// T x C = 200 x 4096 x 4096: 4 x 1 in four 21 / 22, 2 x 1 in two 22 / 23, 4 x 2 in eight
-// 23 / 26; 1000 x 4096 x 4096: 4 x 1 whole 43 / 45, 4 x 2 in two 49 / 53; 1001 x 777 x
-// 4100: 4 x 2 whole 17 / 21, 2 x 1 whole 20 / 24.
+// T x C = 200 x 4096 x 4096: 4 x 1 in four 20 / 21, 2 x 1 in two 21 / 23, 4 x 2 in eight
+// 22 / 25; 1000 x 4096 x 4096: 4 x 1 whole 40 / 42, 4 x 2 in two 43 / 46; 1001 x 777 x
+// 4100: 4 x 2 whole 14 / 21, 2 x 1 whole 18 / 23.
 Form form_of(int R, int C, int T) {
   const int cus = int8_cus();
   const int steps = (T + BT - 1) / BT;
@@ -476,10 +467,11 @@ template <bool TURNED, bool F16, int OUT, bool SPLIT>
 hipError_t launch(const GradArgs& a, int shape, hipStream_t s) {
   const dim3 grid((a.tiles_r * a.tiles_c + kXcds - 1) / kXcds * kXcds, a.splits);
   switch (shape) {
-    case 0: int8_grad_kernel<8, 2, 3, 1, TURNED, F16, OUT, SPLIT><<<grid, 256, 0, s>>>(a); break;
-    case 1: int8_grad_kernel<4, 2, 4, 2, TURNED, F16, OUT, SPLIT><<<grid, 512, 0, s>>>(a); break;
-    case 2: int8_grad_kernel<4, 1, 4, 2, TURNED, F16, OUT, SPLIT><<<grid, 512, 0, s>>>(a); break;
-    default: int8_grad_kernel<2, 1, 4, 2, TURNED, F16, OUT, SPLIT><<<grid, 512, 0, s>>>(a);
+    case 0: int8_grad_kernel<8, 2, 3, false, TURNED, F16, OUT, SPLIT><<<grid, 256, 0, s>>>(a); break;
+    case 1: int8_grad_kernel<4, 2, 4, true, TURNED, F16, OUT, SPLIT><<<grid, 512, 0, s>>>(a); break;
+    case 2: int8_grad_kernel<4, 1, 4, true, TURNED, F16, OUT, SPLIT><<<grid, 512, 0, s>>>(a); break;
+    case 3: int8_grad_kernel<2, 1, 4, true, TURNED, F16, OUT, SPLIT><<<grid, 512, 0, s>>>(a); break;
+    default: int8_grad_kernel<1, 1, 4, true, TURNED, F16, OUT, SPLIT><<<grid, 512, 0, s>>>(a);
   }
   return hipGetLastError();
 }
