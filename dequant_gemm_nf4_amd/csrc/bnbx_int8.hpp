@@ -31,7 +31,7 @@ bool int8_few_takes(int M, int K);
 hipError_t launch_int8_few(const uint16_t* x, int64_t ldx, const Int8Rows& q, const Int8Rows& w,
                            uint16_t* y, int64_t ldy, bool f16, hipStream_t stream);
 
-// The same for up to 64 rows of X, without a workspace.
+// The same for up to 32 rows of X, without a workspace.
 bool int8_rows16_takes(int M);
 hipError_t launch_int8_rows16(const Int8Rows& x, const Int8Rows& w, uint16_t* y, int64_t ldy,
                               bool f16, hipStream_t stream);

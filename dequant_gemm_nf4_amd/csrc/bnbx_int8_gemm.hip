@@ -312,7 +312,7 @@ struct Shape {
   double step;
 };
 constexpr Shape kShapes[] = {
-    {256, 256, 1.72}, {256, 128, 1.05}, {128, 128, 0.60}, {128, 64, 0.38}, {64, 64, 0.23}};
+    {256, 256, 1.72}, {256, 128, 1.05}, {128, 128, 0.60}, {128, 64, 0.36}, {64, 64, 0.23}};
 struct Form {
   int shape;
   int splits, steps_per;   // of K
@@ -321,7 +321,7 @@ struct Form {
 // workgroups over the CUs (a last round that is not full is a little faster),
 // their steps, 4 us for a launch's first copies and its results, and for a split 3 us
 // for the second launch and the partial sums written and read at 6.5 TB/s.
-// Counted and measured (us), 301 x 4096 x 11008: 128 x 64 whole 34 / 31, 128 x 128 in
+// Counted and measured (us), 301 x 4096 x 11008: 128 x 64 whole 33 / 31, 128 x 128 in
 // two splits 34 / 34, 64 x 64 whole 44 / 44; 1000 x 4096 x 11008: 128 x 128 whole 56 /
 // 58, 256 x 128 in two 61 / 64; 2048 x 4096 x 4096: 256 x 128 whole 38 / 38, 256 x 256
 // whole 51 / 48.

@@ -1,15 +1,16 @@
-// Y = X . W^T over int8 codes for up to 64 rows of X (decode batches), for gfx950.
+// Y = X . W^T over int8 codes for up to 32 rows of X (decode batches), for gfx950.
 //
-// Bound: streaming W once.  A workgroup owns 16 FN rows of W and all rows of X (16
-// FM); its waves take the 128-byte steps of K in turn, each with a tile of its own
-// (FN x FM of v_mfma_i32_16x16x64_i8, W the A operand), and add their int32 sums
+// Bound: streaming W once.  A workgroup owns 16 rows of W and all rows of X (16 FM);
+// its waves take the 128-byte steps of K in turn, each with a tile of its own (FM of
+// v_mfma_i32_16x16x64_i8, W the A operand), and add their int32 sums
 // through LDS at the end.  So no wave waits for another until then, and a launch
 // needs no second one to join parts of K.
 //
 // Both operands go from global memory straight into a wave's own LDS (buffer_load
 // ... lds, eight rows of 128 bytes an instruction, 16-byte chunks permuted by the
-// row pair so that 16 lanes reading one chunk of 16 rows meet all banks once); ND
-// steps are under way at a time, and a wave waits for the oldest one only.  Rows
+// row pair so that 16 lanes reading one chunk of 16 rows meet all banks once); two
+// steps are under way at a time, and a wave waits for the older one only (three took 15.7
+// us where two take 13.5, 16 x 11008 x 4096: fewer workgroups on a CU).  Rows
 // past the end and chunks past K read as zeros through the buffer range check.
 #include <type_traits>
 
@@ -31,14 +32,13 @@ struct Rows16Args {
   int64_t ldy;
 };
 
-template <int FM, int FN, int WV, int ND, bool F16>
+template <int FM, int WV, bool F16>
 __global__ __launch_bounds__(WV * 64) void int8_rows16_kernel(Rows16Args a) {
+  constexpr int FN = 1, ND = 2;
   constexpr int kTile = 16 * BK, kStep = (FN + FM) * kTile;   // bytes of a wave's step
   constexpr int C = 2 * (FN + FM);                            // copies of a step
   __shared__ __attribute__((aligned(16))) uint8_t buf0[WV * kStep];
   __shared__ __attribute__((aligned(16))) uint8_t buf1[WV * kStep];
-  __shared__ __attribute__((aligned(16))) uint8_t buf2[ND > 2 ? WV * kStep : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t buf3[ND > 3 ? WV * kStep : 16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = (int)blockIdx.x * 16 * FN;
   const int steps = (a.K + BK - 1) / BK, kp = (a.K + 15) / 16 * 16;
@@ -108,8 +108,6 @@ __global__ __launch_bounds__(WV * 64) void int8_rows16_kernel(Rows16Args a) {
   int t = wave;
   copies(buf0, t);
   copies(buf1, t + WV);
-  if constexpr (ND > 2) copies(buf2, t + 2 * WV);
-  if constexpr (ND > 3) copies(buf3, t + 3 * WV);
   auto step = [&](uint8_t* buf) {
     landed();
     products(buf);
@@ -121,14 +119,6 @@ __global__ __launch_bounds__(WV * 64) void int8_rows16_kernel(Rows16Args a) {
     step(buf0);
     if (t >= steps) break;
     step(buf1);
-    if constexpr (ND > 2) {
-      if (t >= steps) break;
-      step(buf2);
-    }
-    if constexpr (ND > 3) {
-      if (t >= steps) break;
-      step(buf3);
-    }
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): no copy is in flight
   __syncthreads();
@@ -171,28 +161,34 @@ __global__ __launch_bounds__(WV * 64) void int8_rows16_kernel(Rows16Args a) {
   }
 }
 
-template <int FM, int FN, int WV, int ND>
+template <int FM, int WV>
 hipError_t launch(const Rows16Args& a, bool f16, hipStream_t s) {
-  const int64_t grid = ((int64_t)a.N + 16 * FN - 1) / (16 * FN);
+  const int64_t grid = ((int64_t)a.N + 15) / 16;
   if (grid >= ((int64_t)1 << 32) / (WV * 64)) return hipErrorNotSupported;
   if (f16)
-    int8_rows16_kernel<FM, FN, WV, ND, true><<<(int)grid, WV * 64, 0, s>>>(a);
+    int8_rows16_kernel<FM, WV, true><<<(int)grid, WV * 64, 0, s>>>(a);
   else
-    int8_rows16_kernel<FM, FN, WV, ND, false><<<(int)grid, WV * 64, 0, s>>>(a);
+    int8_rows16_kernel<FM, WV, false><<<(int)grid, WV * 64, 0, s>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-bool int8_rows16_takes(int M) { return M <= 64; }
+// From 33 rows on the tiles are faster: 64 x 11008 x 4096 15.6 us against 22.3 here, 64
+// x 4096 x 11008 17.9 / 21.8 (but 64 x 4096 x 4096 10.3 / 9.1); 32 x 11008 x 4096 16.2 /
+// 15.4, 16 x 11008 x 4096 15.1 / 12.7.
+bool int8_rows16_takes(int M) { return M <= 32; }
 
 hipError_t launch_int8_rows16(const Int8Rows& x, const Int8Rows& w, uint16_t* y, int64_t ldy,
                               bool f16, hipStream_t s) {
   const Rows16Args a{x.codes, w.codes, x.scale, w.scale, x.ld, w.ld, x.rows, w.rows, x.cols,
                      y,       ldy};
-  if (x.rows <= 16) return launch<1, 1, 8, 2>(a, f16, s);
-  if (x.rows <= 32) return launch<2, 1, 8, 2>(a, f16, s);
-  return launch<4, 1, 4, 3>(a, f16, s);
+  // Many groups of 16 rows of W: four waves each, so that a CU holds more of them;
+  // few: eight, which split K further.  16 x 11008 x 4096 12.7 us / 13.5 with eight, 16
+  // x 4096 x 4096 6.5 / 6.2; 32 x 11008 x 4096 15.4 / 18.8, 32 x 4096 x 11008 17.9 / 16.4.
+  const bool many = w.rows / 16 > 2 * int8_cus();
+  if (x.rows <= 16) return many ? launch<1, 4>(a, f16, s) : launch<1, 8>(a, f16, s);
+  return many ? launch<2, 4>(a, f16, s) : launch<2, 8>(a, f16, s);
 }
 
 }  // namespace bnbx
