@@ -7,7 +7,7 @@
 // steps of 128 bytes (whole cache lines), four substeps of 32.
 //
 // Both operands go from global memory straight into LDS (buffer_load ... lds, 16
-// bytes a lane), two buffers.  A row is 128 bytes, its eight 16-byte chunks
+// bytes a lane), ND buffers.  A row is 128 bytes, its eight 16-byte chunks
 // permuted by (row / 2) % 8, so that 16 lanes reading one chunk of 16 consecutive
 // rows meet all 64 banks once.  Rows past the end and chunks past K read as zeros
 // through the buffer range check.
@@ -15,8 +15,15 @@
 // Pipeline of step t: substep s multiplies while the operands of substep s + 1
 // are read; before substep 3 one wait and barrier (step t+1 has landed, every
 // wave has read its last operands of step t), and under substep 3's products the
-// first operands of step t+1 are read and the copies of step t+2 begin, into the
-// buffer that step t has left.
+// first operands of step t+1 are read and the copies of step t+ND begin, into the
+// buffer that step t has left.  The wait leaves the copies of later steps in flight:
+// every memory operation of the loop is a copy into LDS, and these land in order.
+//
+// What bounds it: the large tiles the matrix units under the power limit (2048 x 8192
+// x 8192 115-125 us by the card's state, 2.2-2.4 POP/s; the library's int8 product 118;
+// copies and reads alone 96 us, products and reads alone 80-100), the small ones the
+// copies (301 x 4096 x 11008 31 us, copies alone 31, the rest alone 17): bytes come
+// from behind L2 at 45-80 B/ns a CU, from L2 at 130.
 #include <type_traits>
 
 #include "bnbx_int8_device.hpp"
@@ -211,6 +218,7 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_gemm_kernel(GemmArgs a) {
     if (t + k < t1) step(t + k, k);
   });
 
+  land(All{});   // every wave has read its operands, and no copy is in flight
   if constexpr (SPLIT) {
     int* part = a.part + (int64_t)blockIdx.y * a.M * a.ldp;
 #pragma unroll
@@ -235,7 +243,6 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_gemm_kernel(GemmArgs a) {
   // Results through LDS, 32 tokens at a time in a wave's own part of a buffer: rows
   // of 32 FN values, 16-byte chunks permuted by the row, so that a row is written by
   // neighbouring lanes.
-  land(All{});   // every wave has read its operands, and no copy is in flight
   constexpr int CH = 4 * FN;
   constexpr int PER = ND > 2 ? (WV + 1) / 2 : WV;   // waves a buffer serves
   static_assert(PER * 32 * CH * 16 <= kBuf && WV * 256 <= kBuf && TN <= 64 * WV,

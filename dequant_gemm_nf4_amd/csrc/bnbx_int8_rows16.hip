@@ -12,8 +12,6 @@
 // steps are under way at a time, and a wave waits for the older one only (three took 15.7
 // us where two take 13.5, 16 x 11008 x 4096: fewer workgroups on a CU).  Rows
 // past the end and chunks past K read as zeros through the buffer range check.
-#include <type_traits>
-
 #include "bnbx_int8_device.hpp"
 
 namespace bnbx {
@@ -34,24 +32,23 @@ struct Rows16Args {
 
 template <int FM, int WV, bool F16>
 __global__ __launch_bounds__(WV * 64) void int8_rows16_kernel(Rows16Args a) {
-  constexpr int FN = 1, ND = 2;
-  constexpr int kTile = 16 * BK, kStep = (FN + FM) * kTile;   // bytes of a wave's step
-  constexpr int C = 2 * (FN + FM);                            // copies of a step
+  constexpr int kTile = 16 * BK, kStep = (1 + FM) * kTile;   // bytes of a wave's step
+  constexpr int C = 2 * (1 + FM);                            // copies of a step
   __shared__ __attribute__((aligned(16))) uint8_t buf0[WV * kStep];
   __shared__ __attribute__((aligned(16))) uint8_t buf1[WV * kStep];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = (int)blockIdx.x * 16 * FN;
+  const int n0 = (int)blockIdx.x * 16;
   const int steps = (a.K + BK - 1) / BK, kp = (a.K + 15) / 16 * 16;
   const rsrc8_t rw = rsrc8(a.w + (int64_t)n0 * a.ldw, (int64_t)kFar8);
   const rsrc8_t rx = rsrc8(a.x, (int64_t)kFar8);
 
-  // copies: instruction i fills rows 8 i .. 8 i + 7 of the step, lane l chunk slot
-  // l % 8 of row l / 8; odd instructions permute by 4 more
+  // copies: instruction i fills rows 8 i .. 8 i + 7 of the step (16 of W, then X's), lane
+  // l chunk slot l % 8 of row l / 8; odd instructions permute by 4 more
   uint32_t off[C];
 #pragma unroll
   for (int i = 0; i < C; ++i) {
-    const bool isw = i < 2 * FN;
-    const int r = 8 * (isw ? i : i - 2 * FN) + (lane >> 3);
+    const bool isw = i < 2;
+    const int r = 8 * (isw ? i : i - 2) + (lane >> 3);
     const int chunk = (lane & 7) ^ ((r >> 1) & 7);
     const bool in = isw ? n0 + r < a.N : r < a.M;
     off[i] = in ? (uint32_t)r * (uint32_t)(isw ? a.ldw : a.ldx) + 16u * chunk : kFar8;
@@ -63,15 +60,13 @@ __global__ __launch_bounds__(WV * 64) void int8_rows16_kernel(Rows16Args a) {
     uint8_t* const mine = buf + wave * kStep;
 #pragma unroll
     for (int i = 0; i < C; ++i)
-      copy16_lds(i < 2 * FN ? rw : rx, mine + i * 1024, ((i & 1) ? ok1 : ok0) ? off[i] : kFar8,
+      copy16_lds(i < 2 ? rw : rx, mine + i * 1024, ((i & 1) ? ok1 : ok0) ? off[i] : kFar8,
                  (uint32_t)t * BK);
   };
 
-  i32x4_t acc[FN][FM];
+  i32x4_t acc[FM];
 #pragma unroll
-  for (int i = 0; i < FN; ++i)
-#pragma unroll
-    for (int j = 0; j < FM; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+  for (int j = 0; j < FM; ++j) acc[j] = i32x4_t{0, 0, 0, 0};
   // operand reads: row l % 16, chunk 4 s + l / 16
   const int row = lane & 15, q4 = lane >> 4;
   uint32_t rd[2];
@@ -79,42 +74,31 @@ __global__ __launch_bounds__(WV * 64) void int8_rows16_kernel(Rows16Args a) {
   for (int s = 0; s < 2; ++s) rd[s] = row * BK + 16 * ((4 * s + q4) ^ ((row >> 1) & 7));
   auto products = [&](const uint8_t* buf) {
     const uint8_t* const mine = buf + wave * kStep;
-    u32x4_t ow[2][FN], ox[2][FM];
+    u32x4_t ow[2], ox[2][FM];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
+      ow[s] = *(const u32x4_t*)(mine + rd[s]);
 #pragma unroll
-      for (int i = 0; i < FN; ++i) ow[s][i] = *(const u32x4_t*)(mine + i * kTile + rd[s]);
-#pragma unroll
-      for (int j = 0; j < FM; ++j) ox[s][j] = *(const u32x4_t*)(mine + (FN + j) * kTile + rd[s]);
+      for (int j = 0; j < FM; ++j) ox[s][j] = *(const u32x4_t*)(mine + (1 + j) * kTile + rd[s]);
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int j = 0; j < FM; ++j) acc[i][j] = mfma_i8_16x16x64(ow[s][i], ox[s][j], acc[i][j]);
+      for (int j = 0; j < FM; ++j) acc[j] = mfma_i8_16x16x64(ow[s], ox[s][j], acc[j]);
   };
-  // the oldest of ND steps under way has landed
-  auto landed = [&] {
-    constexpr int n = (ND - 1) * C;
-    static_assert(n < 64, "the memory counter");
-    __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | (n >> 4) << 14);   // vmcnt(n)
-    asm volatile("" ::: "memory");
-  };
-  // and its operands have been read
-  auto read = [&] { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
-
   // steps past the end copy zeros, which nothing multiplies
   int t = wave;
   copies(buf0, t);
   copies(buf1, t + WV);
   auto step = [&](uint8_t* buf) {
-    landed();
+    __builtin_amdgcn_s_waitcnt(0x0F70 | C);   // vmcnt(C): the older of two steps has landed
+    asm volatile("" ::: "memory");
     products(buf);
-    read();
-    copies(buf, t + ND * WV);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // its operands have been read
+    copies(buf, t + 2 * WV);
     t += WV;
   };
+  static_assert(C < 16, "the memory counter's low bits");
   while (t < steps) {
     step(buf0);
     if (t >= steps) break;
@@ -124,38 +108,29 @@ __global__ __launch_bounds__(WV * 64) void int8_rows16_kernel(Rows16Args a) {
   __syncthreads();
 
   // the waves' sums: a lane's four values of a tile in 16 bytes, wave by wave
-  constexpr int T = FN * FM;
-  constexpr int kRound = WV * kStep / 1024 / WV;   // tiles a buffer holds of every wave
-  static_assert(kRound >= 1, "a buffer holds a tile of every wave");
+  static_assert(FM * 1024 <= kStep, "a buffer holds every wave's tiles");
 #pragma unroll
-  for (int b = 0; b < T; b += kRound) {
-    const int count = T - b < kRound ? T - b : kRound;
-    if (b > 0) __syncthreads();
+  for (int j = 0; j < FM; ++j) *(i32x4_t*)(buf0 + 16 * ((wave * FM + j) * 64 + lane)) = acc[j];
+  __syncthreads();
+  if (wave < FM) {
+    i32x4_t s = {0, 0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < kRound; ++e)
-      if (b + e < T)
-        *(i32x4_t*)(buf0 + 16 * ((wave * kRound + e) * 64 + lane)) = acc[(b + e) / FM][(b + e) % FM];
-    __syncthreads();
-    for (int e = wave; e < count; e += WV) {
-      i32x4_t s = {0, 0, 0, 0};
+    for (int w = 0; w < WV; ++w)
+      s += *(const i32x4_t*)(buf0 + 16 * ((w * FM + wave) * 64 + lane));
+    const int m = 16 * wave + row, n = n0 + 4 * q4;
+    if (m < a.M && n < a.N) {
+      const float sx = a.sx[m];
+      float f[4];
 #pragma unroll
-      for (int w = 0; w < WV; ++w)
-        s += *(const i32x4_t*)(buf0 + 16 * ((w * kRound + e) * 64 + lane));
-      const int m = 16 * ((b + e) % FM) + row, n = n0 + 16 * ((b + e) / FM) + 4 * q4;
-      if (m < a.M && n < a.N) {
-        const float sx = a.sx[m];
-        float f[4];
+      for (int k = 0; k < 4; ++k) f[k] = ((float)s[k] * sx) * (n + k < a.N ? a.sw[n + k] : 0.0f);
+      uint16_t* y = a.y + (int64_t)m * a.ldy + n;
+      const u32x2_t v = {pack16x2<F16>(f[0], f[1]), pack16x2<F16>(f[2], f[3])};
+      if (n + 4 <= a.N && ((uintptr_t)a.y % 8 == 0) && a.ldy % 4 == 0) {
+        *(u32x2_t*)y = v;
+      } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) f[k] = ((float)s[k] * sx) * (n + k < a.N ? a.sw[n + k] : 0.0f);
-        uint16_t* y = a.y + (int64_t)m * a.ldy + n;
-        const u32x2_t v = {pack16x2<F16>(f[0], f[1]), pack16x2<F16>(f[2], f[3])};
-        if (n + 4 <= a.N && ((uintptr_t)a.y % 8 == 0) && a.ldy % 4 == 0) {
-          *(u32x2_t*)y = v;
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (n + k < a.N) y[k] = (uint16_t)(v[k / 2] >> (16 * (k & 1)));
-        }
+        for (int k = 0; k < 4; ++k)
+          if (n + k < a.N) y[k] = (uint16_t)(v[k / 2] >> (16 * (k & 1)));
       }
     }
   }
