@@ -21,6 +21,8 @@ hipError_t launch_dequantize_rows(const Int8Rows& q, uint16_t* out, int64_t ldo,
                                   hipStream_t stream);
 
 // Y = X . W^T over codes.
+// (fits: whether a launch counts its threads in 32 bits)
+bool int8_gemm_fits(int M, int N, int K);
 size_t int8_gemm_workspace(int M, int N, int K);
 hipError_t launch_int8_gemm(const Int8Rows& x, const Int8Rows& w, uint16_t* y, int64_t ldy,
                             bool f16, void* workspace, hipStream_t stream);
@@ -28,11 +30,13 @@ hipError_t launch_int8_gemm(const Int8Rows& x, const Int8Rows& w, uint16_t* y, i
 // The same for few rows of X, in one launch: x null, the codes q; else X's 16-bit
 // rows, whose codes are written to q where it has any.
 bool int8_few_takes(int M, int K);
+bool int8_few_fits(int N);
 hipError_t launch_int8_few(const uint16_t* x, int64_t ldx, const Int8Rows& q, const Int8Rows& w,
                            uint16_t* y, int64_t ldy, bool f16, hipStream_t stream);
 
 // The same for up to 32 rows of X, without a workspace.
 bool int8_rows16_takes(int M);
+bool int8_rows16_fits(int N);
 hipError_t launch_int8_rows16(const Int8Rows& x, const Int8Rows& w, uint16_t* y, int64_t ldy,
                               bool f16, hipStream_t stream);
 
@@ -51,6 +55,11 @@ struct GradGemm {
 size_t int8_grad_workspace(int R, int C, int T);
 hipError_t launch_int8_grad(const GradGemm& g, bool turned, bool f16, void* workspace,
                             hipStream_t stream);
+
+// Workgroups of `threads` threads that a launch takes: it counts threads in 32 bits.
+inline bool launch_fits(int64_t groups, int threads) {
+  return groups < ((int64_t)1 << 32) / threads;
+}
 
 // Compute units of the current device (256 without one).
 int int8_cus();

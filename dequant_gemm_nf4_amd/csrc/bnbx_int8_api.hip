@@ -24,6 +24,15 @@ int check_rows8(const bnbx_int8_rows* q, bool empty) {
   return BNBX_OK;
 }
 
+// The products count rows to the end of a last tile in 31 bits.
+bool too_many(int rows) { return rows > INT32_MAX - 511; }
+
+// Whether bnbx_gemm_int8 and bnbx_linear_int8 have a launch for a product.
+bool int8_gemm_takes(int M, int N, int K) {
+  if (too_many(M) || too_many(N)) return false;
+  return int8_few_takes(M, K) ? int8_few_fits(N) : int8_gemm_fits(M, N, K);
+}
+
 // Rows of `bytes`-wide values: `cols` of them at p + r * ld.
 int check_matrix8(const void* p, int64_t ld, int64_t rows, int64_t cols, size_t bytes) {
   if (rows > 0 && p == nullptr) return BNBX_E_INVAL;
@@ -52,7 +61,7 @@ Int8Rows rows8(const bnbx_int8_rows* q) {
 int64_t padded(int64_t cols) { return (cols + 15) / 16 * 16; }
 
 // X's codes and scales at the start of a workspace.
-size_t codes_bytes(int M, int K) {
+size_t codes_bytes(int64_t M, int K) {
   return whole256((size_t)M * padded(K)) + whole256((size_t)M * sizeof(float));
 }
 
@@ -96,7 +105,7 @@ int bnbx_dequantize_rows_int8(const bnbx_int8_rows* q, uint16_t* out, int64_t ld
 
 size_t bnbx_gemm_int8_workspace_bytes(int M, int N, int K) {
   if (M < 1 || N < 1 || K < 1 || K > BNBX_INT8_MAX_COLS || int8_few_takes(M, K)) return 0;
-  return int8_gemm_workspace(M, N, K);
+  return int8_gemm_takes(M, N, K) ? int8_gemm_workspace(M, N, K) : 0;
 }
 
 int bnbx_gemm_int8(const bnbx_int8_rows* x, const bnbx_int8_rows* w, uint16_t* y, int64_t ldy,
@@ -108,7 +117,8 @@ int bnbx_gemm_int8(const bnbx_int8_rows* x, const bnbx_int8_rows* w, uint16_t* y
   if (x->cols != w->cols || x->dtype != w->dtype) return BNBX_E_INVAL;
   s = check_matrix8(y, ldy, x->rows, w->rows, 2);
   if (s != BNBX_OK) return s;
-  if (x->cols > BNBX_INT8_MAX_COLS) return BNBX_E_UNSUPPORTED;
+  if (x->cols > BNBX_INT8_MAX_COLS || !int8_gemm_takes(x->rows, w->rows, x->cols))
+    return BNBX_E_UNSUPPORTED;
   if (x->rows == 0) return BNBX_OK;
   const bool f16 = x->dtype == BNBX_DTYPE_F16;
   if (int8_few_takes(x->rows, x->cols))
@@ -141,7 +151,7 @@ int bnbx_linear_int8(const uint16_t* x, int64_t ldx, int M, const bnbx_int8_rows
     if (s != BNBX_OK) return s;
     if (saved->rows != M || saved->cols != K || saved->dtype != w->dtype) return BNBX_E_INVAL;
   }
-  if (K > BNBX_INT8_MAX_COLS) return BNBX_E_UNSUPPORTED;
+  if (K > BNBX_INT8_MAX_COLS || !int8_gemm_takes(M, N, K)) return BNBX_E_UNSUPPORTED;
   if (M == 0) return BNBX_OK;
   s = check_workspace8(workspace, workspace_bytes,
                        bnbx_linear_int8_workspace_bytes(M, N, K, saved != nullptr));
@@ -179,6 +189,7 @@ int bnbx_gemm_int8_dx(const uint16_t* dy, int64_t lddy, int M, const bnbx_int8_r
   if (s != BNBX_OK) return s;
   s = check_dy8(dy, lddy, M, w->rows);
   if (s != BNBX_OK) return s;
+  if (too_many(M) || too_many(w->rows)) return BNBX_E_UNSUPPORTED;
   if (M == 0) return BNBX_OK;
   s = check_workspace8(workspace, workspace_bytes, int8_grad_workspace(M, w->cols, w->rows));
   if (s != BNBX_OK) return s;
@@ -203,6 +214,7 @@ int bnbx_gemm_int8_dw(const uint16_t* dy, int64_t lddy, int N, const bnbx_int8_r
   if (s != BNBX_OK) return s;
   s = check_dy8(dy, lddy, x->rows, N);
   if (s != BNBX_OK) return s;
+  if (too_many(N) || too_many(x->rows)) return BNBX_E_UNSUPPORTED;
   s = check_workspace8(workspace, workspace_bytes, int8_grad_workspace(N, x->cols, x->rows));
   if (s != BNBX_OK) return s;
   const bool f16 = x->dtype == BNBX_DTYPE_F16;

@@ -158,7 +158,6 @@ template <int M, bool FUSED>
 hipError_t launch(const FewArgs& a, bool f16, hipStream_t s) {
   const int kp = (a.K + 15) / 16 * 16;
   const int64_t per = (int64_t)kWaves * a.rows, grid = (a.N + per - 1) / per;
-  if (grid >= ((int64_t)1 << 32) / kThreads) return hipErrorNotSupported;
   if (f16)
     int8_few_kernel<M, FUSED, true><<<(int)grid, kThreads, M * kp, s>>>(a);
   else
@@ -181,6 +180,8 @@ hipError_t launch(const FewArgs& a, bool f16, hipStream_t s) {
 bool int8_few_takes(int M, int K) {
   return M <= 4 && (int64_t)M * ((K + 15) / 16 * 16) <= kLdsCodes;
 }
+
+bool int8_few_fits(int N) { return launch_fits((int64_t)N / kWaves + 1, kThreads); }
 
 hipError_t launch_int8_few(const uint16_t* x, int64_t ldx, const Int8Rows& q, const Int8Rows& w,
                            uint16_t* y, int64_t ldy, bool f16, hipStream_t s) {

@@ -356,6 +356,12 @@ Form form_of(int M, int N, int K) {
   return best;
 }
 
+void tiles_of(const Form& f, int M, int N, int64_t& tm, int64_t& tn) {
+  const Shape& tile = kShapes[f.shape];
+  tm = ((int64_t)M + tile.tm - 1) / tile.tm;
+  tn = ((int64_t)N + tile.tn - 1) / tile.tn;
+}
+
 template <bool F16, bool SPLIT>
 hipError_t launch(const GemmArgs& a, int shape, hipStream_t s) {
   const int total = a.tiles_m * a.tiles_n;
@@ -371,6 +377,14 @@ hipError_t launch(const GemmArgs& a, int shape, hipStream_t s) {
 }
 
 }  // namespace
+
+bool int8_gemm_fits(int M, int N, int K) {
+  if (int8_rows16_takes(M)) return int8_rows16_fits(N);
+  const Form f = form_of(M, N, K);
+  int64_t tm, tn;
+  tiles_of(f, M, N, tm, tn);
+  return launch_fits((tm * tn + kXcds) * f.splits, 512);
+}
 
 size_t int8_gemm_workspace(int M, int N, int K) {
   if (int8_rows16_takes(M)) return 0;
@@ -394,10 +408,8 @@ hipError_t launch_int8_gemm(const Int8Rows& x, const Int8Rows& w, uint16_t* y, i
   a.K = x.cols;
   a.y = y;
   a.ldy = ldy;
-  const Shape& tile = kShapes[f.shape];
-  const int64_t tm = ((int64_t)a.M + tile.tm - 1) / tile.tm, tn = ((int64_t)a.N + tile.tn - 1) / tile.tn;
-  // a launch counts its threads in 32 bits
-  if (tm * tn * f.splits >= ((int64_t)1 << 32) / kThreads - kXcds) return hipErrorNotSupported;
+  int64_t tm, tn;
+  tiles_of(f, a.M, a.N, tm, tn);
   a.tiles_m = (int)tm;
   a.tiles_n = (int)tn;
   a.splits = f.splits;

@@ -518,8 +518,7 @@ hipError_t launch_int8_grad(const GradGemm& g, bool turned, bool f16, void* work
   const int wide_r = 32 * kShapes[f.shape].fr, wide_c = 128 * kShapes[f.shape].fc;
   const int64_t tr = ((int64_t)a.R + wide_r - 1) / wide_r,
                 tc = ((int64_t)a.C + wide_c - 1) / wide_c;
-  // a launch counts its threads in 32 bits
-  if (tr * tc * f.splits >= ((int64_t)1 << 32) / kThreads - kXcds) return hipErrorNotSupported;
+  if (!launch_fits((tr * tc + kXcds) * f.splits, 512)) return hipErrorNotSupported;
   a.tiles_r = (int)tr;
   a.tiles_c = (int)tc;
   a.splits = f.splits;

@@ -139,7 +139,6 @@ __global__ __launch_bounds__(WV * 64) void int8_rows16_kernel(Rows16Args a) {
 template <int FM, int WV>
 hipError_t launch(const Rows16Args& a, bool f16, hipStream_t s) {
   const int64_t grid = ((int64_t)a.N + 15) / 16;
-  if (grid >= ((int64_t)1 << 32) / (WV * 64)) return hipErrorNotSupported;
   if (f16)
     int8_rows16_kernel<FM, WV, true><<<(int)grid, WV * 64, 0, s>>>(a);
   else
@@ -153,6 +152,8 @@ hipError_t launch(const Rows16Args& a, bool f16, hipStream_t s) {
 // x 4096 x 11008 17.9 / 21.8 (but 64 x 4096 x 4096 10.3 / 9.1); 32 x 11008 x 4096 16.2 /
 // 15.4, 16 x 11008 x 4096 15.1 / 12.7.
 bool int8_rows16_takes(int M) { return M <= 32; }
+
+bool int8_rows16_fits(int N) { return launch_fits((int64_t)N / 16 + 1, 512); }
 
 hipError_t launch_int8_rows16(const Int8Rows& x, const Int8Rows& w, uint16_t* y, int64_t ldy,
                               bool f16, hipStream_t s) {

@@ -90,8 +90,10 @@ BNBX_INT8_API size_t bnbx_gemm_int8_workspace_bytes(int M, int N, int K);
  *   y          device, row m at y + m * ldy; ldy >= N (written); 2-byte aligned
  *   workspace  device, >= bnbx_gemm_int8_workspace_bytes(...) bytes, 16-byte
  *              aligned (may be NULL when that is 0); scratch
- * M = 0 is a call that does nothing; w->rows must be positive.
- * Errors: BNBX_E_INVAL, BNBX_E_ALIGN, BNBX_E_UNSUPPORTED, BNBX_E_WORKSPACE. */
+ * M = 0 is a call that does nothing; w->rows must be positive.  y must not overlap
+ * the operands.  Errors: BNBX_E_INVAL, BNBX_E_ALIGN, BNBX_E_UNSUPPORTED (K above
+ * the limit, 2^31 - 511 rows or more of an operand, more output tiles than one launch
+ * takes), BNBX_E_WORKSPACE. */
 BNBX_INT8_API int bnbx_gemm_int8(const bnbx_int8_rows* x, const bnbx_int8_rows* w, uint16_t* y,
                                  int64_t ldy, void* workspace, size_t workspace_bytes,
                                  void* stream);

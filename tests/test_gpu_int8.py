@@ -234,6 +234,61 @@ def test_linear_strides_and_what_lies_around(M, N, K):
         assert (out[M] == 3).all() and (out[:, N:] == 3).all()
 
 
+@pytest.mark.parametrize("M", [1, 4, 20, 70, 300])
+@pytest.mark.parametrize("shift", [1, 2, 4, 8])
+def test_outputs_at_any_address(M, shift):
+    """Outputs that start `shift` values into a buffer (2-byte aligned only)."""
+    N, K = 200, 264
+    x, w, dy = activations(M, K, 1), held(rand((N, K), 2, 0.02)), rand((M, N), 3, 0.05)
+    y = T.linear_int8(x, w)
+    buf = torch.zeros(M * 512 + 64, dtype=torch.bfloat16, device="cuda")
+    out = buf[shift:shift + M * 512].view(M, 512)[:, :N]
+    assert torch.equal(T.linear_int8(x, w, out=out), y)
+    out = buf[shift:shift + M * 512].view(M, 512)[:, :K]
+    assert torch.equal(T.gemm_int8_dx(dy, w, out=out), T.gemm_int8_dx(dy, w))
+    saved = T.quantize_rows(x)
+    for dt in (torch.bfloat16, torch.float32):
+        buf = torch.zeros(N * 512 + 64, dtype=dt, device="cuda")
+        out = buf[shift:shift + N * 512].view(N, 512)[:, :K]
+        assert torch.equal(T.gemm_int8_dw(dy, saved, out=out),
+                           T.gemm_int8_dw(dy, saved, dtype=dt))
+
+
+@pytest.mark.parametrize("M", [2, 20, 70])
+def test_codes_past_32_bit_offsets(M):
+    """A weight, and saved activations, of more than 2^32 bytes: the last rows."""
+    R, K, last = 525_000, 8192, 120
+    codes = torch.randint(-127, 128, (R, K), dtype=torch.int8, device="cuda")
+    scale = torch.rand(R, device="cuda") + 0.5
+    q = T.Int8Rows((R, K), codes, scale)
+    x = activations(M, K, 1)
+    y = T.linear_int8(x, q)
+    qx, sx = codes_in_64(x)
+    tail = codes[-last:].double()
+    exact = (qx.double() @ tail.t().contiguous()) * sx.double()[:, None] * scale[-last:].double()
+    assert ((y[:, -last:].double() - exact).abs() <= exact.abs() * 2.0 ** -8 * 1.001).all()
+    dy = torch.zeros(M, R, dtype=torch.bfloat16, device="cuda")
+    dy[:, -last:] = rand((M, last), 2, 0.05)
+    v = values_of(codes[-last:].long(), scale[-last:], torch.bfloat16)
+    gradient_check(T.gemm_int8_dx(dy, q), dy[:, -last:], v, "dx")
+    dy = torch.zeros(R, 8, dtype=torch.bfloat16, device="cuda")
+    dy[-last:] = rand((last, 8), 3, 0.05)
+    gradient_check(T.gemm_int8_dw(dy, q), dy[-last:].t(), v, "dw")
+    assert torch.equal(T.dequantize_rows(q)[-last:].double(), v)
+
+
+def test_outputs_past_32_bit_offsets():
+    M, N, K = 300_001, 8200, 48
+    x, w = rand((M, K), 1), rand((N, K), 2, 0.02)
+    wq, last = held(w), 90
+    y = T.linear_int8(x, wq)
+    product_check(y[-last:], x[-last:], w)
+    dy = rand((M, 16), 3, 0.05)
+    v = rand((16, N), 4, 0.02)
+    gradient_check(T.gemm_int8_dx(dy, held(v), out=y)[-last:], dy[-last:],
+                   values_of(*codes_in_64(v), torch.bfloat16))
+
+
 def test_linear_no_rows():
     w = held(rand((20, 32), 1))
     assert T.linear_int8(torch.empty(0, 32, dtype=torch.bfloat16, device="cuda"), w).shape == (0, 20)

@@ -135,6 +135,20 @@ def test_dw_rejects(kw, expect):
                      f["out"], f["ws"], f["nbytes"], 0) == expect
 
 
+def test_sizes_past_a_launch_are_refused_before_anything_is_enqueued():
+    most = 2**31 - 512
+    big = dict(ws=E, nbytes=1 << 62)
+    for M, N in ((most + 1, 16), (16, most + 1), (20, most), (100, most)):
+        x, w = rows(rows=M, cols=32, ld=32), rows(rows=N, cols=32, ld=32)
+        assert status_of(bnbx.bnbx_gemm_int8, x, w, C, N, big["ws"], big["nbytes"], 0) == UNSUP
+        assert status_of(bnbx.bnbx_linear_int8, C, 32, M, w, None, D, N, big["ws"], big["nbytes"],
+                         0) == UNSUP
+    w = rows(rows=16, cols=32, ld=32)
+    assert status_of(bnbx.bnbx_gemm_int8_dx, C, 16, most + 1, w, D, 32, E, 1 << 62, 0) == UNSUP
+    assert status_of(bnbx.bnbx_gemm_int8_dw, C, 16, 16, rows(rows=most + 1, cols=32, ld=32), D, 32,
+                     0, E, 1 << 62, 0) == UNSUP
+
+
 def test_calls_without_rows_do_nothing():
     none = rows(codes=None, scale=None, rows=0)
     bnbx.bnbx_quantize_rows_int8(None, 1000, none, 0)
