@@ -248,9 +248,10 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_gemm_kernel(GemmArgs a) {
   static_assert(PER * 32 * CH * 16 <= kBuf && WV * 256 <= kBuf && TN <= 64 * WV,
                 "results and scales fit a buffer");
   uint8_t* const mine = (wave < PER ? buf0 : buf2) + wave % PER * 32 * CH * 16;
-  // the tile's scales of W (64 a wave, TN of them wanted)
-  copy4_lds(rsrc8(a.sw, (int64_t)a.N * 4), buf1 + wave * 256,
-            4u * (uint32_t)(n0 + 64 * wave + lane), 0);
+  // the tile's scales of W (64 a wave, TN of them wanted), from the tile's first on: N
+  // of them may be more than a resource's 2^31 bytes
+  copy4_lds(rsrc8(a.sw + n0, (int64_t)(a.N - n0) * 4), buf1 + wave * 256,
+            4u * (uint32_t)(64 * wave + lane), 0);
   land(All{});
   const bool vec = ((uintptr_t)a.y % 16 == 0) && a.ldy % 8 == 0;
 #pragma unroll
