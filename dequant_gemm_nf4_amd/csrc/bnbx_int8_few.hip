@@ -66,12 +66,13 @@ __global__ __launch_bounds__(kThreads) void int8_few_kernel(FewArgs a) {
 
   u32x4_t wv[2][U];
   auto load = [&](int set, int n, int b) {
-    // rows past the end, and pieces past the row's: zeros
+    // rows past the end, and pieces past the row's: zeros (a piece's whole place is in
+    // the lane's offset, since the range check leaves out the scalar one)
     const rsrc8_t r = rsrc8(a.w + (int64_t)n * a.ldw, n < a.N ? kp : 0);
+    const uint32_t at = 16u * lane + (uint32_t)b * (1024u * U);
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      wv[set][i] = __builtin_amdgcn_raw_buffer_load_b128(
-          r, 16u * lane, (uint32_t)(b * U + i) * 1024u, 2 /* streamed */);
+      wv[set][i] = __builtin_amdgcn_raw_buffer_load_b128(r, at + 1024u * i, 0, 2 /* streamed */);
   };
   load(0, n0, 0);
 
