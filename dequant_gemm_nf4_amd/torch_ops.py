@@ -510,6 +510,10 @@ class Linear4bitAdapters(Linear4bit):
 def _rows8(name: str, codes: torch.Tensor, scale: torch.Tensor, cols: int, dtype) -> T.Int8Rows:
     if dtype not in _DTYPES:
         raise TypeError(f"{name}: bfloat16 or float16, not {dtype}")
+    # codes of more columns would multiply too: a wrong width must not pass as a shorter K
+    if codes.dim() != 2 or codes.shape[1] != _pitch16(cols):
+        raise ValueError(f"{name}: codes of {cols} columns are [rows, {_pitch16(cols)}], not "
+                         f"{tuple(codes.shape)}")
     return T.Int8Rows((codes.shape[0], cols), codes, scale, dtype)
 
 
@@ -697,6 +701,8 @@ class Linear8bit(torch.nn.Module):
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         if x.dtype != self.compute_dtype:
             raise TypeError(f"input dtype {x.dtype} != compute dtype {self.compute_dtype}")
+        if x.shape[-1] != self.in_features:
+            raise ValueError(f"input width {x.shape[-1]} != in_features {self.in_features}")
         return torch.ops.bnbx.linear8bit(x, self.codes, self.scale)
 
     def extra_repr(self) -> str:
