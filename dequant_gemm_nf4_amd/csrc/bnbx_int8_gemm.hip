@@ -27,12 +27,13 @@
 #include <type_traits>
 
 #include "bnbx_int8_device.hpp"
+#include "bnbx_int8_form.hpp"
 
 namespace bnbx {
 namespace {
 
 constexpr int kThreads = 256;   // of the reduction
-constexpr int BK = 128;
+constexpr int BK = kInt8GemmStep;
 
 // Scheduling-group masks (AMDGPU sched_group_barrier).
 constexpr int kSgMfma = 0x008, kSgValu = 0x002, kSgSalu = 0x004, kSgVmem = 0x010,
@@ -313,54 +314,12 @@ __global__ __launch_bounds__(kThreads) void int8_reduce_kernel(GemmArgs a) {
   }
 }
 
-// The forms: rows of X and of W a workgroup, and the time of a step of K with a workgroup on every CU
-// (us; 2048 x 8192 x 8192 and the sizes below, timed one form after the other).
-struct Shape {
-  int tm, tn;
-  double step;
-};
-constexpr Shape kShapes[] = {
-    {256, 256, 1.72}, {256, 128, 1.05}, {128, 128, 0.60}, {128, 64, 0.36}, {64, 64, 0.23}};
-struct Form {
-  int shape;
-  int splits, steps_per;   // of K
-};
-// The form and the split of K that take the least by this count: rounds of
-// workgroups over the CUs (a last round that is not full is a little faster),
-// their steps, 4 us for a launch's first copies and its results, and for a split 3 us
-// for the second launch and the partial sums written and read at 6.5 TB/s.
-// Counted and measured (us), 301 x 4096 x 11008: 128 x 64 whole 33 / 31, 128 x 128 in
-// two splits 34 / 34, 64 x 64 whole 44 / 44; 1000 x 4096 x 11008: 128 x 128 whole 56 /
-// 58, 256 x 128 in two 61 / 64; 2048 x 4096 x 4096: 256 x 128 whole 38 / 38, 256 x 256
-// whole 51 / 48.
-Form form_of(int M, int N, int K) {
-  const int cus = int8_cus();
-  const int steps = (K + BK - 1) / BK;
-  Form best{0, 1, steps};
-  double least = 1e30;
-  for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
-    const Shape& f = kShapes[i];
-    const int64_t tiles = (((int64_t)M + f.tm - 1) / f.tm) * (((int64_t)N + f.tn - 1) / f.tn);
-    for (int splits = 1; splits <= 16 && (splits == 1 || steps / splits >= 4); ++splits) {
-      const int per = (steps + splits - 1) / splits, n = (steps + per - 1) / per;
-      if (n > 1 && tiles * n > 2 * (int64_t)cus) break;
-      const double fill = (double)(tiles * n) / cus;
-      const double rounds = fill <= 1.0 ? 0.7 + 0.3 * fill : (double)((tiles * n + cus - 1) / cus);
-      const double us = rounds * per * f.step + 4.0 +
-                        (n > 1 ? 3.0 + 8.0 * n * (double)M * (double)N / 6.5e6 : 0.0);
-      if (us < least) {
-        least = us;
-        best = {i, n, per};
-      }
-    }
-  }
-  return best;
-}
+Int8Form form_of(int M, int N, int K) { return int8_gemm_form(M, N, K, int8_cus()); }
 
-void tiles_of(const Form& f, int M, int N, int64_t& tm, int64_t& tn) {
-  const Shape& tile = kShapes[f.shape];
-  tm = ((int64_t)M + tile.tm - 1) / tile.tm;
-  tn = ((int64_t)N + tile.tn - 1) / tile.tn;
+void tiles_of(const Int8Form& f, int M, int N, int64_t& tm, int64_t& tn) {
+  const Int8Shape& tile = kInt8GemmShapes[f.shape];
+  tm = ((int64_t)M + tile.rows - 1) / tile.rows;
+  tn = ((int64_t)N + tile.cols - 1) / tile.cols;
 }
 
 template <bool F16, bool SPLIT>
@@ -381,7 +340,7 @@ hipError_t launch(const GemmArgs& a, int shape, hipStream_t s) {
 
 bool int8_gemm_fits(int M, int N, int K) {
   if (int8_rows16_takes(M)) return int8_rows16_fits(N);
-  const Form f = form_of(M, N, K);
+  const Int8Form f = form_of(M, N, K);
   int64_t tm, tn;
   tiles_of(f, M, N, tm, tn);
   return launch_fits((tm * tn + kXcds) * f.splits, 512);
@@ -389,14 +348,14 @@ bool int8_gemm_fits(int M, int N, int K) {
 
 size_t int8_gemm_workspace(int M, int N, int K) {
   if (int8_rows16_takes(M)) return 0;
-  const Form f = form_of(M, N, K);
+  const Int8Form f = form_of(M, N, K);
   return f.splits > 1 ? (size_t)f.splits * M * ((N + 3) / 4 * 4) * sizeof(int) : 0;
 }
 
 hipError_t launch_int8_gemm(const Int8Rows& x, const Int8Rows& w, uint16_t* y, int64_t ldy,
                             bool f16, void* workspace, hipStream_t s) {
   if (int8_rows16_takes(x.rows)) return launch_int8_rows16(x, w, y, ldy, f16, s);
-  const Form f = form_of(x.rows, w.rows, x.cols);
+  const Int8Form f = form_of(x.rows, w.rows, x.cols);
   GemmArgs a{};
   a.x = x.codes;
   a.w = w.codes;

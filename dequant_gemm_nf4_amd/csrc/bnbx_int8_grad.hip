@@ -27,12 +27,13 @@
 #include <type_traits>
 
 #include "bnbx_int8_device.hpp"
+#include "bnbx_int8_form.hpp"
 
 namespace bnbx {
 namespace {
 
 constexpr int kThreads = 256;   // of the reduction
-constexpr int BT = 64;
+constexpr int BT = kInt8GradStep;
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 typedef __attribute__((ext_vector_type(2))) int i32x2_t;
 
@@ -421,47 +422,7 @@ __global__ __launch_bounds__(kThreads) void int8_grad_reduce_kernel(GradArgs a) 
   }
 }
 
-// The forms: FR, FC, and the time of a step of t with a workgroup on every CU (us;
-// 4096 x 11008 x 4096 and the sizes below, timed one form after the other).
-struct Shape {
-  int fr, fc;
-  double step;
-};
-constexpr Shape kShapes[] = {
-    {8, 2, 1.72}, {4, 2, 0.92}, {4, 1, 0.57}, {2, 1, 0.36}, {1, 1, 0.31}};
-struct Form {
-  int shape;
-  int splits, steps_per;   // of t
-};
-// As the forward product's: rounds of workgroups, steps, 4 us a launch, and for a
-// split of t 3 us and the partial sums at 6.5 TB/s.  Counted and measured (us), R x
-// T x C = 200 x 4096 x 4096: 4 x 1 in four 20 / 21, 2 x 1 in two 21 / 23, 4 x 2 in eight
-// 22 / 25; 1000 x 4096 x 4096: 4 x 1 whole 40 / 42, 4 x 2 in two 43 / 46; 1001 x 777 x
-// 4100: 4 x 2 whole 14 / 21, 2 x 1 whole 18 / 23.
-Form form_of(int R, int C, int T) {
-  const int cus = int8_cus();
-  const int steps = (T + BT - 1) / BT;
-  Form best{0, 1, steps};
-  double least = 1e30;
-  for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
-    const Shape& f = kShapes[i];
-    const int64_t tiles = (((int64_t)R + 32 * f.fr - 1) / (32 * f.fr)) *
-                          (((int64_t)C + 128 * f.fc - 1) / (128 * f.fc));
-    for (int splits = 1; splits <= 32 && (splits == 1 || steps / splits >= 4); ++splits) {
-      const int per = (steps + splits - 1) / splits, n = per > 0 ? (steps + per - 1) / per : 1;
-      if (n > 1 && tiles * n > 2 * (int64_t)cus) break;
-      const double fill = (double)(tiles * n) / cus;
-      const double rounds = fill <= 1.0 ? 0.7 + 0.3 * fill : (double)((tiles * n + cus - 1) / cus);
-      const double us = rounds * per * f.step + 4.0 +
-                        (n > 1 ? 3.0 + 8.0 * n * (double)R * (double)C / 6.5e6 : 0.0);
-      if (us < least) {
-        least = us;
-        best = {i, n, per};
-      }
-    }
-  }
-  return best;
-}
+Int8Form form_of(int R, int C, int T) { return int8_grad_form(R, C, T, int8_cus()); }
 
 template <bool TURNED, bool F16, int OUT, bool SPLIT>
 hipError_t launch(const GradArgs& a, int shape, hipStream_t s) {
@@ -477,7 +438,7 @@ hipError_t launch(const GradArgs& a, int shape, hipStream_t s) {
 }
 
 template <bool TURNED, bool F16, int OUT>
-hipError_t launch(const GradArgs& a, const Form& f, hipStream_t s) {
+hipError_t launch(const GradArgs& a, const Int8Form& f, hipStream_t s) {
   if (f.splits == 1) return launch<TURNED, F16, OUT, false>(a, f.shape, s);
   const hipError_t e = launch<TURNED, F16, kOutF32, true>(a, f.shape, s);
   if (e != hipSuccess) return e;
@@ -488,7 +449,7 @@ hipError_t launch(const GradArgs& a, const Form& f, hipStream_t s) {
 }
 
 template <bool TURNED>
-hipError_t launch(const GradArgs& a, const Form& f, bool f16, int out, hipStream_t s) {
+hipError_t launch(const GradArgs& a, const Int8Form& f, bool f16, int out, hipStream_t s) {
   if (out == kOutF32)
     return f16 ? launch<TURNED, true, kOutF32>(a, f, s) : launch<TURNED, false, kOutF32>(a, f, s);
   return f16 ? launch<TURNED, true, kOutF16>(a, f, s) : launch<TURNED, false, kOutBf16>(a, f, s);
@@ -497,13 +458,13 @@ hipError_t launch(const GradArgs& a, const Form& f, bool f16, int out, hipStream
 }  // namespace
 
 size_t int8_grad_workspace(int R, int C, int T) {
-  const Form f = form_of(R, C, T);
+  const Int8Form f = form_of(R, C, T);
   return f.splits > 1 ? (size_t)f.splits * R * ((C + 3) / 4 * 4) * sizeof(float) : 0;
 }
 
 hipError_t launch_int8_grad(const GradGemm& g, bool turned, bool f16, void* workspace,
                             hipStream_t s) {
-  const Form f = form_of(g.R, g.v.cols, g.v.rows);
+  const Int8Form f = form_of(g.R, g.v.cols, g.v.rows);
   GradArgs a{};
   a.dy = g.dy;
   a.ldy = g.ldy;
@@ -515,7 +476,7 @@ hipError_t launch_int8_grad(const GradGemm& g, bool turned, bool f16, void* work
   a.T = g.v.rows;
   a.out = g.out;
   a.ldo = g.ldo;
-  const int wide_r = 32 * kShapes[f.shape].fr, wide_c = 128 * kShapes[f.shape].fc;
+  const int wide_r = kInt8GradShapes[f.shape].rows, wide_c = kInt8GradShapes[f.shape].cols;
   const int64_t tr = ((int64_t)a.R + wide_r - 1) / wide_r,
                 tc = ((int64_t)a.C + wide_c - 1) / wide_c;
   if (!launch_fits((tr * tc + kXcds) * f.splits, 512)) return hipErrorNotSupported;

@@ -13,6 +13,7 @@
 // us where two take 13.5, 16 x 11008 x 4096: fewer workgroups on a CU).  Rows
 // past the end and chunks past K read as zeros through the buffer range check.
 #include "bnbx_int8_device.hpp"
+#include "bnbx_int8_form.hpp"
 
 namespace bnbx {
 namespace {
@@ -148,10 +149,7 @@ hipError_t launch(const Rows16Args& a, bool f16, hipStream_t s) {
 
 }  // namespace
 
-// From 33 rows on the tiles are faster: 64 x 11008 x 4096 15.6 us against 22.3 here, 64
-// x 4096 x 11008 17.9 / 21.8 (but 64 x 4096 x 4096 10.3 / 9.1); 32 x 11008 x 4096 16.2 /
-// 15.4, 16 x 11008 x 4096 15.1 / 12.7.
-bool int8_rows16_takes(int M) { return M <= 32; }
+bool int8_rows16_takes(int M) { return M <= kInt8WaveRows; }
 
 bool int8_rows16_fits(int N) { return launch_fits((int64_t)N / 16 + 1, 512); }
 
