@@ -8,11 +8,12 @@
 // loads of W are under way: X is M K values, little beside a workgroup's part of W,
 // and a launch of its own would cost more than the product.
 #include "bnbx_int8_device.hpp"
+#include "bnbx_int8_form.hpp"
 
 namespace bnbx {
 namespace {
 
-constexpr int kThreads = 1024, kWaves = 16;
+constexpr int kWaves = kInt8FewWaves, kThreads = 64 * kWaves;
 constexpr int kLdsCodes = 65536;   // most bytes of X's codes
 constexpr int U = 4;               // loads of W a lane has under way, twice
 
@@ -198,13 +199,7 @@ hipError_t launch_int8_few(const uint16_t* x, int64_t ldx, const Int8Rows& q, co
   a.M = q.rows;
   a.N = w.rows;
   a.K = w.cols;
-  // One row: a wave a row of W.  More rows of X cost a workgroup more before its first
-  // product: then as many rows a wave as keep the launch to one workgroup a CU.  1, 2, 4
-  // rows beside 11008 x 4096: 11.1, 15.3, 19.4 us a row a wave, 11.5, 12.1, 13.4 three a
-  // wave; beside 32000 x 4096 25.6, 36.8, 46.9 and 30.8, 31.9, 33.0 eight a wave.
-  const int64_t groups = ((int64_t)w.rows + kWaves - 1) / kWaves, cus = int8_cus();
-  const int64_t each = (groups + cus - 1) / cus;
-  a.rows = q.rows == 1 ? 1 : (int)(each < 8 ? each : 8);
+  a.rows = int8_few_rows(a.M, a.N, int8_cus());
   a.y = y;
   a.ldy = ldy;
   return x != nullptr ? launch<true>(a, f16, s) : launch<false>(a, f16, s);

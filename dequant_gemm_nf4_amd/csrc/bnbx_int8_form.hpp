@@ -79,4 +79,17 @@ inline Int8Form int8_grad_form(int R, int C, int T, int cus) {
 // 16 x 11008 x 4096 15.1 / 12.7.
 constexpr int kInt8WaveRows = 32;
 
+// Rows of W a wave of the form for up to four rows of X takes, 16 waves a workgroup.
+// One row of X: one.  More rows of X cost a workgroup more before its first product: then
+// as many as keep the launch to one workgroup a CU, up to eight.  1, 2, 4 rows beside
+// 11008 x 4096: 11.1, 15.3, 19.4 us a row a wave, 11.5, 12.1, 13.4 three a wave; beside
+// 32000 x 4096 25.6, 36.8, 46.9 and 30.8, 31.9, 33.0 eight a wave.
+constexpr int kInt8FewWaves = 16;
+inline int int8_few_rows(int M, int N, int cus) {
+  if (M == 1) return 1;
+  const long long groups = ((long long)N + kInt8FewWaves - 1) / kInt8FewWaves;
+  const long long each = (groups + cus - 1) / cus;
+  return (int)(each < 8 ? each : 8);
+}
+
 }  // namespace bnbx

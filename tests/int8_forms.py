@@ -24,6 +24,8 @@ GRADS = {
     (128, 128, False): (2000, 2000, 131), (128, 128, True): (200, 4096, 4099),
     (64, 128, False): (1880, 389, 521), (64, 128, True): (700, 700, 5001),
     (32, 128, False): (33, 389, 131), (32, 128, True): (40, 130, 9001)}
+# rows of W: how many of them a wave takes with two to four rows of X
+FEW = {4096: 1, 4097: 2, 11009: 3, 33000: 8}
 
 
 def load(folder: str) -> ctypes.CDLL:
@@ -39,6 +41,8 @@ def load(folder: str) -> ctypes.CDLL:
                 '  tell(kInt8GemmShapes, int8_gemm_form(M, N, K, cus), out);\n}\n'
                 'extern "C" void grad(int R, int C, int T, int cus, int* out) {\n'
                 '  tell(kInt8GradShapes, int8_grad_form(R, C, T, cus), out);\n}\n'
+                'extern "C" int few_rows(int M, int N, int cus) {\n'
+                '  return int8_few_rows(M, N, cus);\n}\n'
                 'extern "C" int wave_rows() { return kInt8WaveRows; }\n'
                 'extern "C" int shapes(int grad) {\n'
                 '  return grad ? sizeof(kInt8GradShapes) / sizeof(Int8Shape)\n'

@@ -4,7 +4,8 @@ import pytest
 import torch
 
 from dequant_gemm_nf4_amd import tensors as T
-from int8_helpers import DT, codes_in_64, held, rand
+from int8_helpers import codes_in_64, held, rand
+from tests import int8_forms as F
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +37,17 @@ def test_a_weight_that_ends_with_its_pages(M, N, K):
     wq = held(rand((N, K), 1, 0.02))
     assert wq.codes.untyped_storage().nbytes() % 2**21 == 0
     few_check(rand((M, K), 2), wq, wq.codes[:, :K], wq.scale, (M, N, K))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("K", [40, 4096, 4100, 9000])
+@pytest.mark.parametrize("N", sorted(F.FEW))
+@pytest.mark.parametrize("M", [2, 3, 4])
+def test_several_rows_of_w_a_wave(M, N, K, dtype):
+    """(tests/test_int8_forms.py holds N to its rows a wave.)  One, two and three batches of
+    loads a row, so that the two sets of registers change places within rows and between
+    them; a last wave whose rows end past N."""
+    wq = held(rand((N, K), N + K, 0.02, dtype), spare=16)
+    x = rand((M, K), M + K, 1.0, dtype)
+    x[:, ::97] *= 8
+    few_check(x, wq, wq.codes[:, :K], wq.scale, (M, N, K))

@@ -35,3 +35,11 @@ def test_a_split_covers_the_summed_axis(rule, sizes, cus):
 
 def test_nothing_summed(rule):
     assert F.form(rule.grad, 300, 4096, 0)[2:] == (1, 0)
+
+
+def test_rows_of_w_a_wave(rule):
+    for n, rows in F.FEW.items():
+        assert rule.few_rows(1, n, F.CUS) == 1
+        assert [rule.few_rows(m, n, F.CUS) for m in (2, 3, 4)] == [rows] * 3
+    assert rule.few_rows(4, 1, F.CUS) == 1 and rule.few_rows(2, 2**31 - 512, F.CUS) == 8
+    assert rule.few_rows(2, 33, 1) == 3
