@@ -61,7 +61,9 @@ inline bool launch_fits(int64_t groups, int threads) {
   return groups < ((int64_t)1 << 32) / threads;
 }
 
-// Compute units of the current device (256 without one).
+// Compute units of the device that was current when the process first asked (256 if it
+// could not be asked): one number for all, so that a workspace's size and the call that
+// takes it count alike whatever device is current.
 int int8_cus();
 
 // Workspaces are cut into pieces of whole 256 bytes.

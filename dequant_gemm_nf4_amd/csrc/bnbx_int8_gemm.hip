@@ -20,10 +20,11 @@
 // every memory operation of the loop is a copy into LDS, and these land in order.
 //
 // What bounds it: the large tiles the matrix units under the power limit (2048 x 8192
-// x 8192 115-125 us by the card's state, 2.2-2.4 POP/s; the library's int8 product 118;
+// x 8192 107-115 us by the card's state, 2.4-2.6 POP/s; the library's int8 product 118;
 // copies and reads alone 96 us, products and reads alone 80-100), the small ones the
-// copies (301 x 4096 x 11008 31 us, copies alone 31, the rest alone 17): bytes come
-// from behind L2 at 45-80 B/ns a CU, from L2 at 130.
+// copies (301 x 4096 x 11008 27-29 us; where the whole took 31, the copies alone took 31
+// too and the rest alone 17): bytes come from behind L2 at 28-47 B/ns a CU (64 to 128 KB a CU under
+// way), from L2 at 130, in this product's mixture of both at 73.
 #include <type_traits>
 
 #include "bnbx_int8_device.hpp"

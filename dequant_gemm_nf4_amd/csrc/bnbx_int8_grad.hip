@@ -7,10 +7,10 @@
 // rows of one column in a lane: both operands that lie row by row are read from
 // LDS by the transposing reads (ds_read_b64_tr_b8 / _b16).
 //
-// Tiling.  A workgroup of four waves owns 32 FR rows r by 128 FC columns c; a
-// wave all its rows and 32 FC columns, so every code is read, converted and
-// scaled by one wave only, straight into operand registers, and A's operands are
-// shared by all four.  The codes are the A operand of v_mfma_f32_32x32x16: a lane
+// Tiling.  A workgroup owns 32 FR rows r by 128 FC columns c.  Four of its waves
+// multiply (in all but the largest tile four more copy for them), each all the rows
+// and 32 FC columns, so every code is read, converted and scaled by one wave only,
+// straight into operand registers, and A's operands are shared by all four.  The codes are the A operand of v_mfma_f32_32x32x16: a lane
 // then holds four consecutive columns of one row.  t is walked in steps of 64,
 // four substeps of 16.
 //
@@ -23,7 +23,8 @@
 //
 // What bounds it (4096 x 11008 x 4096, timed in copies with a part taken out): the
 // products with their reads 230 us, the copies 200, the conversion 30, which overlap
-// to 295 us or 1.25 PFLOP/s; a large bf16 library product of that shape runs at 0.92.
+// to 295-310 us by the card's state, 1.19-1.25 PFLOP/s; a large bf16 library product of
+// that shape runs at 0.92.
 #include <type_traits>
 
 #include "bnbx_int8_device.hpp"

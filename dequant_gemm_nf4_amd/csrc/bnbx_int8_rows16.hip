@@ -9,8 +9,9 @@
 // Both operands go from global memory straight into a wave's own LDS (buffer_load
 // ... lds, eight rows of 128 bytes an instruction, 16-byte chunks permuted by the
 // row pair so that 16 lanes reading one chunk of 16 rows meet all banks once); two
-// steps are under way at a time, and a wave waits for the older one only (three took 15.7
-// us where two take 13.5, 16 x 11008 x 4096: fewer workgroups on a CU).  Rows
+// steps are under way at a time, and a wave waits for the older one only (16 x 11008 x
+// 4096, timed with eight waves a workgroup: three steps 15.7 us, two 13.5, for fewer
+// workgroups fit a CU; the four waves that this size takes 10.2-12.5).  Rows
 // past the end and chunks past K read as zeros through the buffer range check.
 #include "bnbx_int8_device.hpp"
 #include "bnbx_int8_form.hpp"

@@ -611,7 +611,9 @@ def linear8bit_train(x: torch.Tensor, weight: torch.Tensor) -> tuple[
     """(Y, X's codes, X's scales, W's codes, W's scales) of Y[..., N] = X[..., K] .
     W^T over 8-bit integers, both quantized within the call.  The backward pass
     of Y needs the codes only: dX = dY . W_hat, dW = dY^T . X_hat, so X itself is
-    not kept (one byte a value instead of two)."""
+    not kept (one byte a value instead of two).  W's codes are kept beside X's, N K
+    bytes for each forward whose graph lives: less than a 16-bit layer keeps in all
+    where X has more rows than W."""
     if weight.dim() != 2 or weight.shape[1] != x.shape[-1] or weight.dtype != x.dtype:
         raise ValueError(f"linear8bit_train: weight must be [N, {x.shape[-1]}] {x.dtype}, not "
                          f"{tuple(weight.shape)} {weight.dtype}")
@@ -714,7 +716,9 @@ class Linear8bitTrain(torch.nn.Module):
     """A bias-free linear layer that trains a 16-bit weight through 8-bit products:
     every forward quantizes the weight for each output feature and the input for
     each row (``torch.ops.bnbx.linear8bit_train``), and what the backward pass keeps
-    of the input are its codes.  The gradients pass the rounding to codes
+    are the codes of both: of the input instead of its 16 bits, and of the weight that the
+    forward multiplied (one byte a value for each forward whose graph lives, so the layer
+    saves memory where the input has more rows than the weight).  The gradients pass the rounding to codes
     unchanged: dX = dY . W_hat, dW = dY^T . X_hat."""
 
     def __init__(self, in_features: int, out_features: int, dtype: torch.dtype = torch.bfloat16,

@@ -34,7 +34,8 @@
  * Conventions and status codes are those of bnbx.h: the caller owns every
  * buffer and the stream, nothing is allocated or synchronised, every argument
  * is checked on the host before anything is enqueued, calls keep no state
- * between them, and calls that share an output or a workspace must be ordered
+ * between them, what a call writes (its workspace too) overlaps nothing else that it is
+ * given, and calls that share an output or a workspace must be ordered
  * by the caller.  The same call on the same inputs repeats bit for bit.
  */
 #ifndef BNBX_INT8_H
